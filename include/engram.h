@@ -67,8 +67,17 @@ typedef enum {
   ENGRAM_ERR_N_MULT64 = 3, /* backward N not a multiple of 64 */
   ENGRAM_ERR_ALIGN = 4,    /* a floating tensor or the workspace is not 16-byte aligned */
   ENGRAM_ERR_OVERLAP = 5,  /* an output or the workspace overlaps an input or another output */
-  ENGRAM_ERR_LAUNCH = 6    /* the HIP runtime refused the launch (see engram_last_hip_error) */
+  ENGRAM_ERR_LAUNCH = 6,   /* the HIP runtime refused the launch (see engram_last_hip_error) */
+  ENGRAM_ERR_KIND = 7      /* an element type or activation that the call does not have */
 } engram_status;
+
+/* Element types of the layers' tensors (linear: the 16-bit ones; query/key
+ * norm: all three). */
+typedef enum { ENGRAM_BF16 = 0, ENGRAM_FP16 = 1, ENGRAM_FP32 = 2 } engram_dtype;
+
+/* Activations of the linear layer: z, max(z, 0), z sigmoid(z), z Phi(z) with
+ * the normal distribution Phi. */
+typedef enum { ENGRAM_ACT_NONE = 0, ENGRAM_ACT_RELU = 1, ENGRAM_ACT_SILU = 2, ENGRAM_ACT_GELU = 3 } engram_act;
 
 /* Size limits (layout paragraph). */
 #define ENGRAM_STREAMS 4
@@ -234,6 +243,204 @@ engram_status engram_gateconv_bwd(const void *dY, const void *H, const void *k, 
  * token chunk, fp32 sums of those partials in blocks of 64 chunks, then one
  * fp32 per row); 0 for sizes the call would reject. */
 size_t engram_gateconv_bwd_workspace_bytes(int64_t M, int64_t T, int64_t d);
+
+/* ==========================================================================
+ * The layers around the gate: the projections in front of it (linear), the
+ * norms of queries and keys with the position rotation (qk_norm_rope), and a
+ * causal token mixer with an unbounded past (decay_attn).
+ *
+ * Common contract: as for the gate (device pointers of the current device,
+ * asynchronous on `stream`, host-side validation before anything is enqueued,
+ * no allocation or synchronisation, capturable, outputs and workspace written
+ * in full and overlapping no input and no other output, results bitwise
+ * reproducible).  In addition:
+ *   - Rows may lie apart: a row argument has a leading dimension `ld*`, the
+ *     number of ELEMENTS from one token's row to the next, at least the row's
+ *     width, a multiple of 8 and at most ENGRAM_LD_MAX; the heads of a token
+ *     lie side by side.  So q and k may be columns of one packed projection,
+ *     and an output may be columns of a wider row (of kv, say).  Columns of
+ *     the same packed rows do not count as overlapping.
+ *   - Tensors and workspaces are 16-byte aligned; 64-bit integer arrays
+ *     8-byte aligned.
+ *   - Two calls that may run at the same time need two workspaces; so do two
+ *     graphs that may.
+ * Errors: ENGRAM_ERR_NULL, ENGRAM_ERR_KIND, ENGRAM_ERR_N_RANGE (a size, a
+ * leading dimension, eps or scale outside its limits), ENGRAM_ERR_ALIGN
+ * (a pointer, or a size or leading dimension that is no multiple of 8),
+ * ENGRAM_ERR_OVERLAP.
+ * ========================================================================== */
+#define ENGRAM_LD_MAX 1048576
+
+/*
+ * Linear layer: z = x W^T + bias, y = act(z) + residual.
+ *   x        [N][K]  in, leading dimension ldx
+ *   w        [M][K]  in, dense
+ *   bias     [M]     fp32, in, or NULL
+ *   residual [N][M]  in, leading dimension ldr, or NULL (ldr not looked at)
+ *   y        [N][M]  out, leading dimension ldy
+ *   z        [N][M]  out, leading dimension ldz, or NULL (not wanted): z
+ *                    rounded to the element type, for the backward of an
+ *                    activation
+ *   workspace  engram_linear_fwd_workspace_bytes(N, K, M) bytes, or NULL where
+ *              that is 0
+ *   N 1..ENGRAM_LINEAR_ROWS_MAX; K, M multiples of 8, 8..ENGRAM_LINEAR_WIDTH_MAX
+ *   dtype  ENGRAM_BF16 or ENGRAM_FP16, of x, w, residual, y and z
+ *   act    an engram_act
+ * Sums are fp32; y and z are each rounded once, y from the unrounded z.
+ */
+#define ENGRAM_LINEAR_ROWS_MAX 1048576
+#define ENGRAM_LINEAR_WIDTH_MAX 131072
+engram_status engram_linear_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,
+                                void *z, void *workspace, int64_t N, int64_t K, int64_t M, int64_t ldx, int64_t ldr,
+                                int64_t ldy, int64_t ldz, int dtype, int act, void *stream);
+
+/* Scratch bytes of engram_linear_fwd (fp32 parts of a contraction that is
+ * split because there are few rows and columns); 0 for sizes the call rejects. */
+size_t engram_linear_fwd_workspace_bytes(int64_t N, int64_t K, int64_t M);
+
+/*
+ * Backward of the linear layer for the gradient grad_y of y: with
+ * dz = grad_y act'(z), grad_x = dz W, grad_w = dz^T x, grad_bias = sum over
+ * rows of dz (the residual's gradient is grad_y itself).
+ *   grad_y [N][M] in, leading dimension ldgy
+ *   x, w          as in the forward, in
+ *   z      [N][M] in, leading dimension ldz: the forward's z; NULL if act is
+ *                 ENGRAM_ACT_NONE (not looked at then)
+ *   grad_x [N][K] out, leading dimension ldgx, or NULL (not wanted)
+ *   grad_w [M][K] out, dense, or NULL (not wanted)
+ *   grad_bias [M] fp32, out, or NULL (not wanted)
+ *   workspace     engram_linear_bwd_workspace_bytes(N, K, M) bytes
+ * At least one of the three outputs.  With an activation dz is rounded to the
+ * element type before the two products (grad_bias sums it unrounded).
+ */
+engram_status engram_linear_bwd(const void *grad_y, const void *x, const void *w, const void *z, void *grad_x,
+                                void *grad_w, float *grad_bias, void *workspace, int64_t N, int64_t K, int64_t M,
+                                int64_t ldgy, int64_t ldx, int64_t ldz, int64_t ldgx, int dtype, int act, void *stream);
+
+/* Scratch bytes of engram_linear_bwd (dz, the slices of grad_bias, the parts
+ * of a split contraction); 0 for sizes the call rejects. */
+size_t engram_linear_bwd_workspace_bytes(int64_t N, int64_t K, int64_t M);
+
+/*
+ * Norms of queries and keys for each head, then the position rotation:
+ *   u = x (mean over the head's D values of x^2 + eps)^(-1/2), y = u w, and
+ *   pair i < R/2 of y turned by positions[n] * freqs[i] / 2^64 of a full turn.
+ * Pair i is (y_i, y_{i+R/2}), or (y_2i, y_{2i+1}) if `interleaved` is not 0;
+ * values from R on are not turned.
+ *   q [N][Hq][D], k [N][Hk][D]  in, leading dimensions ldq, ldk
+ *   wq, wk    [D]  fp32, in: one norm weight for all query (key) heads
+ *   positions [N]  int64, in: any value; NULL if R is 0
+ *   freqs   [R/2]  in: turns per position as 64-bit fractions of a turn
+ *                  (engram_rope_freqs); NULL if R is 0
+ *   q_out, k_out   out, as q and k, leading dimensions ldq_out, ldk_out
+ *   N 1..ENGRAM_QK_ROWS_MAX; Hq, Hk 1..ENGRAM_QK_HEADS_MAX; D a multiple of 8,
+ *   8..ENGRAM_QK_D_MAX; R a multiple of 16, 0..D; 0 <= eps <= 1
+ *   dtype     ENGRAM_BF16, ENGRAM_FP16 or ENGRAM_FP32, of q, k and the outputs
+ * The angle is exact however far the position; everything is fp32 up to the
+ * one rounding of the outputs.
+ */
+#define ENGRAM_QK_ROWS_MAX 4194304
+#define ENGRAM_QK_HEADS_MAX 1024
+#define ENGRAM_QK_D_MAX 512
+engram_status engram_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const float *wk,
+                                      const int64_t *positions, const int64_t *freqs, void *q_out, void *k_out,
+                                      int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t ldq,
+                                      int64_t ldk, int64_t ldq_out, int64_t ldk_out, float eps, int interleaved,
+                                      int dtype, void *stream);
+
+/*
+ * Backward of the above for the gradients of q_out and k_out, from the same
+ * q, k, weights, positions and freqs: the gradients of q and k (leading
+ * dimensions ldgq, ldgk) and of both norm weights, [D] fp32 sums over all
+ * tokens and heads in a fixed order.
+ *   workspace  engram_qk_norm_rope_bwd_workspace_bytes(N, Hq, Hk, D) bytes
+ */
+engram_status engram_qk_norm_rope_bwd(const void *grad_q_out, const void *grad_k_out, const void *q, const void *k,
+                                      const float *wq, const float *wk, const int64_t *positions,
+                                      const int64_t *freqs, void *grad_q, void *grad_k, float *grad_wq,
+                                      float *grad_wk, void *workspace, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
+                                      int64_t R, int64_t ldgq_out, int64_t ldgk_out, int64_t ldq, int64_t ldk,
+                                      int64_t ldgq, int64_t ldgk, float eps, int interleaved, int dtype,
+                                      void *stream);
+
+/* Scratch bytes of engram_qk_norm_rope_bwd; 0 for sizes the call rejects. */
+size_t engram_qk_norm_rope_bwd_workspace_bytes(int64_t N, int64_t Hq, int64_t Hk, int64_t D);
+
+/*
+ * The rotation's table, host arithmetic into HOST memory: freqs[i] =
+ * theta^(-2i/R) / (2 pi) turns per position, times 2^64 (modulo 2^64, two's
+ * complement), i < R/2.  R a multiple of 16, 16..ENGRAM_QK_D_MAX; theta
+ * positive and finite.  A caller with scaled frequencies fills its own.
+ */
+engram_status engram_rope_freqs(double theta, int64_t R, int64_t *freqs);
+
+/*
+ * Causal linear attention with a decay for each head.  For every sequence and
+ * head, with lam = exp(log_decay[h]) and a Dk x Dv state S:
+ *   S_t = lam S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *   q, k [N][H][Dk], v [N][H][Dv]  bf16, in, leading dimensions ldq, ldk, ldv:
+ *                  the tokens of all sequences one behind the other
+ *   log_decay [H]  fp32, in, at most 0 (minus infinity: no past)
+ *   cu_seqlens [B+1] int64, in, device memory: sequence b has the rows from
+ *                  cu_seqlens[b] up to cu_seqlens[b+1]; not decreasing, from 0
+ *                  on; at most N.  Sequences may be empty.  Rows behind the
+ *                  last sequence are left as they are in o.  (The host cannot
+ *                  see the contents: bounds outside 0..N are taken as the
+ *                  nearest of the two, so that nothing outside the arrays is
+ *                  touched, but the results are then unspecified.)
+ *   state_in  [B][H][Dk][Dv] fp32, in: the states before each sequence's first
+ *                  token, or NULL (zero)
+ *   state_out [B][H][Dk][Dv] fp32, out: the states behind each sequence's last
+ *                  token, or NULL (not wanted)
+ *   o [N][H][Dv]   bf16, out, leading dimension ldo
+ *   workspace      engram_decay_attn_fwd_workspace_bytes(N, B, H, Dk, Dv) bytes
+ *   N 1..ENGRAM_DECAY_ROWS_MAX; B 1.., H 1..ENGRAM_DECAY_HEADS_MAX,
+ *   B * H <= ENGRAM_DECAY_STATES_MAX; Dk, Dv multiples of 8, 8..ENGRAM_DECAY_D_MAX
+ *   scale finite
+ * States and sums are fp32 throughout; scores and states are rounded to bf16
+ * as operands of the products that give o.
+ */
+#define ENGRAM_DECAY_ROWS_MAX 16777216
+#define ENGRAM_DECAY_HEADS_MAX 1024
+#define ENGRAM_DECAY_STATES_MAX 4194304 /* B * H */
+#define ENGRAM_DECAY_D_MAX 128
+engram_status engram_decay_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                                    const int64_t *cu_seqlens, const float *state_in, void *o, float *state_out,
+                                    void *workspace, int64_t N, int64_t B, int64_t H, int64_t Dk, int64_t Dv,
+                                    int64_t ldq, int64_t ldk, int64_t ldv, int64_t ldo, float scale, void *stream);
+size_t engram_decay_attn_fwd_workspace_bytes(int64_t N, int64_t B, int64_t H, int64_t Dk, int64_t Dv);
+
+/*
+ * Backward of the above (log_decay is a constant of the layer and has no
+ * gradient): from the gradient grad_o of o and grad_state_out of state_out
+ * (NULL: zero), the gradients of q, k, v and of state_in (NULL: not wanted).
+ * Rows behind the last sequence are left as they are in the gradients.
+ */
+engram_status engram_decay_attn_bwd(const void *grad_o, const void *q, const void *k, const void *v,
+                                    const float *log_decay, const int64_t *cu_seqlens, const float *state_in,
+                                    const float *grad_state_out, void *grad_q, void *grad_k, void *grad_v,
+                                    float *grad_state_in, void *workspace, int64_t N, int64_t B, int64_t H,
+                                    int64_t Dk, int64_t Dv, int64_t ldgo, int64_t ldq, int64_t ldk, int64_t ldv,
+                                    int64_t ldgq, int64_t ldgk, int64_t ldgv, float scale, void *stream);
+size_t engram_decay_attn_bwd_workspace_bytes(int64_t N, int64_t B, int64_t H, int64_t Dk, int64_t Dv);
+
+/*
+ * One token for each row of a decode batch, the states updated in place:
+ *   q, k [B][H][Dk], v [B][H][Dv], o [B][H][Dv]  bf16, as above with rows of
+ *                  the batch for tokens
+ *   state [slots_total][H][Dk][Dv] fp32, in and out: a pool of states
+ *   slots [B]      int64, in, device memory: each row's place in the pool.  A
+ *                  row whose slot is outside 0..slots_total-1 (padding) is
+ *                  skipped and its o left as it is.  Rows with the same slot
+ *                  are tokens of one sequence and are taken in order.
+ *   B 1..ENGRAM_DECAY_STEP_ROWS_MAX; H, Dk, Dv, scale as above;
+ *   slots_total 1..
+ */
+#define ENGRAM_DECAY_STEP_ROWS_MAX 4096
+engram_status engram_decay_attn_step(const void *q, const void *k, const void *v, const float *log_decay,
+                                     float *state, const int64_t *slots, void *o, int64_t B, int64_t H, int64_t Dk,
+                                     int64_t Dv, int64_t slots_total, int64_t ldq, int64_t ldk, int64_t ldv,
+                                     int64_t ldo, float scale, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *engram_status_string(int status);

@@ -24,6 +24,7 @@ BWD_N_MAX = 8192
 BWD_N_MULTIPLE = 64
 
 OK, ERR_NULL, ERR_N_RANGE, ERR_N_MULT64, ERR_ALIGN, ERR_OVERLAP, ERR_LAUNCH = range(7)
+ERR_KIND = 7
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libengram.so is not built ({LIB_PATH}); run __graft_entry__.build() "
@@ -305,5 +306,9 @@ def engram_gateconv_bwd(dY, H, k, v, rms_w_h, rms_w_v, conv_w, vhat, alpha, rrms
                                    _ptr(workspace), M, T, d, _stream(stream, H)))
 
 
+from . import layers as _layers  # noqa: E402  (needs the names above)
+from .layers import *  # noqa: E402,F401,F403
+
 __all__ = ["engram_gate_bwd_noalloc", "engram_gateconv_fwd", "engram_gateconv_bwd", "engram_gateconv_bwd_workspace_bytes", "engram_gate_bwd_with_norm_weights", "engram_fused_weight", "engram_gate_fwd", "engram_gate_bwd", "engram_gate_bwd_workspace_bytes", "EngramError", "lib",
            "LIB_PATH"]
+__all__ += _layers.__all__

@@ -5,6 +5,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,20 +26,35 @@ def sources():
 
 
 def build(verbose: bool = False) -> str:
+    """Every source compiled on its own, side by side, then linked."""
     tmp = LIB + ".tmp"
-    cmd = ["hipcc", *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as objects:
+        jobs, linked = [], []
+        for src in sources():
+            obj = os.path.join(objects, os.path.basename(src) + ".o")
+            jobs.append(["hipcc", *compile_flags, "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, src])
+            linked.append(obj)
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            done = list(pool.map(lambda c: (c, _run(c, verbose)), jobs))
+        done.append((["link"], _run(["hipcc", "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *linked], verbose)
+                     if all(r.returncode == 0 for _, r in done) else None))
     noise = "is not a recognized feature for this target"
-    msgs = [l for l in (r.stdout + r.stderr).splitlines() if noise not in l]
-    if r.returncode != 0:
-        sys.stderr.write("\n".join(msgs) + "\n")
-        raise RuntimeError(f"hipcc failed ({r.returncode}) building {LIB}")
-    if verbose and msgs:
-        print("\n".join(msgs))
+    for cmd, r in done:
+        msgs = [l for l in (r.stdout + r.stderr).splitlines() if noise not in l] if r else []
+        if r is None or r.returncode != 0:
+            sys.stderr.write("\n".join(msgs) + "\n")
+            raise RuntimeError(f"hipcc failed building {LIB}: {cmd[-1]}")
+        if verbose and msgs:
+            print("\n".join(msgs))
     os.replace(tmp, LIB)
     return LIB
+
+
+def _run(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.run(cmd, capture_output=True, text=True)
 
 
 PROBE_SRC = os.path.join(PKG, "probe", "hbm_probe.hip")

@@ -9,7 +9,14 @@
 #include <stdint.h>
 
 #include "engram.h"
+#include "engram_check.h"
 #include "engram_launch.h"
+
+using engram::aligned16;
+using engram::any_overlap;
+using engram::launched;
+using engram::Range;
+using engram::range_of;
 
 namespace {
 
@@ -28,30 +35,6 @@ constexpr int kMaxDevices = 64;
 thread_local int g_last_hip_error = 0;
 std::atomic<int> g_cu_count[kMaxDevices];
 
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-  uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + (uintptr_t)bytes};
-}
-
-bool overlaps(Range a, Range b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Outputs (and scratch) may overlap neither an input nor each other.
-bool any_overlap(const Range* in, int nin, const Range* out, int nout) {
-  for (int i = 0; i < nout; ++i) {
-    for (int j = 0; j < nin; ++j)
-      if (overlaps(out[i], in[j])) return true;
-    for (int j = i + 1; j < nout; ++j)
-      if (overlaps(out[i], out[j])) return true;
-  }
-  return false;
-}
-
 int cu_count() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;
@@ -63,12 +46,12 @@ int cu_count() {
   return v;
 }
 
-engram_status launched(hipError_t e) {
+}  // namespace
+
+engram_status engram::launched(hipError_t e) {
   g_last_hip_error = (int)e;
   return e == hipSuccess ? ENGRAM_OK : ENGRAM_ERR_LAUNCH;
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -236,11 +219,12 @@ const char* engram_status_string(int status) {
   switch (status) {
     case ENGRAM_OK: return "ok";
     case ENGRAM_ERR_NULL: return "a required pointer is NULL";
-    case ENGRAM_ERR_N_RANGE: return "size out of range (gate: forward N 1..4194240, backward N <= 8192; GateConv: M, T >= 1, M*T <= 4194304, d a multiple of 512 up to 5120, 0 <= eps <= 1)";
+    case ENGRAM_ERR_N_RANGE: return "size out of range (gate: forward N 1..4194240, backward N <= 8192; GateConv: M, T >= 1, M*T <= 4194304, d a multiple of 512 up to 5120, 0 <= eps <= 1; the layers: see each call in engram.h)";
     case ENGRAM_ERR_N_MULT64: return "backward N must be a multiple of 64";
     case ENGRAM_ERR_ALIGN: return "floating tensors and workspace must be 16-byte aligned";
     case ENGRAM_ERR_OVERLAP: return "outputs/workspace overlap an input or each other";
     case ENGRAM_ERR_LAUNCH: return "kernel launch failed";
+    case ENGRAM_ERR_KIND: return "an element type or activation that the call does not have";
     default: return "unknown status";
   }
 }

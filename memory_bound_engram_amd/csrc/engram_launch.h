@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "engram.h"
+
 namespace engram {
 
 // Enqueue the forward kernel with `grid` workgroups striding over the tokens (no saved
@@ -60,5 +62,62 @@ hipError_t launch_gateconv_bwd(const void* dY, const void* H, const void* K, con
                                const float* rrk, const float* rrv, void* dH, void* dK, void* dV, float* dwh, float* dwv,
                                float* dcw, void* workspace, int64_t M, int64_t T, int64_t d, int chunk,
                                hipStream_t stream);
+
+// Query/key norm with rotation: one call's arguments (ld: values between
+// tokens).  Backward: grad_q_out, grad_k_out are inputs and q_out, k_out take
+// the gradients of q and k.
+struct QkCall {
+  const void *q, *k, *grad_q_out, *grad_k_out;
+  const float *wq, *wk;
+  const int64_t *positions, *freqs;
+  void *q_out, *k_out;
+  float *grad_wq, *grad_wk;
+  void* workspace;
+  int64_t N, Hq, Hk, D, R;
+  int64_t ldq, ldk, ldgq, ldgk, ldq_out, ldk_out;
+  float eps;
+  bool interleaved;
+  int dtype;
+};
+size_t qk_norm_rope_bwd_workspace(int64_t D);
+hipError_t launch_qk_norm_rope_fwd(const QkCall& q, hipStream_t stream);
+hipError_t launch_qk_norm_rope_bwd(const QkCall& q, hipStream_t stream);
+
+// Decay attention: one call's arguments.
+struct DecayCall {
+  const uint16_t *q, *k, *v, *grad_o;
+  const float* log_decay;
+  const int64_t* cu;            // forward, backward: [B + 1]
+  const float *state_in, *grad_state_out;
+  float *state_out, *grad_state_in;
+  uint16_t *o, *grad_q, *grad_k, *grad_v;
+  void* workspace;
+  float* pool;                  // step: [n_slots] states, and each row's slot
+  const int64_t* slots;
+  int64_t n_slots;
+  int64_t N, B, H, Dk, Dv;
+  int64_t ldq, ldk, ldv, ldo, ldgo, ldgq, ldgk, ldgv;
+  float scale;
+};
+size_t decay_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv);
+hipError_t launch_decay_fwd(const DecayCall& d, hipStream_t stream);
+hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream);
+hipError_t launch_decay_step(const DecayCall& d, hipStream_t stream);
+
+// Linear: one call's arguments.
+struct LinearCall {
+  const void *x, *w, *residual, *grad_y, *z_in;
+  const float* bias;
+  void *y, *z, *grad_x, *grad_w;
+  float* grad_bias;
+  void* workspace;
+  int64_t N, K, M;
+  int64_t ldx, ldr, ldy, ldz, ldgy, ldgx;
+  int dtype, act;
+};
+size_t linear_fwd_workspace(int64_t N, int64_t K, int64_t M);
+size_t linear_bwd_workspace(int64_t N, int64_t K, int64_t M);
+hipError_t launch_linear_fwd(const LinearCall& l, hipStream_t stream);
+hipError_t launch_linear_bwd(const LinearCall& l, hipStream_t stream);
 
 }  // namespace engram

@@ -1,0 +1,657 @@
+// engram_linear.hip -- matrix products with a fused epilogue: the projections
+// in front of the gate and around the token mixers, forward and backward
+// (gfx950).
+//
+//   z = x W^T + bias,   y = act(z) + residual          x [N][K], W [M][K]
+//   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  dbias = sum_n dz
+//
+// One tile kernel makes the three products C[i][j] = sum_c A(i, c) B(j, c).
+// An operand lies with the contraction c contiguous (x and W in the forward)
+// or with i (or j) contiguous (W in dx; dz and x in dW); the second kind is
+// turned on its way from LDS to the registers by the transposing LDS load.
+// Both operands go from memory straight into LDS, 64 values of c at a time,
+// two stages, so that one is filled while the other is multiplied.  The
+// products are fp32 sums over bf16 or fp16 operands on the matrix cores
+// (16x16x32); the one rounding is that of the outputs.  In the backward dz is
+// rounded to the operands' type where it differs from dy (an activation), as
+// it is an operand of two products; dbias is summed before that rounding.
+//
+// Few rows (decode): the weight is read once and bounds the call, so a
+// kernel of its own streams W from memory into the matrix cores without LDS,
+// 16 rows of W to a workgroup whose waves share the contraction.
+#include "engram_device.h"
+#include "engram_launch.h"
+
+namespace engram {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+struct Bf16 {
+  static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return bf_lo(w); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return bf_hi(w); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16x2(a, b); }
+};
+struct Fp16 {
+  static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
+  static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const f16x2 r = {(_Float16)a, (_Float16)b};  // round to nearest even
+    return __builtin_bit_cast(uint32_t, r);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack8(u32x4 r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = T::lo(r[i]);
+    v[2 * i + 1] = T::hi(r[i]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = T::pack(v[2 * i], v[2 * i + 1]);
+  return r;
+}
+
+// erf(x) + 1 halved, the normal distribution at z = x sqrt(2): Abramowitz and
+// Stegun 7.1.26, absolute error 1.5e-7 of erf, far below half a step of the
+// 16-bit outputs; e is exp(-z^2/2), which the gradient needs too.
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float tail = 0.5f * p * t * e;  // the distribution at -|z|
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// act(z); z = -inf gives the limit 0 for silu and gelu.
+__device__ __forceinline__ float act_of(float z, int act) {
+  switch (act) {
+    case ENGRAM_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case ENGRAM_ACT_SILU: return z < -80.0f ? 0.0f : z * sigmoid(z);
+    case ENGRAM_ACT_GELU: return z < -80.0f ? 0.0f : z * normal_cdf(z, __expf(-0.5f * z * z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case ENGRAM_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case ENGRAM_ACT_SILU: {
+      if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;
+      const float p = sigmoid(z);
+      return fmaf(p, z * (1.0f - p), p);
+    }
+    case ENGRAM_ACT_GELU: {
+      if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;
+      const float e = __expf(-0.5f * z * z);
+      return fmaf(z * 0.39894228f, e, normal_cdf(z, e));
+    }
+    default: return 1.0f;
+  }
+}
+
+// What happens to a sum before it is stored; all pointers but y may be null.
+struct Epilogue {
+  const float* bias;
+  const void* residual;
+  void* z;
+  void* y;
+  int64_t ldr, ldz, ldy;
+  int act;
+};
+
+template <typename T>
+__device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], int64_t i, int64_t j, const Epilogue& e) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] += bias[k];
+  if (e.z) store16(static_cast<uint16_t*>(e.z) + i * e.ldz + j, pack8<T>(v));
+  if (e.act != ENGRAM_ACT_NONE) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = act_of(v[k], e.act);
+  }
+  if (e.residual) {
+    float r[8];
+    unpack8<T>(load16(static_cast<const uint16_t*>(e.residual) + i * e.ldr + j), r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += r[k];
+  }
+  store16(static_cast<uint16_t*>(e.y) + i * e.ldy + j, pack8<T>(v));
+}
+
+__device__ __forceinline__ void load_bias(float (&v)[8], const float* bias, int64_t j) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = bias ? bias[j + k] : 0.0f;
+}
+
+// ---------------------------------------------------------------- tiles
+
+constexpr int kBk = 64;                          // contraction values of a stage
+constexpr uint32_t kBeyond = 0xf0000000u;        // an offset outside every tile's buffer: loads give zero
+constexpr uint32_t kTileBytes = 0x80000000u;
+
+struct GemmArgs {
+  const uint16_t *a, *b;
+  int64_t lda, ldb;
+  int64_t I, J, C;      // rows, columns, contraction
+  int ti, tj, splits;   // tiles, parts of the contraction
+  int64_t c_part;       // contraction values of a part, a multiple of kBk
+  float* partial;       // splits > 1: [splits][I][J]
+  Epilogue e;
+};
+
+// One operand's tile in LDS: kRows rows of the product.
+//  contraction contiguous (kTurned false): [kRows][kBk], the eight 16-byte
+//    pieces of row r in the order piece ^ swizzle(r), which spreads the 16
+//    rows that a fragment read touches over all banks;
+//  rows contiguous (kTurned): [kBk][kRows], the 64-byte pieces of line c in
+//    the order piece ^ (c & 3), for the same reason in the transposing reads.
+// kPairs: the rows of two neighbouring 16-row fragments interleave in fours,
+// which leaves a lane of the product with eight neighbouring columns.
+template <int kRows, int kWaves, bool kTurned, bool kPairs>
+struct Operand {
+  static constexpr int kLoads = kRows * kBk * 2 / (kWaves * 1024);  // 16-byte loads of a lane for a stage
+  static_assert(kLoads * kWaves * 1024 == kRows * kBk * 2, "the tile is a whole number of loads");
+
+  static __device__ __forceinline__ int swizzle(int row) { return kPairs ? (row & 3) | ((row >> 1) & 4) : row & 7; }
+
+  // What the lane loads in place q: its row (or line c) and its first value.
+  static __device__ __forceinline__ void place(int q, int wave, int lane, int& line, int& first) {
+    const int at = (q * kWaves + wave) * 64 + lane;
+    if (!kTurned) {
+      line = at / 8;
+      first = (at % 8 ^ swizzle(line)) * 8;
+    } else {
+      constexpr int kPieces = kRows / 8;
+      line = at / kPieces;
+      const int piece = at % kPieces;
+      first = ((piece / 4) ^ (line & 3)) * 32 + piece % 4 * 8;
+    }
+  }
+  // Byte offsets of the lane's loads from the stage's first value.
+  static __device__ __forceinline__ void offsets(uint32_t (&off)[kLoads], int64_t ld, int64_t rows, int64_t left,
+                                                 int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      int line, first;
+      place(q, wave, lane, line, first);
+      const bool in = kTurned ? first < rows && line < left : line < rows && first < left;
+      off[q] = in ? (uint32_t)line * (uint32_t)(ld * 2) + (uint32_t)first * 2 : kBeyond;
+    }
+  }
+  static __device__ __forceinline__ void fill(uint16_t* tile, const uint16_t* from, const uint32_t (&off)[kLoads],
+                                              int wave) {
+    const __amdgpu_buffer_rsrc_t src =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(from), 0, (int)kTileBytes, 0x00020000);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr)(tile + (q * kWaves + wave) * 512), 16, (int)off[q], 0, 0, 0);
+  }
+  // The fragment of rows row0 .. row0+15 (kPairs: of rows row0 .. row0+31, the
+  // fours at half 0 or 1) and contraction values 32 kk .. 32 kk + 31.
+  static __device__ __forceinline__ u32x4 frag(const uint16_t* tile, int row0, int half, int kk, int lane) {
+    const int l = lane % 16, g = lane / 16;
+    if (!kTurned) {
+      const int r = row0 + (kPairs ? 8 * (l / 4) + 4 * half + l % 4 : l);
+      return load16(tile + r * kBk + ((kk * 4 + g) ^ swizzle(r)) * 8);
+    }
+    const int c = 32 * kk + 8 * g + l / 4;
+    const int col = row0 + (kPairs ? 8 * (l % 4) + 4 * half : 4 * (l % 4));
+    const uint16_t* p = tile + c * kRows + ((col / 32) ^ (c & 3)) * 32 + col % 32;
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p));
+    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * kRows)));
+    return u32x4{x[0], x[1], y[0], y[1]};
+  }
+};
+
+// kI x kJ tiles, kWi x kWj waves.
+template <typename T, int kI, int kJ, int kWi, int kWj, bool kTurnA, bool kTurnB>
+__global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
+  constexpr int kWaves = kWi * kWj, kMt = kI / kWi / 16, kNt = kJ / kWj / 16;
+  using A = Operand<kI, kWaves, kTurnA, false>;
+  using B = Operand<kJ, kWaves, kTurnB, true>;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(kI + kJ) * kBk];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // Workgroups go round the eight XCDs; each takes a run of neighbouring tiles
+  // (groups of eight tile rows, column by column), whose operands its L2 holds.
+  const int total = g.ti * g.tj * g.splits, xcd = blockIdx.x & 7, per = total / 8, rest = total % 8;
+  int tile = xcd * per + (xcd < rest ? xcd : rest) + (int)(blockIdx.x >> 3);
+  const int split = tile / (g.ti * g.tj);
+  tile -= split * g.ti * g.tj;
+  constexpr int kGroup = 8;
+  const int group = tile / (kGroup * g.tj), in_group = tile - group * kGroup * g.tj;
+  const int height = min(kGroup, g.ti - group * kGroup);
+  const int64_t i0 = (int64_t)(group * kGroup + in_group % height) * kI, j0 = (int64_t)(in_group / height) * kJ;
+  const int64_t c0 = split * g.c_part, c1 = min(c0 + g.c_part, g.C);
+  const int stages = (int)((c1 - c0 + kBk - 1) / kBk);
+
+  uint32_t oa[A::kLoads], ob[B::kLoads];
+  A::offsets(oa, g.lda, g.I - i0, kBk, wave, lane);
+  B::offsets(ob, g.ldb, g.J - j0, kBk, wave, lane);
+  const uint16_t* pa = g.a + (kTurnA ? c0 * g.lda + i0 : i0 * g.lda + c0);
+  const uint16_t* pb = g.b + (kTurnB ? c0 * g.ldb + j0 : j0 * g.ldb + c0);
+  auto fill = [&](int stage) {
+    const int64_t left = c1 - c0 - (int64_t)stage * kBk;
+    if (left < kBk) {  // the contraction ends inside this stage: the rest is zero
+      A::offsets(oa, g.lda, g.I - i0, left, wave, lane);
+      B::offsets(ob, g.ldb, g.J - j0, left, wave, lane);
+    }
+    A::fill(lds[stage & 1], pa, oa, wave);
+    B::fill(lds[stage & 1] + kI * kBk, pb, ob, wave);
+    pa += kTurnA ? kBk * g.lda : kBk;
+    pb += kTurnB ? kBk * g.ldb : kBk;
+  };
+
+  f32x4 acc[kMt][kNt];
+#pragma unroll
+  for (int m = 0; m < kMt; ++m)
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
+  const int wi = wave / kWj * (kI / kWi), wj = wave % kWj * (kJ / kWj);
+
+  fill(0);
+  for (int s = 0; s < stages; ++s) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of stage s is in LDS
+    __syncthreads();                     // everyone's is, and stage s - 1 is read out
+    if (s + 1 < stages) fill(s + 1);
+    const uint16_t *ta = lds[s & 1], *tb = ta + kI * kBk;
+#pragma unroll
+    for (int kk = 0; kk < kBk / 32; ++kk) {
+      u32x4 fb[kNt];
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) fb[n] = B::frag(tb, wj + n / 2 * 32, n % 2, kk, lane);
+#pragma unroll
+      for (int m = 0; m < kMt; ++m) {
+        const u32x4 fa = A::frag(ta, wi + m * 16, 0, kk, lane);
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) acc[m][n] = T::mfma(fb[n], fa, acc[m][n]);
+      }
+    }
+  }
+
+  // lane: row l of each 16, eight neighbouring columns of each 32
+#pragma unroll
+  for (int n = 0; n < kNt; n += 2) {
+    const int64_t j = j0 + wj + n * 16 + 8 * (lane / 16);
+    if (j >= g.J) continue;
+    float bias[8];
+    if (g.splits == 1) load_bias(bias, g.e.bias, j);
+#pragma unroll
+    for (int m = 0; m < kMt; ++m) {
+      const int64_t i = i0 + wi + m * 16 + lane % 16;
+      if (i >= g.I) continue;
+      if (g.splits > 1) {
+        float* p = g.partial + ((int64_t)split * g.I + i) * g.J + j;
+        *reinterpret_cast<f32x4*>(p) = acc[m][n];
+        *reinterpret_cast<f32x4*>(p + 4) = acc[m][n + 1];
+      } else {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = acc[m][n][k];
+          v[k + 4] = acc[m][n + 1][k];
+        }
+        finish8<T>(v, bias, i, j, g.e);
+      }
+    }
+  }
+}
+
+// Sum of the parts of a split contraction, in order, and the epilogue.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs g) {
+  const int64_t at = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 8;
+  if (at >= g.I * g.J) return;
+  const int64_t i = at / g.J, j = at - i * g.J;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bias[8];
+  for (int s = 0; s < g.splits; ++s) {
+    const float* p = g.partial + s * g.I * g.J + at;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += p[k];
+  }
+  load_bias(bias, g.e.bias, j);
+  finish8<T>(v, bias, i, j, g.e);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// y for N <= 16 kXt rows of x.  A workgroup has 16 kWt rows of W; its waves
+// take every kWaves-th piece of 64 contraction values and join in LDS.
+template <typename T, int kXt, int kWt, int kWaves>
+__global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, const uint16_t* w, int64_t ldx, int N,
+                                                           int64_t K, int64_t M, Epilogue e) {
+  __shared__ f32x4 part[kWaves][kWt][kXt][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane % 16, g = lane / 16;
+  const int64_t m0 = (int64_t)blockIdx.x * 16 * kWt;
+  const uint16_t* wr[kWt];
+  const uint16_t* xr[kXt];
+  // rows behind the last one read the last one again; their sums are not stored
+#pragma unroll
+  for (int t = 0; t < kWt; ++t) wr[t] = w + min(m0 + 16 * t + l, M - 1) * K + 8 * g;
+#pragma unroll
+  for (int t = 0; t < kXt; ++t) xr[t] = x + (int64_t)min(16 * t + l, N - 1) * ldx + 8 * g;
+  f32x4 acc[kWt][kXt];
+#pragma unroll
+  for (int a = 0; a < kWt; ++a)
+#pragma unroll
+    for (int b = 0; b < kXt; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
+  const int pieces = (int)(K / 64);
+  constexpr int kAhead = kXt == 1 ? 4 : kXt == 2 ? 2 : 1;  // pieces whose loads are in flight together
+  int p = wave;
+  for (; p + (kAhead - 1) * kWaves < pieces; p += kAhead * kWaves) {
+    u32x4 fw[kAhead][kWt][2], fx[kAhead][kXt][2];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = (int64_t)(p + u * kWaves) * 64 + 32 * h;
+#pragma unroll
+        for (int t = 0; t < kWt; ++t) fw[u][t][h] = load16_stream(wr[t] + at);
+#pragma unroll
+        for (int t = 0; t < kXt; ++t) fx[u][t][h] = load16(xr[t] + at);
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int a = 0; a < kWt; ++a)
+#pragma unroll
+          for (int b = 0; b < kXt; ++b) acc[a][b] = T::mfma(fw[u][a][h], fx[u][b][h], acc[a][b]);
+  }
+#pragma nounroll
+  for (; p < pieces; p += kWaves) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 fw[kWt], fx[kXt];
+      const int64_t at = (int64_t)p * 64 + 32 * h;
+#pragma unroll
+      for (int t = 0; t < kWt; ++t) fw[t] = load16_stream(wr[t] + at);
+#pragma unroll
+      for (int t = 0; t < kXt; ++t) fx[t] = load16(xr[t] + at);
+#pragma unroll
+      for (int a = 0; a < kWt; ++a)
+#pragma unroll
+        for (int b = 0; b < kXt; ++b) acc[a][b] = T::mfma(fw[a], fx[b], acc[a][b]);
+    }
+  }
+  if (wave == pieces % kWaves) {  // what is left of K, a multiple of 8 below 64
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = (int64_t)pieces * 64 + 32 * h;
+      const bool in = at + 8 * g < K;
+      const u32x4 zero = {0, 0, 0, 0};
+      u32x4 fw[kWt], fx[kXt];
+#pragma unroll
+      for (int t = 0; t < kWt; ++t) fw[t] = in ? load16(wr[t] + at) : zero;
+#pragma unroll
+      for (int t = 0; t < kXt; ++t) fx[t] = in ? load16(xr[t] + at) : zero;
+#pragma unroll
+      for (int a = 0; a < kWt; ++a)
+#pragma unroll
+        for (int b = 0; b < kXt; ++b) acc[a][b] = T::mfma(fw[a], fx[b], acc[a][b]);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < kWt; ++a)
+#pragma unroll
+    for (int b = 0; b < kXt; ++b) part[wave][a][b][lane] = acc[a][b];
+  __syncthreads();
+  // lane: row of x l, four neighbouring rows of W; two lanes' fours make eight columns of y
+  constexpr int kEights = kWt * kXt * 32;
+  for (int at = threadIdx.x; at < kEights; at += kWaves * 64) {
+    const int a = at / (kXt * 32), b = at / 32 % kXt, row = at % 16, half = at / 16 % 2;
+    const int64_t i = 16 * b + row, j = m0 + 16 * a + 8 * half;
+    if (i >= N || j >= M) continue;
+    f32x4 s0 = part[0][a][b][row + 32 * half], s1 = part[0][a][b][row + 32 * half + 16];
+#pragma unroll 2
+    for (int v = 1; v < kWaves; ++v) {
+      s0 += part[v][a][b][row + 32 * half];
+      s1 += part[v][a][b][row + 32 * half + 16];
+    }
+    float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]}, bias[8];
+    load_bias(bias, e.bias, j);
+    finish8<T>(v, bias, i, j, e);
+  }
+}
+
+// ---------------------------------------------------------------- the activation's gradient and dbias
+
+// dz = dy act'(z) and the columns' sums of dz over a slice of the rows.
+constexpr int kGradThreads = 256, kGradCols = 256, kGradLines = 8;
+template <typename T>
+__global__ __launch_bounds__(kGradThreads) void act_grad_kernel(const uint16_t* gy, const uint16_t* z, uint16_t* dz,
+                                                                float* partial, int64_t N, int64_t M, int64_t ldgy,
+                                                                int64_t ldz, int64_t rows, int act) {
+  __shared__ float sums[kGradLines][kGradCols];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const int64_t j = (int64_t)blockIdx.x * kGradCols + 8 * tx;
+  const int64_t n1 = min((int64_t)(blockIdx.y + 1) * rows, N);
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (j < M) {
+#pragma unroll 2
+    for (int64_t n = (int64_t)blockIdx.y * rows + ty; n < n1; n += kGradLines) {
+      float v[8];
+      unpack8<T>(load16_stream(gy + n * ldgy + j), v);
+      if (act != ENGRAM_ACT_NONE) {
+        float zz[8];
+        unpack8<T>(load16_stream(z + n * ldz + j), zz);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= act_slope(zz[k], act);
+        store16(dz + n * M + j, pack8<T>(v));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k] += v[k];
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sums[ty][8 * tx + k] = s[k];
+  __syncthreads();
+  const int64_t col = (int64_t)blockIdx.x * kGradCols + threadIdx.x;
+  if (col < M) {
+    float t = sums[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kGradLines; ++i) t += sums[i][threadIdx.x];
+    partial[blockIdx.y * M + col] = t;
+  }
+}
+
+__global__ __launch_bounds__(256) void bias_grad_kernel(const float* partial, float* db, int64_t M, int slices) {
+  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (col >= M) return;
+  float s = 0.0f;
+  for (int i = 0; i < slices; ++i) s += partial[i * M + col];
+  db[col] = s;
+}
+
+// ---------------------------------------------------------------- plans and launches
+
+struct Plan {
+  bool wide;     // 256 x 256 tiles, else 128 x 128
+  int ti, tj, splits;
+  int64_t c_part;
+};
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Plan plan_of(int64_t I, int64_t J, int64_t C) {
+  Plan p{};
+  p.wide = up(I, 256) * up(J, 256) >= 200;
+  const int t = p.wide ? 256 : 128;
+  p.ti = (int)up(I, t);
+  p.tj = (int)up(J, t);
+  const int64_t tiles = (int64_t)p.ti * p.tj, stages = up(C, kBk);
+  int64_t splits = 1;
+  if (!p.wide && tiles < 256) {  // a split has at least four stages
+    splits = 512 / tiles;
+    if (splits > stages / 4) splits = stages / 4;
+    if (splits < 1) splits = 1;
+  }
+  const int64_t part = up(stages, splits);
+  p.splits = (int)up(stages, part);
+  p.c_part = part * kBk;
+  return p;
+}
+
+size_t plan_bytes(int64_t I, int64_t J, int64_t C) {
+  const Plan p = plan_of(I, J, C);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)I * (size_t)J * sizeof(float) : 0;
+}
+
+template <typename T, bool kTurnA, bool kTurnB>
+hipError_t launch_gemm(GemmArgs g, hipStream_t stream) {
+  const Plan p = plan_of(g.I, g.J, g.C);
+  g.ti = p.ti;
+  g.tj = p.tj;
+  g.splits = p.splits;
+  g.c_part = p.c_part;
+  void* args[] = {&g};
+  const dim3 grid((unsigned)(p.ti * p.tj * p.splits));
+  hipError_t e = p.wide ? hipLaunchKernel((const void*)&gemm_kernel<T, 256, 256, 2, 4, kTurnA, kTurnB>, grid, dim3(512), args, 0, stream)
+                        : hipLaunchKernel((const void*)&gemm_kernel<T, 128, 128, 2, 2, kTurnA, kTurnB>, grid, dim3(256), args, 0, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return hipLaunchKernel((const void*)&gemm_join_kernel<T>, dim3((unsigned)up(g.I * g.J, 8 * kJoinThreads)),
+                         dim3(kJoinThreads), args, 0, stream);
+}
+
+constexpr int64_t kFewRows = 64;
+int64_t grad_rows(int64_t N) { return up(up(N, 64), kGradLines) * kGradLines; }  // rows of a slice: at most 64 slices
+size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
+
+template <typename T, int kXt, int kWt>
+hipError_t launch_rows(const LinearCall& l, const Epilogue& e, hipStream_t stream) {
+  const uint16_t *x = static_cast<const uint16_t*>(l.x), *w = static_cast<const uint16_t*>(l.w);
+  int64_t ldx = l.ldx, K = l.K, M = l.M;
+  int N = (int)l.N;
+  Epilogue ep = e;
+  void* args[] = {&x, &w, &ldx, &N, &K, &M, &ep};
+  const unsigned grid = (unsigned)up(M, 16 * kWt);
+  // waves of a workgroup: enough of them on the chip to keep its memory busy
+  if (grid >= 1024)
+    return hipLaunchKernel((const void*)&rows_kernel<T, kXt, kWt, 4>, dim3(grid), dim3(256), args, 0, stream);
+  if (grid >= 512)
+    return hipLaunchKernel((const void*)&rows_kernel<T, kXt, kWt, 8>, dim3(grid), dim3(512), args, 0, stream);
+  return hipLaunchKernel((const void*)&rows_kernel<T, kXt, kWt, 16>, dim3(grid), dim3(1024), args, 0, stream);
+}
+
+template <typename T>
+hipError_t linear_fwd(const LinearCall& l, hipStream_t stream) {
+  const Epilogue e{l.bias, l.residual, l.z, l.y, l.ldr, l.ldz, l.ldy, l.act};
+  if (l.N <= 16) return launch_rows<T, 1, 1>(l, e, stream);
+  if (l.N <= 32) return launch_rows<T, 2, 1>(l, e, stream);
+  if (l.N <= kFewRows) return launch_rows<T, 4, 1>(l, e, stream);
+  GemmArgs g{};
+  g.a = static_cast<const uint16_t*>(l.x);
+  g.b = static_cast<const uint16_t*>(l.w);
+  g.lda = l.ldx;
+  g.ldb = l.K;
+  g.I = l.N;
+  g.J = l.M;
+  g.C = l.K;
+  g.partial = static_cast<float*>(l.workspace);
+  g.e = e;
+  return launch_gemm<T, false, false>(g, stream);
+}
+
+// Workspace of the backward: dz, the slices' column sums, a split contraction's parts.
+template <typename T>
+hipError_t linear_bwd(const LinearCall& l, hipStream_t stream) {
+  char* ws = static_cast<char*>(l.workspace);
+  uint16_t* dz = reinterpret_cast<uint16_t*>(ws);
+  float* sums = reinterpret_cast<float*>(ws + pad16((size_t)l.N * (size_t)l.M * 2));
+  const int64_t rows = grad_rows(l.N);
+  const int slices = (int)up(l.N, rows);
+  float* parts = sums + pad16((size_t)slices * (size_t)l.M * 4) / 4;
+  const uint16_t* gy = static_cast<const uint16_t*>(l.grad_y);
+  int64_t N = l.N, M = l.M, ldgy = l.ldgy, ldz = l.ldz;
+  if (l.act != ENGRAM_ACT_NONE || l.grad_bias) {
+    const uint16_t* z = static_cast<const uint16_t*>(l.z_in);
+    float* partial = l.grad_bias ? sums : nullptr;
+    int64_t r = rows;
+    int act = l.act;
+    void* args[] = {&gy, &z, &dz, &partial, &N, &M, &ldgy, &ldz, &r, &act};
+    hipError_t e = hipLaunchKernel((const void*)&act_grad_kernel<T>, dim3((unsigned)up(M, kGradCols), (unsigned)slices),
+                                   dim3(kGradThreads), args, 0, stream);
+    if (e != hipSuccess) return e;
+    if (l.grad_bias) {
+      const float* p = sums;
+      float* db = l.grad_bias;
+      int n = slices;
+      void* args2[] = {&p, &db, &M, &n};
+      e = hipLaunchKernel((const void*)&bias_grad_kernel, dim3((unsigned)up(M, 256)), dim3(256), args2, 0, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (l.act != ENGRAM_ACT_NONE) {
+      gy = dz;
+      ldgy = M;
+    }
+  }
+  GemmArgs g{};
+  g.partial = parts;
+  if (l.grad_x) {
+    g.a = gy;
+    g.lda = ldgy;
+    g.b = static_cast<const uint16_t*>(l.w);
+    g.ldb = l.K;
+    g.I = l.N;
+    g.J = l.K;
+    g.C = l.M;
+    g.e = Epilogue{nullptr, nullptr, nullptr, l.grad_x, 0, 0, l.ldgx, ENGRAM_ACT_NONE};
+    const hipError_t e = launch_gemm<T, false, true>(g, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (l.grad_w) {
+    g.a = gy;
+    g.lda = ldgy;
+    g.b = static_cast<const uint16_t*>(l.x);
+    g.ldb = l.ldx;
+    g.I = l.M;
+    g.J = l.K;
+    g.C = l.N;
+    g.e = Epilogue{nullptr, nullptr, nullptr, l.grad_w, 0, 0, l.K, ENGRAM_ACT_NONE};
+    return launch_gemm<T, true, true>(g, stream);
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t linear_fwd_workspace(int64_t N, int64_t K, int64_t M) { return N <= kFewRows ? 0 : plan_bytes(N, M, K); }
+
+size_t linear_bwd_workspace(int64_t N, int64_t K, int64_t M) {
+  const size_t slices = (size_t)up(N, grad_rows(N)), dx = plan_bytes(N, K, M), dw = plan_bytes(M, K, N);
+  return pad16((size_t)N * (size_t)M * 2) + pad16(slices * (size_t)M * 4) + (dx > dw ? dx : dw);
+}
+
+hipError_t launch_linear_fwd(const LinearCall& l, hipStream_t stream) {
+  return l.dtype == ENGRAM_BF16 ? linear_fwd<Bf16>(l, stream) : linear_fwd<Fp16>(l, stream);
+}
+hipError_t launch_linear_bwd(const LinearCall& l, hipStream_t stream) {
+  return l.dtype == ENGRAM_BF16 ? linear_bwd<Bf16>(l, stream) : linear_bwd<Fp16>(l, stream);
+}
+
+}  // namespace engram

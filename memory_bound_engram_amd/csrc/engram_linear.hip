@@ -10,8 +10,7 @@
 // or with i (or j) contiguous (W in dx; dz and x in dW); the second kind is
 // turned on its way from LDS to the registers by the transposing LDS load.
 // Both operands go from memory straight into LDS, 64 values of c at a time,
-// two stages, so that one is filled while the other is multiplied.  The
-// products are fp32 sums over bf16 or fp16 operands on the matrix cores
+// two stages deep.  The products are fp32 sums over bf16 or fp16 operands on the matrix cores
 // (16x16x32); the one rounding is that of the outputs.  In the backward dz is
 // rounded to the operands' type where it differs from dy (an activation), as
 // it is an operand of two products; dbias is summed before that rounding.
@@ -21,6 +20,8 @@
 // 16 rows of W to a workgroup whose waves share the contraction.
 #include "engram_device.h"
 #include "engram_launch.h"
+
+#include <type_traits>
 
 namespace engram {
 namespace {
@@ -70,6 +71,11 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return r;
 }
 
+template <typename T>
+__device__ __forceinline__ u32x2 pack4(f32x4 v) {
+  return u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+}
+
 // erf(x) + 1 halved, the normal distribution at z = x sqrt(2): Abramowitz and
 // Stegun 7.1.26, absolute error 1.5e-7 of erf, far below half a step of the
 // 16-bit outputs; e is exp(-z^2/2), which the gradient needs too.
@@ -93,6 +99,11 @@ __device__ __forceinline__ float act_of(float z, int act) {
     case ENGRAM_ACT_GELU: return z < -80.0f ? 0.0f : z * normal_cdf(z, __expf(-0.5f * z * z));
     default: return z;
   }
+}
+template <int kAct>
+__device__ __forceinline__ void act8(float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = act_of(v[k], kAct);
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
@@ -126,9 +137,10 @@ __device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], i
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] += bias[k];
   if (e.z) store16(static_cast<uint16_t*>(e.z) + i * e.ldz + j, pack8<T>(v));
-  if (e.act != ENGRAM_ACT_NONE) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_of(v[k], e.act);
+  switch (e.act) {
+    case ENGRAM_ACT_RELU: act8<ENGRAM_ACT_RELU>(v); break;
+    case ENGRAM_ACT_SILU: act8<ENGRAM_ACT_SILU>(v); break;
+    case ENGRAM_ACT_GELU: act8<ENGRAM_ACT_GELU>(v); break;
   }
   if (e.residual) {
     float r[8];
@@ -140,8 +152,16 @@ __device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], i
 }
 
 __device__ __forceinline__ void load_bias(float (&v)[8], const float* bias, int64_t j) {
+  f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+  if (bias) {
+    a = *reinterpret_cast<const f32x4*>(bias + j);
+    b = *reinterpret_cast<const f32x4*>(bias + j + 4);
+  }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = bias ? bias[j + k] : 0.0f;
+  for (int k = 0; k < 4; ++k) {
+    v[k] = a[k];
+    v[k + 4] = b[k];
+  }
 }
 
 // ---------------------------------------------------------------- tiles
@@ -150,117 +170,179 @@ constexpr int kBk = 64;                          // contraction values of a stag
 constexpr uint32_t kBeyond = 0xf0000000u;        // an offset outside every tile's buffer: loads give zero
 constexpr uint32_t kTileBytes = 0x80000000u;
 
+// The product's tiles: the first `whole` are made by one workgroup each, the
+// contraction of each of the others is cut into `parts`, whose sums go to
+// `partial` ([tile][part] tiles of fp32) for the join kernel.
 struct GemmArgs {
   const uint16_t *a, *b;
   int64_t lda, ldb;
   int64_t I, J, C;      // rows, columns, contraction
-  int ti, tj, splits;   // tiles, parts of the contraction
+  int ti, tj, whole, parts;
   int64_t c_part;       // contraction values of a part, a multiple of kBk
-  float* partial;       // splits > 1: [splits][I][J]
+  float* partial;
   Epilogue e;
 };
 
-// One operand's tile in LDS: kRows rows of the product.
-//  contraction contiguous (kTurned false): [kRows][kBk], the eight 16-byte
-//    pieces of row r in the order piece ^ swizzle(r), which spreads the 16
-//    rows that a fragment read touches over all banks;
-//  rows contiguous (kTurned): [kBk][kRows], the 64-byte pieces of line c in
-//    the order piece ^ (c & 3), for the same reason in the transposing reads.
-// kPairs: the rows of two neighbouring 16-row fragments interleave in fours,
-// which leaves a lane of the product with eight neighbouring columns.
-template <int kRows, int kWaves, bool kTurned, bool kPairs>
-struct Operand {
-  static constexpr int kLoads = kRows * kBk * 2 / (kWaves * 1024);  // 16-byte loads of a lane for a stage
-  static_assert(kLoads * kWaves * 1024 == kRows * kBk * 2, "the tile is a whole number of loads");
-
-  static __device__ __forceinline__ int swizzle(int row) { return kPairs ? (row & 3) | ((row >> 1) & 4) : row & 7; }
-
-  // What the lane loads in place q: its row (or line c) and its first value.
-  static __device__ __forceinline__ void place(int q, int wave, int lane, int& line, int& first) {
-    const int at = (q * kWaves + wave) * 64 + lane;
-    if (!kTurned) {
-      line = at / 8;
-      first = (at % 8 ^ swizzle(line)) * 8;
-    } else {
-      constexpr int kPieces = kRows / 8;
-      line = at / kPieces;
-      const int piece = at % kPieces;
-      first = ((piece / 4) ^ (line & 3)) * 32 + piece % 4 * 8;
-    }
-  }
-  // Byte offsets of the lane's loads from the stage's first value.
-  static __device__ __forceinline__ void offsets(uint32_t (&off)[kLoads], int64_t ld, int64_t rows, int64_t left,
-                                                 int wave, int lane) {
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      int line, first;
-      place(q, wave, lane, line, first);
-      const bool in = kTurned ? first < rows && line < left : line < rows && first < left;
-      off[q] = in ? (uint32_t)line * (uint32_t)(ld * 2) + (uint32_t)first * 2 : kBeyond;
-    }
-  }
-  static __device__ __forceinline__ void fill(uint16_t* tile, const uint16_t* from, const uint32_t (&off)[kLoads],
-                                              int wave) {
-    const __amdgpu_buffer_rsrc_t src =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(from), 0, (int)kTileBytes, 0x00020000);
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr)(tile + (q * kWaves + wave) * 512), 16, (int)off[q], 0, 0, 0);
-  }
-  // The fragment of rows row0 .. row0+15 (kPairs: of rows row0 .. row0+31, the
-  // fours at half 0 or 1) and contraction values 32 kk .. 32 kk + 31.
-  static __device__ __forceinline__ u32x4 frag(const uint16_t* tile, int row0, int half, int kk, int lane) {
-    const int l = lane % 16, g = lane / 16;
-    if (!kTurned) {
-      const int r = row0 + (kPairs ? 8 * (l / 4) + 4 * half + l % 4 : l);
-      return load16(tile + r * kBk + ((kk * 4 + g) ^ swizzle(r)) * 8);
-    }
-    const int c = 32 * kk + 8 * g + l / 4;
-    const int col = row0 + (kPairs ? 8 * (l % 4) + 4 * half : 4 * (l % 4));
-    const uint16_t* p = tile + c * kRows + ((col / 32) ^ (c & 3)) * 32 + col % 32;
-    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p));
-    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * kRows)));
-    return u32x4{x[0], x[1], y[0], y[1]};
-  }
-};
-
-// kI x kJ tiles, kWi x kWj waves.
-template <typename T, int kI, int kJ, int kWi, int kWj, bool kTurnA, bool kTurnB>
-__global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
-  constexpr int kWaves = kWi * kWj, kMt = kI / kWi / 16, kNt = kJ / kWj / 16;
-  using A = Operand<kI, kWaves, kTurnA, false>;
-  using B = Operand<kJ, kWaves, kTurnB, true>;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(kI + kJ) * kBk];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-  // Workgroups go round the eight XCDs; each takes a run of neighbouring tiles
-  // (groups of eight tile rows, column by column), whose operands its L2 holds.
-  const int total = g.ti * g.tj * g.splits, xcd = blockIdx.x & 7, per = total / 8, rest = total % 8;
-  int tile = xcd * per + (xcd < rest ? xcd : rest) + (int)(blockIdx.x >> 3);
-  const int split = tile / (g.ti * g.tj);
-  tile -= split * g.ti * g.tj;
+// Where a tile lies: groups of eight tile rows, column by column, so that
+// neighbouring workgroups share operands.
+__device__ __forceinline__ void tile_origin(const GemmArgs& g, int tile, int size_i, int size_j, int64_t& i0, int64_t& j0) {
   constexpr int kGroup = 8;
   const int group = tile / (kGroup * g.tj), in_group = tile - group * kGroup * g.tj;
   const int height = min(kGroup, g.ti - group * kGroup);
-  const int64_t i0 = (int64_t)(group * kGroup + in_group % height) * kI, j0 = (int64_t)(in_group / height) * kJ;
-  const int64_t c0 = split * g.c_part, c1 = min(c0 + g.c_part, g.C);
+  i0 = (int64_t)(group * kGroup + in_group % height) * size_i;
+  j0 = (int64_t)(in_group / height) * size_j;
+}
+
+// 16 bytes a lane from src + off into LDS, lane l's at to + 16 l.  Written in
+// assembly because the compiler, for the builtin, waits for every load on its
+// way before a transposing LDS read (dx 1.19 ms instead of 0.9 ms at 8192^3);
+// there is no result register, and the waits are `meet` below.
+__device__ __forceinline__ void load_to_lds(uint32_t to, u32x4 src, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(to), "v"(off), "s"(src)
+               : "memory");  // m0 is reserved: the compiler itself sets it anew wherever it uses it
+}
+
+typedef __attribute__((address_space(3))) const u32x4* lds_u32x4;
+
+// One operand's stage in LDS: kRows rows of the product, 64 contraction values.
+//  contraction contiguous (kTurned false): [kRows][64], a line of memory a
+//    row, its eight 16-byte pieces in the order piece ^ swizzle(row);
+//  rows contiguous (kTurned): [64][kRows], the 64-byte pieces of line c in the
+//    order piece ^ (c & 3) and their halves changed over in every other eight
+//    lines.
+// Either way the lanes that LDS serves at once (sixteen of a 16-byte read: rows
+// 0-3 and 12-15 of one piece with 4-11 of the next, or the other way round;
+// thirty-two of a transposing read) find their values in different banks.
+// kPairs (not kTurned): the rows of two neighbouring 16-row fragments
+// interleave in fours, which leaves a lane of the product with eight
+// neighbouring columns instead of four and four.
+// kFrags fragments of 16 rows belong to a wave.
+template <int kRows, int kWaves, int kFrags, bool kTurned, bool kPairs>
+struct Operand {
+  static constexpr int kLoads = kRows * kBk * 2 / (kWaves * 1024);  // 16-byte loads of a lane for a stage
+  static constexpr int kReads = kTurned ? 2 : 1;                    // LDS reads of a fragment
+  static_assert(kLoads * kWaves * 1024 == kRows * kBk * 2, "the tile is a whole number of loads");
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    return kPairs ? ((row >> 3) & 3) << 1 | ((row >> 1) & 1) : (row >> 1) & 7;
+  }
+  static __device__ __forceinline__ int halves(int line) { return ((line >> 3) ^ (line >> 4)) & 1; }
+
+  // The lane's loads of a stage: byte offsets from the stage's first value,
+  // and of the first load its contraction value (those of the others: kStep more each).
+  static constexpr int kStep = kTurned ? kWaves * 64 / (kRows / 8) : 0;
+  struct Loads {
+    uint32_t off[kLoads];
+    int c;
+    __device__ __forceinline__ void set(int64_t ld, int64_t rows, int wave, int lane) {
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        const int at = (q * kWaves + wave) * 64 + lane;
+        int line, first;
+        if (!kTurned) {
+          line = at / 8;
+          first = (at % 8 ^ swizzle(line)) * 8;
+        } else {
+          constexpr int kPieces = kRows / 8;
+          line = at / kPieces;
+          const int piece = at % kPieces;
+          first = ((piece / 4) ^ (line & 3)) * 32 + ((piece % 4) ^ 2 * halves(line)) * 8;
+        }
+        if (q == 0) c = kTurned ? line : first;
+        off[q] = (kTurned ? first : line) < rows ? (uint32_t)line * (uint32_t)(ld * 2) + (uint32_t)first * 2 : kBeyond;
+      }
+    }
+    // Into LDS at `to`; contraction values from `left` on are zero.
+    __device__ __forceinline__ void fill(uint32_t to, const uint16_t* from, int left, int wave) const {
+      const uint64_t at = reinterpret_cast<uint64_t>(from);
+      const u32x4 src = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, kTileBytes, 0x00020000u};
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q)
+        load_to_lds(to + (q * kWaves + wave) * 1024u, src, c + q * kStep < left ? off[q] : kBeyond);
+    }
+  };
+
+  // Where the lane finds its part of the wave's fragments in a stage: byte
+  // addresses, to which half h of the contraction and the fragment add
+  // constants.  Turned: one for each 64-byte piece and half of it.
+  static constexpr int kPlaces = kTurned ? (kFrags < 8 ? kFrags : 8) : 2;
+  struct Places {
+    uint32_t at[kPlaces];
+    __device__ __forceinline__ void set(uint32_t lds, int row0, int lane) {
+      const int l = lane % 16, g = lane / 16;
+      if (!kTurned) {
+        const int r = row0 + (kPairs ? 8 * (l / 4) + l % 4 : l);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) at[h] = lds + 2 * (r * kBk + ((4 * h + g) ^ swizzle(r)) * 8);
+      } else {
+        const int c = 8 * g + l / 4;
+#pragma unroll
+        for (int n = 0; n < kPlaces; ++n) {
+          const int col = row0 + n * 16 + 4 * (l % 4);
+          at[n] = lds + 2 * (c * kRows + ((col / 32) ^ (c & 3)) * 32 + (col % 32 ^ 16 * halves(c)));
+        }
+      }
+    }
+    template <int kHalf>
+    __device__ __forceinline__ u32x4 frag(int n, uint32_t stage) const {
+      if constexpr (!kTurned) {
+        const int row = kPairs ? n / 2 * 32 + n % 2 * 4 : n * 16;
+        return *((lds_u32x4)(uintptr_t)(at[kHalf] + stage) + row * kBk / 8);
+      } else {
+        const lds_s16x4 p = (lds_s16x4)(uintptr_t)(at[n % kPlaces] + stage) + (n / kPlaces * 16 * kPlaces + 32 * kHalf * kRows) / 4;
+        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + kRows));
+        return u32x4{x[0], x[1], y[0], y[1]};
+      }
+    }
+  };
+};
+
+// kI x kJ tiles, kWi x kWj waves.  Two stages in LDS, and half a stage's
+// fragments ahead in registers: while one half is multiplied, the next half is
+// read; in the middle of a stage it is read out, and the stage after the next
+// is sent for into its place, one whole stage of products before its use.
+template <typename T, int kI, int kJ, int kWi, int kWj, bool kTurnA, bool kTurnB>
+__global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
+  constexpr int kWaves = kWi * kWj, kMt = kI / kWi / 16, kNt = kJ / kWj / 16;
+  using A = Operand<kI, kWaves, kMt, kTurnA, false>;
+  using B = Operand<kJ, kWaves, kNt, kTurnB, !kTurnB>;
+  constexpr uint32_t kStageBytes = (kI + kJ) * kBk * 2;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(kI + kJ) * kBk];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // Workgroups go round the eight XCDs; each takes a run of neighbouring
+  // tiles, whose operands its L2 holds.
+  int tile = blockIdx.x, part = 0;
+  if (tile < g.whole) {
+    const int xcd = tile & 7, per = g.whole / 8, rest = g.whole % 8;
+    tile = xcd * per + min(xcd, rest) + (tile >> 3);
+  } else {
+    part = (tile - g.whole) % g.parts;
+    tile = g.whole + (tile - g.whole) / g.parts;
+  }
+  const bool cut = tile >= g.whole;
+  int64_t i0, j0;
+  tile_origin(g, tile, kI, kJ, i0, j0);
+  const int64_t c0 = cut ? part * g.c_part : 0, c1 = cut ? min(c0 + g.c_part, g.C) : g.C;
   const int stages = (int)((c1 - c0 + kBk - 1) / kBk);
 
-  uint32_t oa[A::kLoads], ob[B::kLoads];
-  A::offsets(oa, g.lda, g.I - i0, kBk, wave, lane);
-  B::offsets(ob, g.ldb, g.J - j0, kBk, wave, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr)&lds[0][0];
+  typename A::Loads la;
+  typename B::Loads lb;
+  la.set(g.lda, g.I - i0, wave, lane);
+  lb.set(g.ldb, g.J - j0, wave, lane);
   const uint16_t* pa = g.a + (kTurnA ? c0 * g.lda + i0 : i0 * g.lda + c0);
   const uint16_t* pb = g.b + (kTurnB ? c0 * g.ldb + j0 : j0 * g.ldb + c0);
-  auto fill = [&](int stage) {
-    const int64_t left = c1 - c0 - (int64_t)stage * kBk;
-    if (left < kBk) {  // the contraction ends inside this stage: the rest is zero
-      A::offsets(oa, g.lda, g.I - i0, left, wave, lane);
-      B::offsets(ob, g.ldb, g.J - j0, left, wave, lane);
-    }
-    A::fill(lds[stage & 1], pa, oa, wave);
-    B::fill(lds[stage & 1] + kI * kBk, pb, ob, wave);
+  int left = (int)(c1 - c0);
+  auto fill = [&](uint32_t stage) {  // a stage behind the last is zeros
+    la.fill(lds0 + stage, pa, left, wave);
+    lb.fill(lds0 + stage + kI * kBk * 2, pb, left, wave);
     pa += kTurnA ? kBk * g.lda : kBk;
     pb += kTurnB ? kBk * g.ldb : kBk;
+    left -= kBk;
   };
 
   f32x4 acc[kMt][kNt];
@@ -269,67 +351,152 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
 #pragma unroll
     for (int n = 0; n < kNt; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
   const int wi = wave / kWj * (kI / kWi), wj = wave % kWj * (kJ / kWj);
+  typename A::Places wa;
+  typename B::Places wb;
+  wa.set(lds0, wi, lane);
+  wb.set(lds0 + kI * kBk * 2, wj, lane);
+  u32x4 fa[2][kMt], fb[2][kNt];
+  auto read = [&](auto half, uint32_t stage) {
+    constexpr int h = decltype(half)::value;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) fb[h][n] = wb.template frag<h>(n, stage);
+#pragma unroll
+    for (int m = 0; m < kMt; ++m) fa[h][m] = wa.template frag<h>(m, stage);
+  };
+  // The products of one half, the LDS reads of the next between them.
+  auto multiply = [&](auto half) {
+    constexpr int h = decltype(half)::value;
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) acc[m][n] = T::mfma(fb[h][n], fa[h][m], acc[m][n]);
+    constexpr int kReads = kNt * B::kReads + kMt * A::kReads, kEach = kMt * kNt / kReads > 0 ? kMt * kNt / kReads : 1;
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // an LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);  // matrix products
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // All but this wave's `newer` youngest loads are in LDS and its reads done; then all waves'.
+  auto meet = [&](auto newer) {
+    constexpr int n = decltype(newer)::value;
+    static_assert(n < 16, "one field of the wait count");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0070 | n);  // vmcnt n, lgkmcnt 0
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> kFirst{};
+  constexpr std::integral_constant<int, 1> kSecond{};
 
   fill(0);
+  fill(kStageBytes);
+  meet(std::integral_constant<int, A::kLoads + B::kLoads>{});
+  read(kFirst, 0);
+  uint32_t stage = 0;
+#pragma nounroll
   for (int s = 0; s < stages; ++s) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of stage s is in LDS
-    __syncthreads();                     // everyone's is, and stage s - 1 is read out
-    if (s + 1 < stages) fill(s + 1);
-    const uint16_t *ta = lds[s & 1], *tb = ta + kI * kBk;
+    read(kSecond, stage);
+    multiply(kFirst);
+    meet(std::integral_constant<int, 0>{});  // stage s + 1 is there, stage s read out by all
+    fill(stage);
+    stage ^= kStageBytes;
+    read(kFirst, stage);
+    multiply(kSecond);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the last fills, of nothing, must not outlive the workgroup's LDS
+
+  // lane: row l of each 16; eight neighbouring columns of each 32 (a turned B: two fours, 16 apart)
+  const bool plain = !g.e.z && !g.e.residual && g.e.act == ENGRAM_ACT_NONE;
+  if (cut || kTurnB || plain) {
+    float* sums = cut ? g.partial + ((int64_t)(tile - g.whole) * g.parts + part) * kI * kJ : nullptr;
+    constexpr int kApart = kTurnB ? 16 : 4;
 #pragma unroll
-    for (int kk = 0; kk < kBk / 32; ++kk) {
-      u32x4 fb[kNt];
-#pragma unroll
-      for (int n = 0; n < kNt; ++n) fb[n] = B::frag(tb, wj + n / 2 * 32, n % 2, kk, lane);
+    for (int n = 0; n < kNt; n += 2) {
+      const int jj = wj + n * 16 + (kTurnB ? 4 : 8) * (lane / 16);
+      float bias[8];
+      load_bias(bias, cut || kTurnB || j0 + jj >= g.J ? nullptr : g.e.bias, j0 + jj);
 #pragma unroll
       for (int m = 0; m < kMt; ++m) {
-        const u32x4 fa = A::frag(ta, wi + m * 16, 0, kk, lane);
+        const int ii = wi + m * 16 + lane % 16;
+        if (i0 + ii >= g.I) continue;
+        if (cut) {
+          float* p = sums + ii * kJ + jj;
+          *reinterpret_cast<f32x4*>(p) = acc[m][n];
+          *reinterpret_cast<f32x4*>(p + kApart) = acc[m][n + 1];
+          continue;
+        }
+        uint16_t* p = static_cast<uint16_t*>(g.e.y) + (i0 + ii) * g.e.ldy + j0 + jj;
+        if constexpr (kTurnB) {
+          if (j0 + jj < g.J) *reinterpret_cast<u32x2*>(p) = pack4<T>(acc[m][n]);
+          if (j0 + jj + 16 < g.J) *reinterpret_cast<u32x2*>(p + 16) = pack4<T>(acc[m][n + 1]);
+        } else if (j0 + jj < g.J) {
+          float v[8];
 #pragma unroll
-        for (int n = 0; n < kNt; ++n) acc[m][n] = T::mfma(fb[n], fa, acc[m][n]);
+          for (int k = 0; k < 4; ++k) {
+            v[k] = acc[m][n][k] + bias[k];
+            v[k + 4] = acc[m][n + 1][k] + bias[k + 4];
+          }
+          store16(p, pack8<T>(v));
+        }
       }
     }
+    return;
   }
-
-  // lane: row l of each 16, eight neighbouring columns of each 32
+  // With an activation, a residual or z the epilogue is long, and unrolled over
+  // the accumulators it would be more code than the instruction cache holds: the
+  // sums go through LDS, 32 columns of each wave at a time, and one loop ends them.
+  // Piece p (four columns) of row r lies at p ^ (r & 7).
+  if constexpr (!kTurnB) {
+    __syncthreads();  // the last fragments are read
+    constexpr int kRows = kI / kWi;
+    float* mine = reinterpret_cast<float*>(&lds[0][0]) + wave * kRows * 32;
+    static_assert(kWaves * kRows * 32 * sizeof(float) <= sizeof(lds), "the waves' sums fit");
 #pragma unroll
-  for (int n = 0; n < kNt; n += 2) {
-    const int64_t j = j0 + wj + n * 16 + 8 * (lane / 16);
-    if (j >= g.J) continue;
-    float bias[8];
-    if (g.splits == 1) load_bias(bias, g.e.bias, j);
+    for (int n = 0; n < kNt; n += 2) {
 #pragma unroll
-    for (int m = 0; m < kMt; ++m) {
-      const int64_t i = i0 + wi + m * 16 + lane % 16;
-      if (i >= g.I) continue;
-      if (g.splits > 1) {
-        float* p = g.partial + ((int64_t)split * g.I + i) * g.J + j;
-        *reinterpret_cast<f32x4*>(p) = acc[m][n];
-        *reinterpret_cast<f32x4*>(p + 4) = acc[m][n + 1];
-      } else {
-        float v[8];
+      for (int m = 0; m < kMt; ++m)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = acc[m][n][k];
-          v[k + 4] = acc[m][n + 1][k];
+        for (int h = 0; h < 2; ++h) {
+          const int r = m * 16 + lane % 16;
+          *reinterpret_cast<f32x4*>(mine + r * 32 + ((2 * (lane / 16) + h) ^ (r & 7)) * 4) = acc[m][n + h];
         }
-        finish8<T>(v, bias, i, j, g.e);
+      const int64_t j = j0 + wj + n * 16 + 8 * (lane % 4);
+      float bias[8];
+      load_bias(bias, j < g.J ? g.e.bias : nullptr, j);
+#pragma nounroll
+      for (int r = lane / 4; r < kRows; r += 16) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(mine + r * 32 + ((2 * (lane % 4)) ^ (r & 7)) * 4);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(mine + r * 32 + ((2 * (lane % 4) + 1) ^ (r & 7)) * 4);
+        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        const int64_t i = i0 + wi + r;
+        if (i < g.I && j < g.J) finish8<T>(v, bias, i, j, g.e);
       }
     }
   }
 }
 
-// Sum of the parts of a split contraction, in order, and the epilogue.
+// The cut tiles: the sum of each one's parts, in order, and the epilogue.
 constexpr int kJoinThreads = 256;
-template <typename T>
+template <typename T, int kI, int kJ>
 __global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs g) {
-  const int64_t at = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 8;
-  if (at >= g.I * g.J) return;
-  const int64_t i = at / g.J, j = at - i * g.J;
+  const int tile = blockIdx.y, at = (blockIdx.x * kJoinThreads + threadIdx.x) * 8;
+  int64_t i0, j0;
+  tile_origin(g, g.whole + tile, kI, kJ, i0, j0);
+  const int64_t i = i0 + at / kJ, j = j0 + at % kJ;
+  if (i >= g.I || j >= g.J) return;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bias[8];
-  for (int s = 0; s < g.splits; ++s) {
-    const float* p = g.partial + s * g.I * g.J + at;
+  const float* p = g.partial + (int64_t)tile * g.parts * kI * kJ + at;
+  for (int s = 0; s < g.parts; ++s, p += kI * kJ) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += p[k];
+    for (int k = 0; k < 4; ++k) {
+      v[k] += a[k];
+      v[k + 4] += b[k];
+    }
   }
   load_bias(bias, g.e.bias, j);
   finish8<T>(v, bias, i, j, g.e);
@@ -490,36 +657,63 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* partial, fl
 
 // ---------------------------------------------------------------- plans and launches
 
-struct Plan {
-  bool wide;     // 256 x 256 tiles, else 128 x 128
-  int ti, tj, splits;
-  int64_t c_part;
-};
-
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-Plan plan_of(int64_t I, int64_t J, int64_t C) {
+// How a product is cut into workgroups.  256 x 256 tiles, one to a CU, or
+// 128 x 128, two to a CU.  Tiles that fill whole rounds of the chip's 256 (512)
+// places are made whole; those of the last, partial round are cut along the
+// contraction into as many parts as there are places for, at least four
+// stages each.
+struct Plan {
+  bool wide;
+  int ti, tj, whole, cut, parts;
+  int64_t c_part;
+  double cost;
+};
+
+Plan plan_with(bool wide, int64_t I, int64_t J, int64_t C) {
   Plan p{};
-  p.wide = up(I, 256) * up(J, 256) >= 200;
-  const int t = p.wide ? 256 : 128;
-  p.ti = (int)up(I, t);
-  p.tj = (int)up(J, t);
+  p.wide = wide;
+  const int64_t size = wide ? 256 : 128, places = wide ? 256 : 512;
+  p.ti = (int)up(I, size);
+  p.tj = (int)up(J, size);
   const int64_t tiles = (int64_t)p.ti * p.tj, stages = up(C, kBk);
-  int64_t splits = 1;
-  if (!p.wide && tiles < 256) {  // a split has at least four stages
-    splits = 512 / tiles;
-    if (splits > stages / 4) splits = stages / 4;
-    if (splits < 1) splits = 1;
-  }
-  const int64_t part = up(stages, splits);
-  p.splits = (int)up(stages, part);
-  p.c_part = part * kBk;
+  const int64_t last = tiles % places;
+  int64_t parts = last ? places / last : 1;
+  if (parts > stages / 4) parts = stages / 4;
+  if (parts < 1) parts = 1;
+  const int64_t part_stages = up(stages, parts);
+  parts = up(stages, part_stages);
+  p.parts = (int)parts;
+  p.c_part = part_stages * kBk;
+  p.cut = parts > 1 ? (int)last : 0;
+  p.whole = (int)tiles - p.cut;
+  // microseconds: a stage of a full CU, and the cut tiles' sums written and read again
+  const double round = (wide ? 1.40 : 0.84) * stages;
+  p.cost = up(p.whole, places) * round;
+  if (p.cut) p.cost += round / (double)parts + 6.0 + p.cut * (double)parts * (double)(size * size) * 8.0 / 4.0e6;
   return p;
+}
+
+Plan plan_of(int64_t I, int64_t J, int64_t C) {
+  const Plan a = plan_with(true, I, J, C), b = plan_with(false, I, J, C);
+  return a.cost <= b.cost ? a : b;
 }
 
 size_t plan_bytes(int64_t I, int64_t J, int64_t C) {
   const Plan p = plan_of(I, J, C);
-  return p.splits > 1 ? (size_t)p.splits * (size_t)I * (size_t)J * sizeof(float) : 0;
+  const size_t size = p.wide ? 256 : 128;
+  return (size_t)p.cut * (size_t)p.parts * size * size * sizeof(float);
+}
+
+template <typename T, bool kTurnA, bool kTurnB, int kSize, int kWi, int kWj>
+hipError_t launch_tiles(const Plan& p, GemmArgs& g, hipStream_t stream) {
+  void* args[] = {&g};
+  const hipError_t e = hipLaunchKernel((const void*)&gemm_kernel<T, kSize, kSize, kWi, kWj, kTurnA, kTurnB>,
+                                       dim3((unsigned)(p.whole + p.cut * p.parts)), dim3(kWi * kWj * 64), args, 0, stream);
+  if (e != hipSuccess || p.cut == 0) return e;
+  return hipLaunchKernel((const void*)&gemm_join_kernel<T, kSize, kSize>,
+                         dim3(kSize * kSize / 8 / kJoinThreads, (unsigned)p.cut), dim3(kJoinThreads), args, 0, stream);
 }
 
 template <typename T, bool kTurnA, bool kTurnB>
@@ -527,15 +721,11 @@ hipError_t launch_gemm(GemmArgs g, hipStream_t stream) {
   const Plan p = plan_of(g.I, g.J, g.C);
   g.ti = p.ti;
   g.tj = p.tj;
-  g.splits = p.splits;
+  g.whole = p.whole;
+  g.parts = p.parts;
   g.c_part = p.c_part;
-  void* args[] = {&g};
-  const dim3 grid((unsigned)(p.ti * p.tj * p.splits));
-  hipError_t e = p.wide ? hipLaunchKernel((const void*)&gemm_kernel<T, 256, 256, 2, 4, kTurnA, kTurnB>, grid, dim3(512), args, 0, stream)
-                        : hipLaunchKernel((const void*)&gemm_kernel<T, 128, 128, 2, 2, kTurnA, kTurnB>, grid, dim3(256), args, 0, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
-  return hipLaunchKernel((const void*)&gemm_join_kernel<T>, dim3((unsigned)up(g.I * g.J, 8 * kJoinThreads)),
-                         dim3(kJoinThreads), args, 0, stream);
+  return p.wide ? launch_tiles<T, kTurnA, kTurnB, 256, 2, 4>(p, g, stream)
+                : launch_tiles<T, kTurnA, kTurnB, 128, 2, 2>(p, g, stream);
 }
 
 constexpr int64_t kFewRows = 64;

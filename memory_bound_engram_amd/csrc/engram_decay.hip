@@ -31,17 +31,17 @@
 // The scores (times their power of the decay) and X are rounded to bf16 where
 // they become operands of the products that give y, which is rounded to bf16
 // itself.  The products that update X, which all later chunks read and the
-// caller gets in fp32, take c times its power of the decay as the sum of two
-// bf16 values (relative error 2^-17), so X keeps fp32's standing.
+// caller gets in fp32, take c times its power of the decay as the sum of three
+// bf16 values, 24 bits, which is all of it (two leave 2.5e-6 of the state).
 #include "engram_device.h"
 #include "engram_launch.h"
+
+#include <utility>
 
 namespace engram {
 namespace {
 
 constexpr int kChunk = 64;
-constexpr int kWalkThreads = 256;
-constexpr int kPad = 16;  // 32 bytes: rows 8 banks apart for 16-byte and for transposing reads
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -49,6 +49,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef __attribute__((address_space(3))) const void* lds_ptr;
 
 
 __device__ __forceinline__ bf16x8 join8(u32x2 lo, u32x2 hi) {
@@ -56,30 +57,89 @@ __device__ __forceinline__ bf16x8 join8(u32x2 lo, u32x2 hi) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+// A tile in LDS: rows of kD (64 or 128) values without gaps, the 16-byte pieces
+// of row r in the order piece ^ turn(r).  LDS serves sixteen lanes of a 16-byte
+// read at once (rows 0-3 and 12-15 of one piece with rows 4-11 of the next, or
+// the other way round) and thirty-two of an 8-byte or transposing one (sixteen
+// rows of one piece; or rows 0-3 of two eights in different halves of 16); with
+// this order the lanes of each kind find their values in different banks.
+template <int kD>
+__device__ __forceinline__ uint32_t turn(uint32_t row) {
+  const uint32_t b2 = row >> 2 & 1, b3 = row >> 3 & 1, b4 = row >> 4 & 1;
+  return kD == 128 ? (b4 ^ b3 ^ b2) << 3 | (row & 3) << 1 | b3 : (b4 ^ b3 ^ b2) << 2 | (row & 2) | b3;
+}
+// Value `col` of row `row`; the reads below take 4 or 8 values from a multiple of that.
+template <int kD>
+__device__ __forceinline__ uint32_t place(uint32_t row, uint32_t col) {
+  return row * kD + ((col >> 3) ^ turn<kD>(row)) * 8 + (col & 7);
+}
+
 // Operand fragments of the 16x16x32 product: lane l holds row (or column)
 // l % 16 and, with g = l / 16, the eight contraction indices 8g .. 8g+7.
 // Here the row is a row of the tile.
-template <int kStride>
-__device__ __forceinline__ bf16x8 frag_rows(const uint16_t* tile, int row0, int k0, int lane) {
-  return __builtin_bit_cast(bf16x8, load16(tile + (row0 + lane % 16) * kStride + k0 + 8 * (lane / 16)));
+template <int kD>
+__device__ __forceinline__ bf16x8 frag_rows(const uint16_t* tile, uint32_t row0, uint32_t k0, uint32_t lane) {
+  return __builtin_bit_cast(bf16x8, load16(tile + place<kD>(row0 + lane % 16, k0 + 8 * (lane / 16))));
 }
-// The same, with the contraction indices in the order of an accumulator's
-// rows: 4g .. 4g+3 of the first sixteen, then of the second.
-template <int kStride>
-__device__ __forceinline__ bf16x8 frag_rows_acc_order(const uint16_t* tile, int row0, int k0, int lane) {
-  const uint16_t* p = tile + (row0 + lane % 16) * kStride + k0 + 4 * (lane / 16);
-  return join8(*reinterpret_cast<const u32x2*>(p), *reinterpret_cast<const u32x2*>(p + 16));
-}
+// The reads of the next two kinds differ from each other by a piece and by rows
+// that are constants: kD / 16 bases a lane serve all of them.
+//
+// The same rows, with the contraction indices in the order of an accumulator's
+// rows: 4g .. 4g+3 of the first sixteen, then of the second.  Base j: row
+// l % 16, values 16 j + 4 g; sixteen rows further on, bit 4 of the row turns
+// the pieces by half of them.
+template <int kD>
+struct AccOrder {
+  uint32_t at[kD / 16];
+  __device__ __forceinline__ explicit AccOrder(uint32_t lane) {
+    const uint32_t l = lane % 16, g = lane / 16, first = place<kD>(l, 4 * g);
+#pragma unroll
+    for (int j = 0; j < kD / 16; ++j) at[j] = first ^ 16 * j;
+  }
+  template <int kTt, int kKk>
+  __device__ __forceinline__ bf16x8 frag(const uint16_t* tile) const {
+    constexpr int kHalf = kTt & 1 ? kD / 32 : 0;
+    return join8(*reinterpret_cast<const u32x2*>(tile + at[(2 * kKk) ^ kHalf] + 16 * kTt * kD),
+                 *reinterpret_cast<const u32x2*>(tile + at[(2 * kKk + 1) ^ kHalf] + 16 * kTt * kD));
+  }
+};
 // Here the row is a column of the tile and the contraction runs down the
 // tile's rows, read through the transposing LDS load: the sixteen lanes of a
-// group name four rows of sixteen values and get a column of four each.
-template <int kStride>
-__device__ __forceinline__ bf16x8 frag_cols(const uint16_t* tile, int k0, int col0, int lane) {
-  const int l = lane % 16;
-  const uint16_t* p = tile + (k0 + 8 * (lane / 16) + l / 4) * kStride + col0 + 4 * (l % 4);
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * kStride));
-  return join8(__builtin_bit_cast(u32x2, lo), __builtin_bit_cast(u32x2, hi));
+// group name four rows of sixteen values and get a column of four each.  Base
+// j: row 8 g + l / 4, values 16 j + 4 (l % 4); four rows further on, bit 2 of
+// the row turns the pieces by half of them.
+template <int kD>
+struct Columns {
+  uint32_t at[kD / 16];
+  __device__ __forceinline__ explicit Columns(uint32_t lane) {
+    const uint32_t l = lane % 16, first = place<kD>(8 * (lane / 16) + l / 4, 4 * (l % 4));
+#pragma unroll
+    for (int j = 0; j < kD / 16; ++j) at[j] = first ^ 16 * j;
+  }
+  template <int kKt, int kDt>
+  __device__ __forceinline__ bf16x8 frag(const uint16_t* tile) const {
+    return two(tile + at[kDt] + 32 * kKt * kD, tile + at[kDt ^ (kD / 32)] + (32 * kKt + 4) * kD);
+  }
+  static __device__ __forceinline__ bf16x8 two(const uint16_t* x, const uint16_t* y) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)x);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)y);
+    return join8(__builtin_bit_cast(u32x2, lo), __builtin_bit_cast(u32x2, hi));
+  }
+};
+// The same for one sixteen columns of a wave's own.
+template <int kD>
+__device__ __forceinline__ bf16x8 frag_cols(const uint16_t* tile, uint32_t k0, uint32_t col0, uint32_t lane) {
+  const uint32_t l = lane % 16, row = k0 + 8 * (lane / 16) + l / 4, col = col0 + 4 * (l % 4);
+  return Columns<kD>::two(tile + place<kD>(row, col), tile + place<kD>(row + 4, col));
+}
+
+template <int... kI, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, kI...>, F f) {
+  (f(std::integral_constant<int, kI>{}), ...);
+}
+template <int kN, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  unrolled(std::make_integer_sequence<int, kN>{}, f);
 }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -91,17 +151,23 @@ __device__ __forceinline__ u32x2 pack4(f32x4 v) {
   return r;
 }
 
-// lam^steps for steps >= 0 (lam^0 is 1 also where lam is 0).
-__device__ __forceinline__ float decay_power(float log_decay, int steps) {
-  return steps == 0 ? 1.0f : expf(log_decay * (float)steps);
+// lam^steps for steps >= 0, from the logarithm of lam to base 2 (lam^0 is 1
+// also where lam is 0).
+__device__ __forceinline__ float decay_power(float log2_decay, int steps) {
+  return steps == 0 ? 1.0f : __builtin_amdgcn_exp2f(log2_decay * (float)steps);
 }
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
 // The lane's number as a value the compiler knows nothing of: what is computed
 // from it stays where it is used, instead of moving out of loops and being
 // spilled.
-__device__ __forceinline__ int afresh(int lane) {
+__device__ __forceinline__ uint32_t afresh(uint32_t lane) {
   asm volatile("" : "+v"(lane));
-  return lane;
+  return lane & 63;
+}
+__device__ __forceinline__ float afresh(float v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
 // A value that all lanes share, in a scalar register.
@@ -112,9 +178,6 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | lo);
 }
 
-// Memory through a buffer descriptor: a base that all lanes share and a 32-bit
-// offset each; loads from kBeyond give zero and stores to it are dropped.
-constexpr uint32_t kBeyond = 0xf0000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0x80000000u, 0x00020000);
 }
@@ -172,290 +235,316 @@ struct Sequences {
 // state of the segment's last, unfinished sequence in the next segment's carry.
 template <int kDa, int kDc, bool kStateOnly>
 struct Walk {
-  static constexpr int kSa = kDa + kPad, kSc = kDc + kPad, kSp = kChunk + kPad;
+  static constexpr int kWaves = kDc / 16;         // a wave for every sixteen columns of X
+  static constexpr int kThreads = kWaves * 64;
   static constexpr int kDt = kDa / 16;            // tiles of state rows
-  static constexpr int kNt = kDc / 64;            // tiles of state columns in a wave
-  static constexpr int kVa = kDa * kChunk / 8 / kWalkThreads;  // 16-byte vectors a thread stages of a (and of b)
-  static constexpr int kVc = kDc * kChunk / 8 / kWalkThreads;
+  static constexpr int kSt = 16 / kWaves;         // of the scores' sixteen tiles, those a wave makes
 
+  // b's tile is there twice, as its last reads come at a chunk's end; a's and
+  // c's are read out before, and filled again behind that (the state alone is
+  // one pass over b and c, and has both twice).
   struct Lds {
-    alignas(16) uint16_t a[kStateOnly ? 1 : kChunk * kSa];
-    alignas(16) uint16_t b[kChunk * kSa];
-    alignas(16) uint16_t c[kChunk * kSc];
-    alignas(16) uint16_t p[kStateOnly ? 1 : kChunk * kSp];
+    alignas(16) uint16_t a[kStateOnly ? 8 : kChunk * kDa];
+    alignas(16) uint16_t b[2][kChunk * kDa];
+    alignas(16) uint16_t c[kStateOnly ? 2 : 1][kChunk * kDc];
+    alignas(16) uint16_t p[kStateOnly ? 8 : kChunk * kChunk];
     int bad[2];
   };
 
-  // Rows pos .. pos + L - 1 of the head, the rest zero.
-  template <int kV, int kD>
-  static __device__ __forceinline__ void fetch(u32x4 (&r)[kV], const uint16_t* x, int64_t ld, int head, int d,
-                                               int64_t pos, int L, const WalkArgs& w, int tid) {
-    const __amdgpu_buffer_rsrc_t src = buffer_of(x + (w.turned ? w.N - pos - L : pos) * ld + (int64_t)head * d);
-    const int row = tid / (kD / 8), col = tid % (kD / 8) * 8;
-    constexpr int kRows = kWalkThreads / (kD / 8);
-    const uint32_t line = (uint32_t)ld * 2;
+  // Rows pos .. pos + L - 1 of the head, straight into LDS as the tile's last L
+  // rows, the rows before them zero.
+  template <int kD>
+  static __device__ __forceinline__ void fetch(const uint16_t* tile, const uint16_t* x, int64_t ld, int head, int d,
+                                               int64_t pos, int L, const WalkArgs& w, uint32_t wave, uint32_t lane) {
+    const u32x4 src = buffer_words(x + (w.turned ? w.N - pos - L : pos) * ld + (int64_t)head * d);
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile, line = (uint32_t)ld * 2;
+    // a lane's rows are kRows apart, a multiple of 32 or of 16, with which the order of the pieces
+    // does not (or, at 16, by half of them) change
+    constexpr uint32_t kLoads = kD * kChunk / 8 / kThreads, kRows = kThreads / (kD / 8);
+    const uint32_t t0 = (wave * 64 + lane) / (kD / 8), piece = (wave * 64 + lane) % (kD / 8) ^ turn<kD>(t0);
+    const uint32_t first = token_of(t0, L, w) * line, step = w.turned ? 0 - kRows * line : kRows * line;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int t = row + i * kRows;
-      const uint32_t off = (uint32_t)(w.turned ? L - 1 - t : t) * line + (uint32_t)col * 2;
-      r[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (int)(t < L && col < d ? off : kBeyond), 0, 0);
+    for (uint32_t q = 0; q < kLoads; ++q) {
+      const uint32_t col = (piece ^ turn<kD>(q * kRows)) * 8;
+      const bool in = (t0 + q * kRows >= kChunk - (uint32_t)L) & (col < (uint32_t)d);
+      load_to_lds(to + (q * kWaves + wave) * 1024, src, in ? first + q * step + col * 2 : kBeyond);
     }
   }
-  template <int kV, int kD, int kStride>
-  static __device__ __forceinline__ void put(uint16_t* tile, const u32x4 (&r)[kV], int tid) {
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      constexpr int kRows = kWalkThreads / (kD / 8);
-      store16(tile + (tid / (kD / 8) + i * kRows) * kStride + tid % (kD / 8) * 8, r[i]);
-    }
+  // The token of a tile's row t, from the chunk's first token in memory.
+  static __device__ __forceinline__ uint32_t token_of(uint32_t t, int L, const WalkArgs& w) {
+    return w.turned ? kChunk - 1 - t : t - (uint32_t)(kChunk - L);
   }
-  template <int kV>
-  static __device__ __forceinline__ bool not_finite(const u32x4 (&r)[kV]) {
-    bool bad = false;
+  static __device__ __forceinline__ bool not_finite(const bf16x8 (&c)[2]) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 most = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
+    for (int i = 0; i < 2; ++i) {
+      const u32x4 r = __builtin_bit_cast(u32x4, c[i]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        bad |= (r[i][k] & 0x7f80u) == 0x7f80u || (r[i][k] & 0x7f800000u) == 0x7f800000u;
-    return bad;
+      for (int k = 0; k < 4; ++k) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, r[k] & 0x7fff7fffu));
+    }
+    return (most[0] >= 0x7f80) | (most[1] >= 0x7f80);
+  }
+  // This wave's loads into LDS (and all else) are done; then all waves'.
+  static __device__ __forceinline__ void meet() {
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __syncthreads();
   }
 
-  // X as accumulators: tile (dt, nt) of a wave holds rows 16 dt + 4 g + r and
-  // column 16 (wave kNt + nt) + lane % 16.
-  typedef f32x4 State[kDt][kNt];
+  // X as accumulators: tile dt of a wave holds rows 16 dt + 4 g + r and column
+  // 16 wave + lane % 16.
+  typedef f32x4 State[kDt];
 
   // kOut: X to p, else p to X (zero where p is null).
   template <bool kOut, bool kTransposed>
-  static __device__ __forceinline__ void move_state(State& X, const float* p, const WalkArgs& w, int wave, int lane0) {
-    const int lane = afresh(lane0);
+  static __device__ __forceinline__ void move_state(State& X, const float* p, const WalkArgs& w, uint32_t wave, uint32_t lane0) {
+    const uint32_t lane = afresh(lane0);
     const __amdgpu_buffer_rsrc_t at = buffer_of(p);
-    const int d = 4 * (lane / 16);
+    const uint32_t Da = w.Da, Dc = w.Dc, d = 4 * (lane / 16), n = 16 * wave + lane % 16;
+    const uint32_t first = p && n < Dc ? 4 * (kTransposed ? n * Da + d : d * Dc + n) : kBeyond;
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) {
-      const int n = 16 * (wave * kNt + nt) + lane % 16;
-      const uint32_t first = p && n < w.Dc ? 4u * (uint32_t)(kTransposed ? n * w.Da + d : d * w.Dc + n) : kBeyond;
+    for (int dt = 0; dt < kDt; ++dt) {
+      const int off = (int)(16 * dt + d < Da ? first : kBeyond);
+      if constexpr (kTransposed && kOut) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, X[dt]), at, off, 64 * dt, 0);
+      } else if constexpr (kTransposed) {
+        X[dt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(at, off, 64 * dt, 0));
+      } else {
 #pragma unroll
-      for (int dt = 0; dt < kDt; ++dt) {
-        const int off = (int)(16 * dt + d < w.Da ? first : kBeyond);
-        if constexpr (kTransposed && kOut) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, X[dt][nt]), at, off, 64 * dt, 0);
-        } else if constexpr (kTransposed) {
-          X[dt][nt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(at, off, 64 * dt, 0));
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int line = 4 * (16 * dt + r) * w.Dc;
-            if constexpr (kOut) {
-              const float v = X[dt][nt][r];
-              __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), at, off, line, 0);
-            } else {
-              X[dt][nt][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(at, off, line, 0));
-            }
+        for (int r = 0; r < 4; ++r) {
+          const int line = 4 * (16 * dt + r) * w.Dc;
+          if constexpr (kOut) {
+            const float v = X[dt][r];
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), at, off, line, 0);
+          } else {
+            X[dt][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(at, off, line, 0));
           }
         }
       }
     }
   }
-  static __device__ __forceinline__ void load_state(State& X, const float* p, bool transposed, const WalkArgs& w, int wave,
-                                                    int lane) {
+  static __device__ __forceinline__ void load_state(State& X, const float* p, bool transposed, const WalkArgs& w, uint32_t wave,
+                                                    uint32_t lane) {
     if (transposed) move_state<false, true>(X, p, w, wave, lane);
     else move_state<false, false>(X, p, w, wave, lane);
   }
-  static __device__ __forceinline__ void store_state(State& X, float* p, bool transposed, const WalkArgs& w, int wave,
-                                                     int lane) {
+  static __device__ __forceinline__ void store_state(State& X, float* p, bool transposed, const WalkArgs& w, uint32_t wave,
+                                                     uint32_t lane) {
     if (transposed) move_state<true, true>(X, p, w, wave, lane);
     else move_state<true, false>(X, p, w, wave, lane);
   }
 
   // The powers of the decay that a lane needs, as products of a factor of its
-  // own and one that all lanes share: scores lam^(t-s) with t = 16 wave + l and
-  // s = 16 st + 4 g + r, the carried state lam^(t+e) with t = 16 tt + l, and the
-  // rows of a full chunk lam^(64-e-s) with s = 32 kt + 8 g + i.
+  // own and one that all lanes share: scores lam^(t-s) with t = 16 tile + l and
+  // s = 16 st + 4 g + r, and the rows that go into X, lam^(64-e-s) with
+  // s = 32 kt + 8 g + i.  A chunk of fewer rows is the tile's last ones, so these
+  // do not depend on its length.
   struct Powers {
-    float diagonal[4];   // s_intra lam^(l-4g-r), 0 above the diagonal
-    float below[4];      // s_intra lam^(16+l-4g-r)
+    float below;         // s_intra lam^(13+l-4g), times lam^(3-r)
     float tiles[3];      // lam^(16 i)
-    float in;            // s_inter lam^(l+e)
     float rows[2];       // s_upd lam^(57-e-32kt-8g)
     float eight[8];      // lam^i
-    __device__ __forceinline__ void set(float ld, const WalkArgs& w, int lane) {
-      const int g = lane / 16, l = lane % 16;
-      for (int r = 0; r < 4; ++r) {
-        const int steps = l - 4 * g - r;
-        diagonal[r] = steps >= 0 ? w.s_intra * decay_power(ld, steps) : 0.0f;
-        below[r] = w.s_intra * decay_power(ld, 16 + steps);
-      }
+    float less_one;      // lam^64 - 1
+    __device__ __forceinline__ void set(float ld, const WalkArgs& w, uint32_t lane0) {
+      const int lane = (int)lane0, g = lane / 16, l = lane % 16;
+      below = w.s_intra * decay_power(ld, 13 + l - 4 * g);
       for (int i = 0; i < 3; ++i) tiles[i] = uniform(decay_power(ld, 16 * i));
-      in = w.s_inter * decay_power(ld, l + w.e);
       for (int kt = 0; kt < 2; ++kt) rows[kt] = w.s_upd * decay_power(ld, kChunk - 7 - w.e - 32 * kt - 8 * g);
       for (int i = 0; i < 8; ++i) eight[i] = uniform(decay_power(ld, i));
+      less_one = uniform(expm1f(ld * (kLn2 * (float)kChunk)));
     }
   };
 
+  // Eight values of c times their powers of the decay, each as three bf16
+  // values: the upper eight bits of what is left, three times.  kInf: they may
+  // be infinite, and then have no further parts.
+  template <bool kInf>
+  static __device__ __forceinline__ void split(bf16x8 (&to)[3], bf16x8 c, float up, const Powers& pw) {
+    const u32x4 raw = __builtin_bit_cast(u32x4, c);
+    u32x4 part[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x0 = bf_lo(raw[i]) * (up * pw.eight[7 - 2 * i]), x1 = bf_hi(raw[i]) * (up * pw.eight[6 - 2 * i]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        part[k][i] = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
+        if (k == 2) break;
+        x0 -= __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
+        x1 -= __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
+        if (kInf) {
+          x0 = x0 == x0 ? x0 : 0.0f;
+          x1 = x1 == x1 ? x1 : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) to[k] = __builtin_bit_cast(bf16x8, part[k]);
+  }
+
   // Walk the rows [pos, stop) of one sequence, chunk by chunk.
   static __device__ __forceinline__ void rows(Lds& lds, State& X, int64_t pos, int64_t stop, int head, const float ld,
-                                              const Powers& pw, int& parity, const WalkArgs& w, int wave, int lane0) {
-    u32x4 ra[kStateOnly ? 1 : kVa], rb[kVa], rc[kVc];
+                                              const Powers& pw, int& parity, const WalkArgs& w, uint32_t wave, uint32_t lane0) {
     int64_t single = pos;  // rows before this one are walked one at a time
-    int L = (int)(stop - pos < kChunk ? stop - pos : kChunk);
-    auto get = [&](int64_t at, int n, int tid) {
-      if constexpr (!kStateOnly) fetch<kVa, kDa>(ra, w.a, w.lda, head, w.Da, at, n, w, tid);
-      fetch<kVa, kDa>(rb, w.b, w.ldb, head, w.Da, at, n, w, tid);
-      fetch<kVc, kDc>(rc, w.c, w.ldc, head, w.Dc, at, n, w, tid);
+    int L = (int)(stop - pos < kChunk ? stop - pos : kChunk), at_b = 0;
+    auto get_b = [&](int to, int64_t at, int n, uint32_t lane) {
+      fetch<kDa>(lds.b[to], w.b, w.ldb, head, w.Da, at, n, w, wave, lane);
     };
-    get(pos, L, threadIdx.x);
+    auto get_c = [&](int to, int64_t at, int n, uint32_t lane) {
+      fetch<kDc>(lds.c[to], w.c, w.ldc, head, w.Dc, at, n, w, wave, lane);
+    };
+    auto get_a = [&](int64_t at, int n, uint32_t lane) { fetch<kDa>(lds.a, w.a, w.lda, head, w.Da, at, n, w, wave, lane); };
+    get_b(0, pos, L, lane0);
+    get_c(0, pos, L, lane0);
+    if constexpr (!kStateOnly) get_a(pos, L, lane0);
     while (pos < stop) {
-      const int lane = afresh(lane0);
-      const int g = lane / 16, l = lane % 16, tid = wave * 64 + lane;
-      if constexpr (!kStateOnly) put<kVa, kDa, kSa>(lds.a, ra, tid);
-      put<kVa, kDa, kSa>(lds.b, rb, tid);
-      put<kVc, kDc, kSc>(lds.c, rc, tid);
-      if (not_finite<kVc>(rc)) lds.bad[parity] = 1;
-      __syncthreads();
-      // An infinity or NaN in a row of c would reach the rows before it too, as
-      // 0 * c in the product with the scores: such a chunk is walked row by row.
-      const bool bad = lds.bad[parity] != 0;
-      if (bad && L > 1) {
-        single = pos + L;
-        L = 1;
-        get(pos, L, tid);
-        parity ^= 1;
-        if (threadIdx.x == 0) lds.bad[parity] = 0;
-        __syncthreads();
-        continue;
-      }
-      if (threadIdx.x == 0) lds.bad[parity ^ 1] = 0;
+      const uint32_t lane = afresh(lane0), g = lane / 16, l = lane % 16;
       const int64_t next = pos + L;
       const int next_L = next < single ? 1 : (int)(stop - next < kChunk ? stop - next : kChunk);
-      if (next < stop) get(next, next_L, tid);
-
-      bf16x8 cf[2][kNt];
+      meet();
+      if constexpr (kStateOnly) {
+        if (next < stop) {
+          get_b(at_b ^ 1, next, next_L, lane);
+          get_c(at_b ^ 1, next, next_L, lane);
+        }
+      }
+      const uint16_t *tb = lds.b[at_b], *tc = lds.c[kStateOnly ? at_b : 0];
+      bf16x8 cf[2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) cf[kt] = frag_cols<kDc>(tc, 32 * kt, 16 * wave, lane);
       if constexpr (!kStateOnly) {
-        // scores of the wave's sixteen rows t, transposed: the lane has t = 16 wave + l and four neighbouring s
+        // scores, transposed: the lane has row t = 16 tile + l and four neighbouring s; with eight
+        // waves two share the rows of a tile
+        const uint32_t tile = wave & 3, st0 = wave / 4 * kSt;
         bf16x8 at[kDa / 32];
 #pragma unroll
-        for (int kk = 0; kk < kDa / 32; ++kk) at[kk] = frag_rows<kSa>(lds.a, 16 * wave, 32 * kk, lane);
+        for (int kk = 0; kk < kDa / 32; ++kk) at[kk] = frag_rows<kDa>(lds.a, 16 * tile, 32 * kk, lane);
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
+        for (int i = 0; i < kSt; ++i) {
+          const uint32_t st = st0 + i;
           u32x2 packed = {0, 0};
-          if (st <= wave) {
+          if (st <= tile) {
             f32x4 s = {0, 0, 0, 0};
-            const float between = wave - st <= 1 ? 1.0f : wave - st == 2 ? pw.tiles[1] : pw.tiles[2];
+            bf16x8 bt[kDa / 32];
 #pragma unroll
-            for (int kk = 0; kk < kDa / 32; ++kk) s = mfma(frag_rows<kSa>(lds.b, 16 * st, 32 * kk, lane), at[kk], s);
+            for (int kk = 0; kk < kDa / 32; ++kk) bt[kk] = frag_rows<kDa>(tb, 16 * st, 32 * kk, lane);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if (st == wave) s[r] = 4 * g + r <= l ? s[r] * pw.diagonal[r] : 0.0f;
-              else s[r] *= pw.below[r] * between;
+            for (int kk = 0; kk < kDa / 32; ++kk) s = mfma(bt[kk], at[kk], s);
+            if (st == tile) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int steps = (int)l - (int)(4 * g + r);
+                s[r] = steps >= 0 ? s[r] * (w.s_intra * decay_power(ld, steps)) : 0.0f;
+              }
+            } else {
+              const float between = pw.below * (tile - st == 1 ? 1.0f : tile - st == 2 ? pw.tiles[1] : pw.tiles[2]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[r] *= between * pw.eight[3 - r];
             }
             packed = pack4(s);
           }
-          *reinterpret_cast<u32x2*>(lds.p + (16 * wave + l) * kSp + 16 * st + 4 * g) = packed;
+          *reinterpret_cast<u32x2*>(lds.p + place<kChunk>(16 * tile + l, 16 * st + 4 * g)) = packed;
         }
       }
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) cf[kt][nt] = frag_cols<kSc>(lds.c, 32 * kt, 16 * (wave * kNt + nt), lane);
       if constexpr (!kStateOnly) {
-        bf16x8 xf[kDa / 32][kNt];
+        // An infinity or NaN in a row of c would reach the rows before it too, as
+        // 0 * c in the product with the scores: such a chunk is walked row by row.
+        if (not_finite(cf)) lds.bad[parity] = 1;
+        __syncthreads();  // the scores of all waves, and their word on c
+        const bool bad = __builtin_amdgcn_readfirstlane(lds.bad[parity]) != 0;
+        parity ^= 1;
+        if (threadIdx.x == 0) lds.bad[parity] = 0;
+        if (bad && L > 1) {
+          single = next;
+          L = 1;
+          get_b(at_b, pos, 1, lane);
+          get_c(0, pos, 1, lane);
+          get_a(pos, 1, lane);
+          continue;
+        }
+        if (next < stop) get_b(at_b ^ 1, next, next_L, lane);
+        // y^T = X^T a^T, then += c^T scores^T: the lane has row t = 16 tt + l and four neighbouring columns
+        f32x4 y[4];
 #pragma unroll
-        for (int kk = 0; kk < kDa / 32; ++kk)
+        for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0, 0, 0, 0};
+        const AccOrder<kDa> as(lane);
+        unrolled<kDa / 32>([&](auto kk) {
+          constexpr int kKk = decltype(kk)::value;
+          __builtin_amdgcn_sched_barrier(0);
+          const bf16x8 xf = join8(pack4(X[2 * kKk]), pack4(X[2 * kKk + 1]));
+          bf16x8 af[4];
+          unrolled<4>([&](auto tt) {
+            constexpr int kTt = decltype(tt)::value;
+            // without this the compiler joins the reads of tt and tt + 2, whose results then need moving
+            if constexpr (kTt == 2) asm volatile("" ::: "memory");
+            af[kTt] = as.template frag<kTt, kKk>(lds.a);
+          });
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) xf[kk][nt] = join8(pack4(X[2 * kk][nt]), pack4(X[2 * kk + 1][nt]));
+          for (int tt = 0; tt < 4; ++tt) y[tt] = mfma(xf, af[tt], y[tt]);
+        });
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) y[tt] *= w.s_inter * decay_power(ld, max((int)(16 * tt + l) - (kChunk - L) + w.e, 0));
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int tt = 2 * kt; tt < 4; ++tt) y[tt] = mfma(cf[kt], frag_rows<kChunk>(lds.p, 16 * tt, 32 * kt, lane), y[tt]);
         const __amdgpu_buffer_rsrc_t dst =
             buffer_of(w.y + (w.turned ? w.N - pos - L : pos) * w.ldy + (int64_t)head * w.Dc);
-        __syncthreads();  // the scores of all waves
+        const uint32_t n = 16 * wave + 4 * g, line = (uint32_t)w.ldy * 2;
+        const uint32_t first = token_of(l, L, w) * line + 2 * n;
+        const bool in = n < (uint32_t)w.Dc;
+        const uint32_t step = w.turned ? 0 - 16 * line : 16 * line;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          __builtin_amdgcn_sched_barrier(0);
-          f32x4 y[kNt];
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) y[nt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int kk = 0; kk < kDa / 32; ++kk) {
-            const bf16x8 af = frag_rows_acc_order<kSa>(lds.a, 16 * tt, 32 * kk, lane);
-#pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) y[nt] = mfma(xf[kk][nt], af, y[nt]);
-          }
-          const float in = pw.in * (tt < 3 ? pw.tiles[tt] : pw.tiles[1] * pw.tiles[2]);
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) y[nt] *= in;
-#pragma unroll
-          for (int kt = 0; kt <= tt / 2; ++kt) {
-            const bf16x8 sf = frag_rows<kSp>(lds.p, 16 * tt, 32 * kt, lane);
-#pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) y[nt] = mfma(cf[kt][nt], sf, y[nt]);
-          }
-          const int t = 16 * tt + l;
-          const uint32_t line = (uint32_t)(w.turned ? L - 1 - t : t) * (uint32_t)w.ldy * 2;
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            const int n = 16 * (wave * kNt + nt) + 4 * g;
-            __builtin_amdgcn_raw_buffer_store_b64(pack4(y[nt]), dst, (int)(t < L && n < w.Dc ? line + 2 * n : kBeyond), 0, 0);
-          }
+        for (int tt = 0; tt < 4; ++tt)
+          __builtin_amdgcn_raw_buffer_store_b64(
+              pack4(y[tt]), dst, (int)(((16 * tt + l >= kChunk - (uint32_t)L) & in) ? first + tt * step : kBeyond), 0, 0);
+      }
+      if constexpr (!kStateOnly) {
+        __syncthreads();  // a and c are read out
+        if (next < stop) {
+          get_c(0, next, next_L, lane);
+          get_a(next, next_L, lane);
         }
       }
       // X = lam^L X + s_upd sum_s lam^(L-e-s) b_s c_s^T
-      __builtin_amdgcn_sched_barrier(0);
-      const float less_one = uniform(expm1f(ld * (float)L));
-      float up[2][8];
+      const float less_one = L == kChunk ? pw.less_one : uniform(expm1f(ld * (kLn2 * (float)L)));
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+      for (int dt = 0; dt < kDt; ++dt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int s = 32 * kt + 8 * g + i;
-          if (L == kChunk) up[kt][i] = pw.rows[kt] * pw.eight[7 - i];
-          else up[kt][i] = s < L ? w.s_upd * decay_power(ld, L - w.e - s) : 0.0f;
-        }
-      bf16x8 hi[2][kNt], lo[2][kNt];
+        for (int r = 0; r < 4; ++r) X[dt][r] = fmaf(X[dt][r], less_one, X[dt][r]);
+      const Columns<kDa> bs(lane);
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+      for (int kt = 0; kt < 2; ++kt) {
+        bf16x8 cs[3];
+        const float up = afresh(pw.rows[kt]);
+        if (kStateOnly || L == 1) split<true>(cs, cf[kt], up, pw);
+        else split<false>(cs, cf[kt], up, pw);
+        unrolled<kDt / 4>([&](auto quarter) {
+          constexpr int kD0 = 4 * decltype(quarter)::value;
+          __builtin_amdgcn_sched_barrier(0);
+          bf16x8 bf[4];
+          unrolled<4>([&](auto i) {
+            constexpr int kI = decltype(i)::value;
+            bf[kI] = kt == 0 ? bs.template frag<0, kD0 + kI>(tb) : bs.template frag<1, kD0 + kI>(tb);
+          });
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          const u32x4 raw = __builtin_bit_cast(u32x4, cf[kt][nt]);
-          u32x4 h, q;
+          for (int k = 0; k < 3; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x0 = bf_lo(raw[i]) * up[kt][2 * i], x1 = bf_hi(raw[i]) * up[kt][2 * i + 1];
-            h[i] = pack_bf16x2(x0, x1);
-            const float h0 = bf_lo(h[i]), h1 = bf_hi(h[i]);
-            // an infinite value has no second part
-            q[i] = pack_bf16x2(x0 == h0 ? 0.0f : x0 - h0, x1 == h1 ? 0.0f : x1 - h1);
-          }
-          hi[kt][nt] = __builtin_bit_cast(bf16x8, h);
-          lo[kt][nt] = __builtin_bit_cast(bf16x8, q);
-        }
-#pragma unroll
-      for (int dt = 0; dt < kDt; ++dt) {
-        if (dt % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) X[dt][nt][r] = fmaf(X[dt][nt][r], less_one, X[dt][nt][r]);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const bf16x8 bf = frag_cols<kSa>(lds.b, 32 * kt, 16 * dt, lane);
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            X[dt][nt] = mfma(bf, hi[kt][nt], X[dt][nt]);
-            X[dt][nt] = mfma(bf, lo[kt][nt], X[dt][nt]);
-          }
-        }
+            for (int i = 0; i < 4; ++i) X[kD0 + i] = mfma(bf[i], cs[k], X[kD0 + i]);
+        });
       }
-      parity ^= 1;
+      at_b ^= 1;
       pos = next;
       L = next_L;
-      __syncthreads();  // the tiles are read out
     }
+    __syncthreads();  // the tiles are read out
   }
 
   static __device__ __forceinline__ void run(const WalkArgs& w) {
     __shared__ __attribute__((aligned(16))) Lds lds;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.x % w.H;
     const int64_t seg = blockIdx.x / w.H;
-    const float ld = uniform(w.log_decay[head]);
+    const float ld = uniform(w.log_decay[head]) * kLog2e;  // to base 2
     const Sequences seqs{w.cu, w.N, w.B, w.turned};
     const int64_t from = seg * w.seg, to = from + w.seg < w.N ? from + w.seg : w.N;
     const size_t state = (size_t)w.Da * w.Dc;
@@ -490,7 +579,7 @@ struct Walk {
 };
 
 template <int kDa, int kDc, bool kStateOnly>
-__global__ __launch_bounds__(kWalkThreads, 2) void decay_walk_kernel(WalkArgs w) {
+__global__ __launch_bounds__(kDc * 4, kDc / 32) void decay_walk_kernel(WalkArgs w) {
   Walk<kDa, kDc, kStateOnly>::run(w);
 }
 
@@ -626,19 +715,28 @@ __global__ __launch_bounds__(kStepThreads) void decay_step_kernel(const uint16_t
   }
 }
 
+struct WalkKernel {
+  const void* kernel;
+  int threads;
+};
+template <int kDa, int kDc, bool kStateOnly>
+WalkKernel walk_of() {
+  return {(const void*)&decay_walk_kernel<kDa, kDc, kStateOnly>, Walk<kDa, kDc, kStateOnly>::kThreads};
+}
 template <bool kStateOnly>
-const void* walk_kernel(int Da, int Dc) {
-  if (Da <= 64)
-    return Dc <= 64 ? (const void*)&decay_walk_kernel<64, 64, kStateOnly> : (const void*)&decay_walk_kernel<64, 128, kStateOnly>;
-  return Dc <= 64 ? (const void*)&decay_walk_kernel<128, 64, kStateOnly> : (const void*)&decay_walk_kernel<128, 128, kStateOnly>;
+WalkKernel walk_kernel(int Da, int Dc) {
+  if (Da <= 64) return Dc <= 64 ? walk_of<64, 64, kStateOnly>() : walk_of<64, 128, kStateOnly>();
+  return Dc <= 64 ? walk_of<128, 64, kStateOnly>() : walk_of<128, 128, kStateOnly>();
 }
 
 int64_t segments(int64_t N, int64_t seg) { return (N + seg - 1) / seg; }
 
-hipError_t launch_state_pass(WalkArgs w, hipStream_t stream) {
+template <bool kStateOnly>
+hipError_t launch_walk(WalkArgs w, hipStream_t stream) {
+  const WalkKernel k = walk_kernel<kStateOnly>(w.Da, w.Dc);
+  const int64_t n = segments(w.N, w.seg) - (kStateOnly ? 1 : 0);  // the last segment leaves no state to another
   void* args[] = {&w};
-  return hipLaunchKernel(walk_kernel<true>(w.Da, w.Dc), dim3((unsigned)((segments(w.N, w.seg) - 1) * w.H)),
-                         dim3(kWalkThreads), args, 0, stream);
+  return hipLaunchKernel(k.kernel, dim3((unsigned)(n * w.H)), dim3((unsigned)k.threads), args, 0, stream);
 }
 hipError_t launch_join(WalkArgs w, hipStream_t stream) {
   void* args[] = {&w};
@@ -646,25 +744,21 @@ hipError_t launch_join(WalkArgs w, hipStream_t stream) {
   return hipLaunchKernel(reinterpret_cast<const void*>(&decay_join_kernel), dim3((unsigned)(w.B * w.H), parts),
                          dim3(kJoinThreads), args, 0, stream);
 }
-hipError_t launch_walk(WalkArgs w, hipStream_t stream) {
-  void* args[] = {&w};
-  return hipLaunchKernel(walk_kernel<false>(w.Da, w.Dc), dim3((unsigned)(segments(w.N, w.seg) * w.H)),
-                         dim3(kWalkThreads), args, 0, stream);
-}
 // The states of a cut axis, and the states of empty sequences.
 hipError_t launch_carries(const WalkArgs& w, hipStream_t stream) {
   hipError_t e = hipSuccess;
-  if (segments(w.N, w.seg) > 1) e = launch_state_pass(w, stream);
+  if (segments(w.N, w.seg) > 1) e = launch_walk<true>(w, stream);
   if (e == hipSuccess && (segments(w.N, w.seg) > 1 || w.state_out)) e = launch_join(w, stream);
   return e;
 }
 
 }  // namespace
 
-// Tokens of a segment: enough segments for about two workgroups a CU.
+// Tokens of a segment: as many segments as fit the chip at once (two
+// workgroups a CU), since one more would be a second round.
 int64_t decay_segment(int64_t N, int64_t H) {
-  constexpr int64_t kWant = 512;
-  const int64_t want = (kWant + H - 1) / H;  // segments
+  constexpr int64_t kPlaces = 512;
+  const int64_t want = H < kPlaces ? kPlaces / H : 1;  // segments
   int64_t seg = (N + want - 1) / want;
   seg = (seg + kChunk - 1) / kChunk * kChunk;
   return seg < 2 * kChunk ? 2 * kChunk : seg;
@@ -686,7 +780,7 @@ hipError_t launch_decay_fwd(const DecayCall& d, hipStream_t stream) {
   w.s_intra = w.s_inter = d.scale;
   w.s_upd = 1.0f;
   hipError_t e = launch_carries(w, stream);
-  return e == hipSuccess ? launch_walk(w, stream) : e;
+  return e == hipSuccess ? launch_walk<false>(w, stream) : e;
 }
 
 hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream) {
@@ -704,7 +798,7 @@ hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream) {
   w.s_intra = w.s_inter = d.scale;
   w.s_upd = 1.0f;
   hipError_t e = launch_carries(w, stream);
-  if (e == hipSuccess) e = launch_walk(w, stream);
+  if (e == hipSuccess) e = launch_walk<false>(w, stream);
   if (e != hipSuccess) return e;
   // dv: against time; this walk's last states are the gradients of state_in
   w.turned = true;
@@ -716,14 +810,14 @@ hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream) {
   w.s_inter = 1.0f;
   w.s_upd = d.scale;
   e = launch_carries(w, stream);
-  if (e == hipSuccess) e = launch_walk(w, stream);
+  if (e == hipSuccess) e = launch_walk<false>(w, stream);
   if (e != hipSuccess) return e;
   // dk: the same states, transposed
   w.a = d.v; w.b = d.grad_o; w.c = d.q; w.y = d.grad_k;
   w.lda = d.ldv; w.ldb = d.ldgo; w.ldc = d.ldq; w.ldy = d.ldgk;
   w.Da = (int)d.Dv; w.Dc = (int)d.Dk;
   w.state_out = nullptr; w.state_t = true; w.carry_t = true;
-  return launch_walk(w, stream);
+  return launch_walk<false>(w, stream);
 }
 
 hipError_t launch_decay_step(const DecayCall& d, hipStream_t stream) {

@@ -15,9 +15,8 @@
 // rounded to the operands' type where it differs from dy (an activation), as
 // it is an operand of two products; dbias is summed before that rounding.
 //
-// Few rows (decode): the weight is read once and bounds the call, so a
-// kernel of its own streams W from memory into the matrix cores without LDS,
-// 16 rows of W to a workgroup whose waves share the contraction.
+// Single tokens: the weight is read once and bounds the call; a kernel of its
+// own takes whole rows of it with plain fp32 products.
 #include "engram_device.h"
 #include "engram_launch.h"
 
@@ -166,9 +165,7 @@ __device__ __forceinline__ void load_bias(float (&v)[8], const float* bias, int6
 
 // ---------------------------------------------------------------- tiles
 
-constexpr int kBk = 64;                          // contraction values of a stage
-constexpr uint32_t kBeyond = 0xf0000000u;        // an offset outside every tile's buffer: loads give zero
-constexpr uint32_t kTileBytes = 0x80000000u;
+constexpr int kBk = 64;  // contraction values of a stage
 
 // The product's tiles: the first `whole` are made by one workgroup each, the
 // contraction of each of the others is cut into `parts`, whose sums go to
@@ -193,24 +190,13 @@ __device__ __forceinline__ void tile_origin(const GemmArgs& g, int tile, int siz
   j0 = (int64_t)(in_group / height) * size_j;
 }
 
-// 16 bytes a lane from src + off into LDS, lane l's at to + 16 l.  Written in
-// assembly because the compiler, for the builtin, waits for every load on its
-// way before a transposing LDS read (dx 1.19 ms instead of 0.9 ms at 8192^3);
-// there is no result register, and the waits are `meet` below.
-__device__ __forceinline__ void load_to_lds(uint32_t to, u32x4 src, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(to), "v"(off), "s"(src)
-               : "memory");  // m0 is reserved: the compiler itself sets it anew wherever it uses it
-}
-
 typedef __attribute__((address_space(3))) const u32x4* lds_u32x4;
 
 // One operand's stage in LDS: kRows rows of the product, 64 contraction values.
 //  contraction contiguous (kTurned false): [kRows][64], a line of memory a
 //    row, its eight 16-byte pieces in the order piece ^ swizzle(row);
 //  rows contiguous (kTurned): [64][kRows], the 64-byte pieces of line c in the
-//    order piece ^ (c & 3) and their halves changed over in every other eight
+//    order piece ^ (c & kTurns) and their halves changed over in every other eight
 //    lines.
 // Either way the lanes that LDS serves at once (sixteen of a 16-byte read: rows
 // 0-3 and 12-15 of one piece with 4-11 of the next, or the other way round;
@@ -228,6 +214,7 @@ struct Operand {
   static __device__ __forceinline__ int swizzle(int row) {
     return kPairs ? ((row >> 3) & 3) << 1 | ((row >> 1) & 1) : (row >> 1) & 7;
   }
+  static constexpr int kTurns = kRows >= 128 ? 3 : kRows / 32 - 1;  // a line has at least kTurns + 1 pieces
   static __device__ __forceinline__ int halves(int line) { return ((line >> 3) ^ (line >> 4)) & 1; }
 
   // The lane's loads of a stage: byte offsets from the stage's first value,
@@ -248,7 +235,7 @@ struct Operand {
           constexpr int kPieces = kRows / 8;
           line = at / kPieces;
           const int piece = at % kPieces;
-          first = ((piece / 4) ^ (line & 3)) * 32 + ((piece % 4) ^ 2 * halves(line)) * 8;
+          first = ((piece / 4) ^ (line & kTurns)) * 32 + ((piece % 4) ^ 2 * halves(line)) * 8;
         }
         if (q == 0) c = kTurned ? line : first;
         off[q] = (kTurned ? first : line) < rows ? (uint32_t)line * (uint32_t)(ld * 2) + (uint32_t)first * 2 : kBeyond;
@@ -256,8 +243,7 @@ struct Operand {
     }
     // Into LDS at `to`; contraction values from `left` on are zero.
     __device__ __forceinline__ void fill(uint32_t to, const uint16_t* from, int left, int wave) const {
-      const uint64_t at = reinterpret_cast<uint64_t>(from);
-      const u32x4 src = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, kTileBytes, 0x00020000u};
+      const u32x4 src = buffer_words(from);
 #pragma unroll
       for (int q = 0; q < kLoads; ++q)
         load_to_lds(to + (q * kWaves + wave) * 1024u, src, c + q * kStep < left ? off[q] : kBeyond);
@@ -281,7 +267,7 @@ struct Operand {
 #pragma unroll
         for (int n = 0; n < kPlaces; ++n) {
           const int col = row0 + n * 16 + 4 * (l % 4);
-          at[n] = lds + 2 * (c * kRows + ((col / 32) ^ (c & 3)) * 32 + (col % 32 ^ 16 * halves(c)));
+          at[n] = lds + 2 * (c * kRows + ((col / 32) ^ (c & kTurns)) * 32 + (col % 32 ^ 16 * halves(c)));
         }
       }
     }
@@ -504,65 +490,106 @@ __global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs g) {
 
 // ---------------------------------------------------------------- few rows
 
-// y for N <= 16 kXt rows of x.  A workgroup has 16 kWt rows of W; its waves
-// take every kWaves-th piece of 64 contraction values and join in LDS.
-template <typename T, int kXt, int kWt, int kWaves>
+template <typename T>
+__device__ __forceinline__ float finish1(float v, int64_t i, int64_t j, const Epilogue& e) {
+  if (e.bias) v += e.bias[j];
+  if (e.z) static_cast<uint16_t*>(e.z)[i * e.ldz + j] = (uint16_t)T::pack(v, 0.0f);
+  if (e.act != ENGRAM_ACT_NONE) v = act_of(v, e.act);
+  if (e.residual) v += T::lo(static_cast<const uint16_t*>(e.residual)[i * e.ldr + j]);
+  return v;
+}
+
+// y for N <= kN rows of x.  W is read once, a wave reading whole rows of it, 1 KB
+// side by side, kR rows at a time; the products are plain fp32 ones (at N = 1
+// a matrix product would leave fifteen of sixteen columns empty).
+constexpr int kVecThreads = 256;
+template <typename T, int kN, int kR>
+__global__ __launch_bounds__(kVecThreads) void vector_kernel(const uint16_t* x, const uint16_t* w, int64_t ldx, int N,
+                                                             int64_t K, int64_t M, Epilogue e) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = ((int64_t)blockIdx.x * (kVecThreads / 64) + wave) * kR;
+  if (m0 >= M) return;
+  float s[kN][kR];
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) s[n][r] = 0.0f;
+  // rows behind the last one read the last one again; their sums are not stored
+#pragma unroll 2
+  for (int64_t k = 8 * lane; k < K; k += 512) {
+    u32x4 fw[kR], fx[kN];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) fw[r] = load16(w + min(m0 + r, M - 1) * K + k);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) fx[n] = load16(x + min(n, N - 1) * ldx + k);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float xv[8];
+      unpack8<T>(fx[n], xv);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        float wv[8];
+        unpack8<T>(fw[r], wv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[n][r] = fmaf(xv[i], wv[i], s[n][r]);
+      }
+    }
+  }
+  // the sum of value (n, r) goes to lane n kR + r
+  float mine = 0.0f;
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const float t = read_lane(wave_sum_to_lane63(s[n][r]), 63);
+      if (lane == n * kR + r) mine = t;
+    }
+  const int n = lane / kR;
+  const int64_t m = m0 + lane % kR;
+  if (n < kN && n < N && m < M)
+    static_cast<uint16_t*>(e.y)[n * e.ldy + m] = (uint16_t)T::pack(finish1<T>(mine, n, m, e), 0.0f);
+}
+
+// y for N <= 16 rows of x and a small W.  A workgroup has 16 rows of W; its waves
+// take every kWaves-th piece of 64 contraction values, straight from memory into
+// the matrix cores, and join in LDS: one launch, where tiles would need a second
+// one to join a split contraction (13 x 5120 x 1368: 12.5 us against 15.5; at
+// 131 MB of W the tiles' whole lines win, 33 us against 39).
+template <typename T, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, const uint16_t* w, int64_t ldx, int N,
                                                            int64_t K, int64_t M, Epilogue e) {
-  __shared__ f32x4 part[kWaves][kWt][kXt][64];
+  __shared__ f32x4 part[kWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane % 16, g = lane / 16;
-  const int64_t m0 = (int64_t)blockIdx.x * 16 * kWt;
-  const uint16_t* wr[kWt];
-  const uint16_t* xr[kXt];
+  const int64_t m0 = (int64_t)blockIdx.x * 16;
   // rows behind the last one read the last one again; their sums are not stored
-#pragma unroll
-  for (int t = 0; t < kWt; ++t) wr[t] = w + min(m0 + 16 * t + l, M - 1) * K + 8 * g;
-#pragma unroll
-  for (int t = 0; t < kXt; ++t) xr[t] = x + (int64_t)min(16 * t + l, N - 1) * ldx + 8 * g;
-  f32x4 acc[kWt][kXt];
-#pragma unroll
-  for (int a = 0; a < kWt; ++a)
-#pragma unroll
-    for (int b = 0; b < kXt; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
+  const uint16_t* wr = w + min(m0 + l, M - 1) * K + 8 * g;
+  const uint16_t* xr = x + (int64_t)min(l, N - 1) * ldx + 8 * g;
+  f32x4 acc = {0, 0, 0, 0};
   const int pieces = (int)(K / 64);
-  constexpr int kAhead = kXt == 1 ? 4 : kXt == 2 ? 2 : 1;  // pieces whose loads are in flight together
+  constexpr int kAhead = 8;  // pieces whose loads are in flight together
   int p = wave;
   for (; p + (kAhead - 1) * kWaves < pieces; p += kAhead * kWaves) {
-    u32x4 fw[kAhead][kWt][2], fx[kAhead][kXt][2];
+    u32x4 fw[kAhead][2], fx[kAhead][2];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t at = (int64_t)(p + u * kWaves) * 64 + 32 * h;
-#pragma unroll
-        for (int t = 0; t < kWt; ++t) fw[u][t][h] = load16_stream(wr[t] + at);
-#pragma unroll
-        for (int t = 0; t < kXt; ++t) fx[u][t][h] = load16(xr[t] + at);
+        fw[u][h] = load16(wr + at);
+        fx[u][h] = load16(xr + at);
       }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int a = 0; a < kWt; ++a)
-#pragma unroll
-          for (int b = 0; b < kXt; ++b) acc[a][b] = T::mfma(fw[u][a][h], fx[u][b][h], acc[a][b]);
+      for (int h = 0; h < 2; ++h) acc = T::mfma(fw[u][h], fx[u][h], acc);
   }
 #pragma nounroll
   for (; p < pieces; p += kWaves) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      u32x4 fw[kWt], fx[kXt];
       const int64_t at = (int64_t)p * 64 + 32 * h;
-#pragma unroll
-      for (int t = 0; t < kWt; ++t) fw[t] = load16_stream(wr[t] + at);
-#pragma unroll
-      for (int t = 0; t < kXt; ++t) fx[t] = load16(xr[t] + at);
-#pragma unroll
-      for (int a = 0; a < kWt; ++a)
-#pragma unroll
-        for (int b = 0; b < kXt; ++b) acc[a][b] = T::mfma(fw[a], fx[b], acc[a][b]);
+      acc = T::mfma(load16(wr + at), load16(xr + at), acc);
     }
   }
   if (wave == pieces % kWaves) {  // what is left of K, a multiple of 8 below 64
@@ -571,38 +598,24 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, co
       const int64_t at = (int64_t)pieces * 64 + 32 * h;
       const bool in = at + 8 * g < K;
       const u32x4 zero = {0, 0, 0, 0};
-      u32x4 fw[kWt], fx[kXt];
-#pragma unroll
-      for (int t = 0; t < kWt; ++t) fw[t] = in ? load16(wr[t] + at) : zero;
-#pragma unroll
-      for (int t = 0; t < kXt; ++t) fx[t] = in ? load16(xr[t] + at) : zero;
-#pragma unroll
-      for (int a = 0; a < kWt; ++a)
-#pragma unroll
-        for (int b = 0; b < kXt; ++b) acc[a][b] = T::mfma(fw[a], fx[b], acc[a][b]);
+      acc = T::mfma(in ? load16(wr + at) : zero, in ? load16(xr + at) : zero, acc);
     }
   }
-#pragma unroll
-  for (int a = 0; a < kWt; ++a)
-#pragma unroll
-    for (int b = 0; b < kXt; ++b) part[wave][a][b][lane] = acc[a][b];
+  part[wave][lane] = acc;
   __syncthreads();
   // lane: row of x l, four neighbouring rows of W; two lanes' fours make eight columns of y
-  constexpr int kEights = kWt * kXt * 32;
-  for (int at = threadIdx.x; at < kEights; at += kWaves * 64) {
-    const int a = at / (kXt * 32), b = at / 32 % kXt, row = at % 16, half = at / 16 % 2;
-    const int64_t i = 16 * b + row, j = m0 + 16 * a + 8 * half;
-    if (i >= N || j >= M) continue;
-    f32x4 s0 = part[0][a][b][row + 32 * half], s1 = part[0][a][b][row + 32 * half + 16];
-#pragma unroll 2
-    for (int v = 1; v < kWaves; ++v) {
-      s0 += part[v][a][b][row + 32 * half];
-      s1 += part[v][a][b][row + 32 * half + 16];
-    }
-    float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]}, bias[8];
-    load_bias(bias, e.bias, j);
-    finish8<T>(v, bias, i, j, e);
+  const int row = threadIdx.x % 16, half = threadIdx.x / 16;
+  const int64_t j = m0 + 8 * half;
+  if (half >= 2 || row >= N || j >= M) return;
+  f32x4 s0 = part[0][row + 32 * half], s1 = part[0][row + 32 * half + 16];
+#pragma unroll 4
+  for (int v = 1; v < kWaves; ++v) {
+    s0 += part[v][row + 32 * half];
+    s1 += part[v][row + 32 * half + 16];
   }
+  float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]}, bias[8];
+  load_bias(bias, e.bias, j);
+  finish8<T>(v, bias, row, j, e);
 }
 
 // ---------------------------------------------------------------- the activation's gradient and dbias
@@ -659,27 +672,34 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* partial, fl
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How a product is cut into workgroups.  256 x 256 tiles, one to a CU, or
-// 128 x 128, two to a CU.  Tiles that fill whole rounds of the chip's 256 (512)
-// places are made whole; those of the last, partial round are cut along the
-// contraction into as many parts as there are places for, at least four
-// stages each.
+// How a product is cut into workgroups.  Tiles are 256 x 256, one to a CU, or
+// 128 x 128, two to a CU; few rows take 64 x 128 or 32 x 128, three or four to a
+// CU, whose LDS then holds more of W on its way.  Tiles that fill whole rounds
+// of the chip's places are made whole; those of the last, partial round are cut
+// along the contraction into as many parts as there are places for, at least
+// four stages each.
+struct Shape {
+  int i, j, places;
+  double stage;  // microseconds of a stage with all places taken
+};
+constexpr Shape kShapes[] = {{256, 256, 256, 1.40}, {128, 128, 512, 0.84}, {64, 128, 768, 0.80}, {32, 128, 1024, 0.80}};
+
 struct Plan {
-  bool wide;
+  int shape;
   int ti, tj, whole, cut, parts;
   int64_t c_part;
   double cost;
 };
 
-Plan plan_with(bool wide, int64_t I, int64_t J, int64_t C) {
+Plan plan_with(int shape, int64_t I, int64_t J, int64_t C) {
   Plan p{};
-  p.wide = wide;
-  const int64_t size = wide ? 256 : 128, places = wide ? 256 : 512;
-  p.ti = (int)up(I, size);
-  p.tj = (int)up(J, size);
+  p.shape = shape;
+  const Shape& s = kShapes[shape];
+  p.ti = (int)up(I, s.i);
+  p.tj = (int)up(J, s.j);
   const int64_t tiles = (int64_t)p.ti * p.tj, stages = up(C, kBk);
-  const int64_t last = tiles % places;
-  int64_t parts = last ? places / last : 1;
+  const int64_t last = tiles % s.places;
+  int64_t parts = last ? s.places / last : 1;
   if (parts > stages / 4) parts = stages / 4;
   if (parts < 1) parts = 1;
   const int64_t part_stages = up(stages, parts);
@@ -689,31 +709,32 @@ Plan plan_with(bool wide, int64_t I, int64_t J, int64_t C) {
   p.cut = parts > 1 ? (int)last : 0;
   p.whole = (int)tiles - p.cut;
   // microseconds: a stage of a full CU, and the cut tiles' sums written and read again
-  const double round = (wide ? 1.40 : 0.84) * stages;
-  p.cost = up(p.whole, places) * round;
-  if (p.cut) p.cost += round / (double)parts + 6.0 + p.cut * (double)parts * (double)(size * size) * 8.0 / 4.0e6;
+  const double round = s.stage * stages;
+  p.cost = up(p.whole, s.places) * round;
+  if (p.cut) p.cost += round / (double)parts + 6.0 + p.cut * (double)parts * s.i * s.j * 8.0 / 4.0e6;
   return p;
 }
 
 Plan plan_of(int64_t I, int64_t J, int64_t C) {
-  const Plan a = plan_with(true, I, J, C), b = plan_with(false, I, J, C);
+  if (I <= 32) return plan_with(3, I, J, C);
+  if (I <= 64) return plan_with(2, I, J, C);
+  const Plan a = plan_with(0, I, J, C), b = plan_with(1, I, J, C);
   return a.cost <= b.cost ? a : b;
 }
 
 size_t plan_bytes(int64_t I, int64_t J, int64_t C) {
   const Plan p = plan_of(I, J, C);
-  const size_t size = p.wide ? 256 : 128;
-  return (size_t)p.cut * (size_t)p.parts * size * size * sizeof(float);
+  return (size_t)p.cut * (size_t)p.parts * kShapes[p.shape].i * kShapes[p.shape].j * sizeof(float);
 }
 
-template <typename T, bool kTurnA, bool kTurnB, int kSize, int kWi, int kWj>
+template <typename T, bool kTurnA, bool kTurnB, int kI, int kJ, int kWi, int kWj>
 hipError_t launch_tiles(const Plan& p, GemmArgs& g, hipStream_t stream) {
   void* args[] = {&g};
-  const hipError_t e = hipLaunchKernel((const void*)&gemm_kernel<T, kSize, kSize, kWi, kWj, kTurnA, kTurnB>,
+  const hipError_t e = hipLaunchKernel((const void*)&gemm_kernel<T, kI, kJ, kWi, kWj, kTurnA, kTurnB>,
                                        dim3((unsigned)(p.whole + p.cut * p.parts)), dim3(kWi * kWj * 64), args, 0, stream);
   if (e != hipSuccess || p.cut == 0) return e;
-  return hipLaunchKernel((const void*)&gemm_join_kernel<T, kSize, kSize>,
-                         dim3(kSize * kSize / 8 / kJoinThreads, (unsigned)p.cut), dim3(kJoinThreads), args, 0, stream);
+  return hipLaunchKernel((const void*)&gemm_join_kernel<T, kI, kJ>, dim3(kI * kJ / 8 / kJoinThreads, (unsigned)p.cut),
+                         dim3(kJoinThreads), args, 0, stream);
 }
 
 template <typename T, bool kTurnA, bool kTurnB>
@@ -724,36 +745,53 @@ hipError_t launch_gemm(GemmArgs g, hipStream_t stream) {
   g.whole = p.whole;
   g.parts = p.parts;
   g.c_part = p.c_part;
-  return p.wide ? launch_tiles<T, kTurnA, kTurnB, 256, 2, 4>(p, g, stream)
-                : launch_tiles<T, kTurnA, kTurnB, 128, 2, 2>(p, g, stream);
+  switch (p.shape) {
+    case 0: return launch_tiles<T, kTurnA, kTurnB, 256, 256, 2, 4>(p, g, stream);
+    case 1: return launch_tiles<T, kTurnA, kTurnB, 128, 128, 2, 2>(p, g, stream);
+    case 2: return launch_tiles<T, kTurnA, kTurnB, 64, 128, 1, 4>(p, g, stream);
+    default: return launch_tiles<T, kTurnA, kTurnB, 32, 128, 1, 4>(p, g, stream);
+  }
 }
 
-constexpr int64_t kFewRows = 64;
+constexpr int64_t kVectorRows = 4;
+constexpr int64_t kFewRows = 16, kSmallWeight = 1 << 24;  // rows, and values of W, of rows_kernel
+bool few_rows(int64_t N, int64_t K, int64_t M) { return N <= kVectorRows || (N <= kFewRows && K * M <= kSmallWeight); }
 int64_t grad_rows(int64_t N) { return up(up(N, 64), kGradLines) * kGradLines; }  // rows of a slice: at most 64 slices
 size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
-template <typename T, int kXt, int kWt>
-hipError_t launch_rows(const LinearCall& l, const Epilogue& e, hipStream_t stream) {
+template <typename T, int kN, int kR>
+hipError_t launch_vector(const LinearCall& l, const Epilogue& e, hipStream_t stream) {
   const uint16_t *x = static_cast<const uint16_t*>(l.x), *w = static_cast<const uint16_t*>(l.w);
   int64_t ldx = l.ldx, K = l.K, M = l.M;
   int N = (int)l.N;
   Epilogue ep = e;
   void* args[] = {&x, &w, &ldx, &N, &K, &M, &ep};
-  const unsigned grid = (unsigned)up(M, 16 * kWt);
-  // waves of a workgroup: enough of them on the chip to keep its memory busy
-  if (grid >= 1024)
-    return hipLaunchKernel((const void*)&rows_kernel<T, kXt, kWt, 4>, dim3(grid), dim3(256), args, 0, stream);
-  if (grid >= 512)
-    return hipLaunchKernel((const void*)&rows_kernel<T, kXt, kWt, 8>, dim3(grid), dim3(512), args, 0, stream);
-  return hipLaunchKernel((const void*)&rows_kernel<T, kXt, kWt, 16>, dim3(grid), dim3(1024), args, 0, stream);
+  return hipLaunchKernel((const void*)&vector_kernel<T, kN, kR>, dim3((unsigned)up(M, kR * kVecThreads / 64)),
+                         dim3(kVecThreads), args, 0, stream);
 }
 
 template <typename T>
 hipError_t linear_fwd(const LinearCall& l, hipStream_t stream) {
   const Epilogue e{l.bias, l.residual, l.z, l.y, l.ldr, l.ldz, l.ldy, l.act};
-  if (l.N <= 16) return launch_rows<T, 1, 1>(l, e, stream);
-  if (l.N <= 32) return launch_rows<T, 2, 1>(l, e, stream);
-  if (l.N <= kFewRows) return launch_rows<T, 4, 1>(l, e, stream);
+  if (l.N <= kVectorRows) {
+    // rows of W a wave has on its way: four, or fewer where that leaves the chip short of waves
+    // (1 x 5120 x 5120: 11.2 us with one; 4 x 5120 x 5120: 15.7 us with two, 19.6 with one)
+    const bool many = l.M >= 8192;
+    if (l.N == 1) return many ? launch_vector<T, 1, 4>(l, e, stream) : launch_vector<T, 1, 1>(l, e, stream);
+    if (l.N == 2) return many ? launch_vector<T, 2, 4>(l, e, stream) : launch_vector<T, 2, 1>(l, e, stream);
+    return many ? launch_vector<T, 4, 4>(l, e, stream) : launch_vector<T, 4, 2>(l, e, stream);
+  }
+  if (few_rows(l.N, l.K, l.M)) {
+    const uint16_t *x = static_cast<const uint16_t*>(l.x), *w = static_cast<const uint16_t*>(l.w);
+    int64_t ldx = l.ldx, K = l.K, M = l.M;
+    int N = (int)l.N;
+    Epilogue ep = e;
+    void* args[] = {&x, &w, &ldx, &N, &K, &M, &ep};
+    const unsigned grid = (unsigned)up(M, 16);
+    // waves of a workgroup: enough of them on the chip to keep its memory busy
+    if (grid >= 1024) return hipLaunchKernel((const void*)&rows_kernel<T, 4>, dim3(grid), dim3(256), args, 0, stream);
+    return hipLaunchKernel((const void*)&rows_kernel<T, 16>, dim3(grid), dim3(1024), args, 0, stream);
+  }
   GemmArgs g{};
   g.a = static_cast<const uint16_t*>(l.x);
   g.b = static_cast<const uint16_t*>(l.w);
@@ -830,7 +868,7 @@ hipError_t linear_bwd(const LinearCall& l, hipStream_t stream) {
 
 }  // namespace
 
-size_t linear_fwd_workspace(int64_t N, int64_t K, int64_t M) { return N <= kFewRows ? 0 : plan_bytes(N, M, K); }
+size_t linear_fwd_workspace(int64_t N, int64_t K, int64_t M) { return few_rows(N, K, M) ? 0 : plan_bytes(N, M, K); }
 
 size_t linear_bwd_workspace(int64_t N, int64_t K, int64_t M) {
   const size_t slices = (size_t)up(N, grad_rows(N)), dx = plan_bytes(N, K, M), dw = plan_bytes(M, K, N);

@@ -59,54 +59,66 @@ if _torch is not None:
     _F32, _INTS = (_torch.float32,), (_torch.int64,)
 
 
+def _raw_stream():
+    """The current torch stream of a device, as an address.  torch.cuda.current_stream()
+    takes 2.7 us to say the same (it makes an object), more than half of a launch."""
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return raw if raw is not None else lambda index: _torch.cuda.current_stream(index).cuda_stream
+
+
 class _Args:
     """The tensors of one call: each is checked as it is named, all for the
     device of the first."""
 
-    def __init__(self):
-        self.device = None
+    __slots__ = ("device",)
 
-    def _common(self, name, t, dtypes):
+    def __init__(self):
+        self.device = -1
+
+    def _refuse(self, name, t, dtypes, shape):
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: dtype {str(t.dtype)[6:]}, expected {' or '.join(str(d)[6:] for d in dtypes)}")
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
 
-    def _placed(self, name, t):
-        device = t.device
-        if self.device is None:
-            if device.type != "cuda":
-                raise ValueError(f"{name}: on {device}, libengram needs GPU (HIP) tensors")
-            self.device = device
-        elif device != self.device:
-            raise ValueError(f"{name}: on {device}, other arguments on {self.device}")
+    def _place(self, name, t):
+        device = t.get_device() if t.is_cuda else -1
+        if device < 0:
+            raise ValueError(f"{name}: on {t.device}, libengram needs GPU (HIP) tensors")
+        if self.device >= 0:
+            raise ValueError(f"{name}: on {t.device}, other arguments on cuda:{self.device}")
+        self.device = device
 
     def dense(self, name, t, dtypes, shape):
         if t is None:
             return None
-        self._common(name, t, dtypes)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype not in dtypes or t.shape != shape:
+            self._refuse(name, t, dtypes, shape)
         if not t.is_contiguous():
             raise ValueError(f"{name}: libengram needs this tensor contiguous")
-        self._placed(name, t)
+        if not t.is_cuda or t.get_device() != self.device:
+            self._place(name, t)
         return t.data_ptr()
 
-    def rows(self, name, t, dtypes, shape):
+    def rows(self, name, t, dtypes, shape, width):
         """Address and elements between rows of a tensor of rows: each row's
-        values side by side, the rows at one distance."""
+        `width` values side by side, the rows at one distance."""
         if t is None:
             return None, 0
-        self._common(name, t, dtypes)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        width = 1
-        for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-            if size != 1 and stride != width:
-                raise ValueError(f"{name}: the values of a row are not side by side (strides {t.stride()})")
-            width *= size
-        ld = t.stride(0) if shape[0] > 1 else width
-        if ld < width:
-            raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-        self._placed(name, t)
+        if t.dtype not in dtypes or t.shape != shape:
+            self._refuse(name, t, dtypes, shape)
+        ld = width
+        if not t.is_contiguous():
+            strides, values = t.stride(), 1
+            for size, stride in zip(shape[:0:-1], strides[:0:-1]):
+                if size != 1 and stride != values:
+                    raise ValueError(f"{name}: the values of a row are not side by side (strides {strides})")
+                values *= size
+            if shape[0] > 1:
+                ld = strides[0]
+                if ld < width:
+                    raise ValueError(f"{name}: rows overlap (strides {strides})")
+        if not t.is_cuda or t.get_device() != self.device:
+            self._place(name, t)
         return t.data_ptr(), ld
 
     def workspace(self, t, need):
@@ -114,27 +126,32 @@ class _Args:
             if need:
                 raise ValueError(f"workspace: none given, the call needs {need} bytes")
             return None
-        if t.numel() * t.element_size() < need:
-            raise ValueError(f"workspace: {t.numel() * t.element_size()} bytes, the call needs {need}")
+        if t.nbytes < need:
+            raise ValueError(f"workspace: {t.nbytes} bytes, the call needs {need}")
         if not t.is_contiguous():
             raise ValueError("workspace: libengram needs this tensor contiguous")
-        self._placed("workspace", t)
+        if not t.is_cuda or t.get_device() != self.device:
+            self._place("workspace", t)
         return t.data_ptr() if need else None
 
-    def call(self, fn, *args, stream):
+    def call(self, fn, args, stream):
         """The library call with the tensors' device current and on `stream`
         (default: that device's current torch stream)."""
-        index = self.device.index
-        if index is not None and index != _torch.cuda.current_device():
+        index = self.device
+        if index != _torch.cuda.current_device():
             with _torch.cuda.device(index):
-                return self.call(fn, *args, stream=stream)
+                return self.call(fn, args, stream)
         if stream is None:
-            stream = _torch.cuda.current_stream().cuda_stream
+            stream = _raw_stream_of(index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
         status = fn(*args, stream)
         if status:
             raise _eg.EngramError(status)
+
+
+if _torch is not None:
+    _raw_stream_of = _raw_stream()
 
 
 def _shape(name, t, dims):
@@ -170,15 +187,14 @@ def engram_linear_fwd(x, w, y, workspace=None, bias=None, residual=None, z=None,
     N, K = _shape("x", x, 2)
     M = _shape("w", w, 2)[0]
     dt = (x.dtype,)
-    px, ldx = a.rows("x", x, _HALVES, (N, K))
+    px, ldx = a.rows("x", x, _HALVES, (N, K), K)
     pw = a.dense("w", w, dt, (M, K))
-    py, ldy = a.rows("y", y, dt, (N, M))
+    py, ldy = a.rows("y", y, dt, (N, M), M)
     pb = a.dense("bias", bias, _F32, (M,))
-    pr, ldr = a.rows("residual", residual, dt, (N, M))
-    pz, ldz = a.rows("z", z, dt, (N, M))
+    pr, ldr = a.rows("residual", residual, dt, (N, M), M)
+    pz, ldz = a.rows("z", z, dt, (N, M), M)
     ws = a.workspace(workspace, _eg.lib.engram_linear_fwd_workspace_bytes(N, K, M))
-    a.call(_eg.lib.engram_linear_fwd, px, pw, pb, pr, py, pz, ws, N, K, M, ldx, ldr, ldy, ldz, _CODE[x.dtype], _act(act),
-           stream=stream)
+    a.call(_eg.lib.engram_linear_fwd, (px, pw, pb, pr, py, pz, ws, N, K, M, ldx, ldr, ldy, ldz, _CODE[x.dtype], _act(act)), stream)
 
 
 def engram_linear_bwd(grad_y, x, w, grad_x, grad_w, workspace, z=None, grad_bias=None, act="none", stream=None) -> None:
@@ -192,16 +208,16 @@ def engram_linear_bwd(grad_y, x, w, grad_x, grad_w, workspace, z=None, grad_bias
     code = _act(act)
     if code and z is None:
         raise ValueError(f"z: the backward of {act} needs the forward's z")
-    pg, ldgy = a.rows("grad_y", grad_y, dt, (N, M))
-    px, ldx = a.rows("x", x, _HALVES, (N, K))
+    pg, ldgy = a.rows("grad_y", grad_y, dt, (N, M), M)
+    px, ldx = a.rows("x", x, _HALVES, (N, K), K)
     pw = a.dense("w", w, dt, (M, K))
-    pz, ldz = a.rows("z", z, dt, (N, M))
-    pgx, ldgx = a.rows("grad_x", grad_x, dt, (N, K))
+    pz, ldz = a.rows("z", z, dt, (N, M), M)
+    pgx, ldgx = a.rows("grad_x", grad_x, dt, (N, K), K)
     pgw = a.dense("grad_w", grad_w, dt, (M, K))
     pgb = a.dense("grad_bias", grad_bias, _F32, (M,))
     ws = a.workspace(workspace, _eg.lib.engram_linear_bwd_workspace_bytes(N, K, M))
-    a.call(_eg.lib.engram_linear_bwd, pg, px, pw, pz, pgx, pgw, pgb, ws, N, K, M, ldgy, ldx, ldz, ldgx, _CODE[x.dtype],
-           code, stream=stream)
+    a.call(_eg.lib.engram_linear_bwd, (pg, px, pw, pz, pgx, pgw, pgb, ws, N, K, M, ldgy, ldx, ldz, ldgx, _CODE[x.dtype],
+           code), stream)
 
 
 def engram_rope_freqs(theta: float, rotary_dim: int):
@@ -223,8 +239,8 @@ def _qk_inputs(a, q, k, wq, wk, positions, freqs):
     Hk = _shape("k", k, 3)[1]
     dt = (q.dtype,)
     R = 0 if freqs is None else 2 * _shape("freqs", freqs, 1)[0]
-    pq, ldq = a.rows("q", q, _FLOATS, (N, Hq, D))
-    pk, ldk = a.rows("k", k, dt, (N, Hk, D))
+    pq, ldq = a.rows("q", q, _FLOATS, (N, Hq, D), Hq * D)
+    pk, ldk = a.rows("k", k, dt, (N, Hk, D), Hk * D)
     pwq, pwk = a.dense("wq", wq, _F32, (D,)), a.dense("wk", wk, _F32, (D,))
     if R and positions is None:
         raise ValueError("positions: the rotation needs them")
@@ -242,10 +258,10 @@ def engram_qk_norm_rope_fwd(q, k, wq, wk, positions, freqs, q_out, k_out, eps=1e
     a = _Args()
     sizes, ptrs, (ldq, ldk), dt = _qk_inputs(a, q, k, wq, wk, positions, freqs)
     N, Hq, Hk, D, _ = sizes
-    pqo, ldqo = a.rows("q_out", q_out, dt, (N, Hq, D))
-    pko, ldko = a.rows("k_out", k_out, dt, (N, Hk, D))
-    a.call(_eg.lib.engram_qk_norm_rope_fwd, *ptrs, pqo, pko, *sizes, ldq, ldk, ldqo, ldko, eps, int(interleaved),
-           _CODE[q.dtype], stream=stream)
+    pqo, ldqo = a.rows("q_out", q_out, dt, (N, Hq, D), Hq * D)
+    pko, ldko = a.rows("k_out", k_out, dt, (N, Hk, D), Hk * D)
+    a.call(_eg.lib.engram_qk_norm_rope_fwd, (*ptrs, pqo, pko, *sizes, ldq, ldk, ldqo, ldko, eps, int(interleaved),
+           _CODE[q.dtype]), stream)
 
 
 def engram_qk_norm_rope_bwd(grad_q_out, grad_k_out, q, k, wq, wk, positions, freqs, grad_q, grad_k, grad_wq, grad_wk,
@@ -255,14 +271,14 @@ def engram_qk_norm_rope_bwd(grad_q_out, grad_k_out, q, k, wq, wk, positions, fre
     a = _Args()
     sizes, ptrs, (ldq, ldk), dt = _qk_inputs(a, q, k, wq, wk, positions, freqs)
     N, Hq, Hk, D, _ = sizes
-    pgqo, ldgqo = a.rows("grad_q_out", grad_q_out, dt, (N, Hq, D))
-    pgko, ldgko = a.rows("grad_k_out", grad_k_out, dt, (N, Hk, D))
-    pgq, ldgq = a.rows("grad_q", grad_q, dt, (N, Hq, D))
-    pgk, ldgk = a.rows("grad_k", grad_k, dt, (N, Hk, D))
+    pgqo, ldgqo = a.rows("grad_q_out", grad_q_out, dt, (N, Hq, D), Hq * D)
+    pgko, ldgko = a.rows("grad_k_out", grad_k_out, dt, (N, Hk, D), Hk * D)
+    pgq, ldgq = a.rows("grad_q", grad_q, dt, (N, Hq, D), Hq * D)
+    pgk, ldgk = a.rows("grad_k", grad_k, dt, (N, Hk, D), Hk * D)
     pgwq, pgwk = a.dense("grad_wq", grad_wq, _F32, (D,)), a.dense("grad_wk", grad_wk, _F32, (D,))
     ws = a.workspace(workspace, _eg.lib.engram_qk_norm_rope_bwd_workspace_bytes(N, Hq, Hk, D))
-    a.call(_eg.lib.engram_qk_norm_rope_bwd, pgqo, pgko, *ptrs, pgq, pgk, pgwq, pgwk, ws, *sizes, ldgqo, ldgko, ldq, ldk,
-           ldgq, ldgk, eps, int(interleaved), _CODE[q.dtype], stream=stream)
+    a.call(_eg.lib.engram_qk_norm_rope_bwd, (pgqo, pgko, *ptrs, pgq, pgk, pgwq, pgwk, ws, *sizes, ldgqo, ldgko, ldq, ldk,
+           ldgq, ldgk, eps, int(interleaved), _CODE[q.dtype]), stream)
 
 
 def engram_decay_attn_fwd_workspace_bytes(N: int, B: int, H: int, Dk: int, Dv: int) -> int:
@@ -278,9 +294,9 @@ def engram_decay_attn_bwd_workspace_bytes(N: int, B: int, H: int, Dk: int, Dv: i
 def _decay_inputs(a, q, k, v, log_decay):
     N, H, Dk = _shape("q", q, 3)
     Dv = _shape("v", v, 3)[2]
-    pq, ldq = a.rows("q", q, _BF, (N, H, Dk))
-    pk, ldk = a.rows("k", k, _BF, (N, H, Dk))
-    pv, ldv = a.rows("v", v, _BF, (N, H, Dv))
+    pq, ldq = a.rows("q", q, _BF, (N, H, Dk), H * Dk)
+    pk, ldk = a.rows("k", k, _BF, (N, H, Dk), H * Dk)
+    pv, ldv = a.rows("v", v, _BF, (N, H, Dv), H * Dv)
     return (N, H, Dk, Dv), (pq, pk, pv, a.dense("log_decay", log_decay, _F32, (H,))), (ldq, ldk, ldv)
 
 
@@ -294,11 +310,11 @@ def engram_decay_attn_fwd(q, k, v, log_decay, cu_seqlens, o, workspace, scale=1.
     (N, H, Dk, Dv), ptrs, lds = _decay_inputs(a, q, k, v, log_decay)
     B = _shape("cu_seqlens", cu_seqlens, 1)[0] - 1
     pcu = a.dense("cu_seqlens", cu_seqlens, _INTS, (B + 1,))
-    po, ldo = a.rows("o", o, _BF, (N, H, Dv))
+    po, ldo = a.rows("o", o, _BF, (N, H, Dv), H * Dv)
     pin = a.dense("state_in", state_in, _F32, (B, H, Dk, Dv))
     pout = a.dense("state_out", state_out, _F32, (B, H, Dk, Dv))
     ws = a.workspace(workspace, _eg.lib.engram_decay_attn_fwd_workspace_bytes(N, B, H, Dk, Dv))
-    a.call(_eg.lib.engram_decay_attn_fwd, *ptrs, pcu, pin, po, pout, ws, N, B, H, Dk, Dv, *lds, ldo, scale, stream=stream)
+    a.call(_eg.lib.engram_decay_attn_fwd, (*ptrs, pcu, pin, po, pout, ws, N, B, H, Dk, Dv, *lds, ldo, scale), stream)
 
 
 def engram_decay_attn_bwd(grad_o, q, k, v, log_decay, cu_seqlens, grad_q, grad_k, grad_v, workspace, scale=1.0,
@@ -309,16 +325,16 @@ def engram_decay_attn_bwd(grad_o, q, k, v, log_decay, cu_seqlens, grad_q, grad_k
     (N, H, Dk, Dv), ptrs, lds = _decay_inputs(a, q, k, v, log_decay)
     B = _shape("cu_seqlens", cu_seqlens, 1)[0] - 1
     pcu = a.dense("cu_seqlens", cu_seqlens, _INTS, (B + 1,))
-    pgo, ldgo = a.rows("grad_o", grad_o, _BF, (N, H, Dv))
-    pgq, ldgq = a.rows("grad_q", grad_q, _BF, (N, H, Dk))
-    pgk, ldgk = a.rows("grad_k", grad_k, _BF, (N, H, Dk))
-    pgv, ldgv = a.rows("grad_v", grad_v, _BF, (N, H, Dv))
+    pgo, ldgo = a.rows("grad_o", grad_o, _BF, (N, H, Dv), H * Dv)
+    pgq, ldgq = a.rows("grad_q", grad_q, _BF, (N, H, Dk), H * Dk)
+    pgk, ldgk = a.rows("grad_k", grad_k, _BF, (N, H, Dk), H * Dk)
+    pgv, ldgv = a.rows("grad_v", grad_v, _BF, (N, H, Dv), H * Dv)
     states = (B, H, Dk, Dv)
     pin, pgout = a.dense("state_in", state_in, _F32, states), a.dense("grad_state_out", grad_state_out, _F32, states)
     pgin = a.dense("grad_state_in", grad_state_in, _F32, states)
     ws = a.workspace(workspace, _eg.lib.engram_decay_attn_bwd_workspace_bytes(N, B, H, Dk, Dv))
-    a.call(_eg.lib.engram_decay_attn_bwd, pgo, *ptrs, pcu, pin, pgout, pgq, pgk, pgv, pgin, ws, N, B, H, Dk, Dv, ldgo, *lds,
-           ldgq, ldgk, ldgv, scale, stream=stream)
+    a.call(_eg.lib.engram_decay_attn_bwd, (pgo, *ptrs, pcu, pin, pgout, pgq, pgk, pgv, pgin, ws, N, B, H, Dk, Dv, ldgo, *lds,
+           ldgq, ldgk, ldgv, scale), stream)
 
 
 def engram_decay_attn_step(q, k, v, log_decay, state, slots, o, scale=1.0, stream=None) -> None:
@@ -331,8 +347,8 @@ def engram_decay_attn_step(q, k, v, log_decay, state, slots, o, scale=1.0, strea
     total = _shape("state", state, 4)[0]
     ps = a.dense("state", state, _F32, (total, H, Dk, Dv))
     pslots = a.dense("slots", slots, _INTS, (B,))
-    po, ldo = a.rows("o", o, _BF, (B, H, Dv))
-    a.call(_eg.lib.engram_decay_attn_step, *ptrs, ps, pslots, po, B, H, Dk, Dv, total, *lds, ldo, scale, stream=stream)
+    po, ldo = a.rows("o", o, _BF, (B, H, Dv), H * Dv)
+    a.call(_eg.lib.engram_decay_attn_step, (*ptrs, ps, pslots, po, B, H, Dk, Dv, total, *lds, ldo, scale), stream)
 
 
 __all__ = ["engram_linear_fwd", "engram_linear_bwd", "engram_linear_fwd_workspace_bytes",

@@ -40,50 +40,73 @@ constexpr float kInv2p32 = 2.3283064365386963e-10f;  // 2^-32
 
 struct bf16_t { uint16_t v; };
 
-__device__ __forceinline__ void load8(const bf16_t* p, float (&v)[8]) {
-  const u32x4 r = load16(p);
+// Eight values as they lie in memory.
+template <typename T>
+struct Raw {
+  u32x4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = load16(reinterpret_cast<const u32x4*>(p) + i);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> zero_raw() {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = u32x4{0, 0, 0, 0};
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw<bf16_t>& r, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf_lo(r[i]);
-    v[2 * i + 1] = bf_hi(r[i]);
+    v[2 * i] = bf_lo(r.w[0][i]);
+    v[2 * i + 1] = bf_hi(r.w[0][i]);
   }
 }
-__device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
+__device__ __forceinline__ void unpack8(const Raw<_Float16>& r, float (&v)[8]) {
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-  const f16x8 r = *reinterpret_cast<const f16x8*>(p);
+  const f16x8 h = __builtin_bit_cast(f16x8, r.w[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)r[i];
+  for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+__device__ __forceinline__ void unpack8(const Raw<float>& r, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[i + 4] = b[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i / 4][i % 4]);
 }
+// kStream: the line is not kept in the caches.
+template <bool kStream>
+__device__ __forceinline__ void put16(void* p, u32x4 v) {
+  if (kStream) store16_stream(p, v);
+  else store16(p, v);
+}
+template <bool kStream>
 __device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
   u32x4 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  store16(p, r);
+  put16<kStream>(p, r);
 }
+template <bool kStream>
 __device__ __forceinline__ void store8(_Float16* p, const float (&v)[8]) {
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
   f16x8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r[i] = (_Float16)v[i];
-  *reinterpret_cast<f16x8*>(p) = r;
+  put16<kStream>(p, __builtin_bit_cast(u32x4, r));
 }
+template <bool kStream>
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  f32x4 a, b;
+  u32x4 a, b;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    a[i] = v[i];
-    b[i] = v[i + 4];
+    a[i] = __float_as_uint(v[i]);
+    b[i] = __float_as_uint(v[i + 4]);
   }
-  *reinterpret_cast<f32x4*>(p) = a;
-  *reinterpret_cast<f32x4*>(p + 4) = b;
+  put16<kStream>(p, a);
+  put16<kStream>(p + 4, b);
 }
 
 // Sum over the kLanes lanes of a row, the same value in each of them.
@@ -173,8 +196,8 @@ struct Side {
   int64_t ldx, ldg, ldy;  // values between tokens
   int heads;
   int blocks;         // workgroups on this side
-  int splits;         // units a token's heads are split into
-  int unit_passes;    // passes (of 64 / lanes heads) in a unit
+  int passes;         // a token's heads in passes of 64 / lanes
+  int share;          // passes of a wave, one behind the other
 };
 
 struct QkArgs {
@@ -185,6 +208,28 @@ struct QkArgs {
   int64_t N;
   int D, R;
   float eps;
+};
+
+// A wave's share of the passes over all tokens' heads: token after token, the
+// passes of each in order, so that shares differ by less than a pass and a
+// token's angles are computed once (or again where a share begins inside it).
+struct Passes {
+  int64_t n;  // token
+  int pass, passes, left;
+  __device__ __forceinline__ Passes(const Side& s, int64_t tokens, int64_t wave) {
+    const int64_t all = tokens * s.passes, first = wave * s.share;
+    passes = s.passes;
+    left = first < all ? (int)min((int64_t)s.share, all - first) : 0;
+    n = first / passes;
+    pass = (int)(first - n * passes);
+  }
+  __device__ __forceinline__ bool next() {
+    if (++pass == passes) {
+      pass = 0;
+      ++n;
+    }
+    return --left > 0;
+  }
 };
 
 template <typename T, int kLanes, bool kInter>
@@ -202,42 +247,51 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_rope_fwd_kernel(QkArgs arg
   uint64_t f[8];
   zero8(wa);
   zero8(wb);
-  if (c.has_a) load8(s.w + c.a, wa);
-  if (c.has_b) load8(s.w + c.b, wb);
+  if (c.has_a) unpack8(load_raw(s.w + c.a), wa);
+  if (c.has_b) unpack8(load_raw(s.w + c.b), wb);
   load_freqs<T, kInter>(args.freqs, c, f);
   const T* x = static_cast<const T*>(s.x);
   T* y = static_cast<T*>(s.y);
-  const int64_t units = args.N * s.splits;
-  for (int64_t u = (int64_t)block * kQkWaves + wave; u < units; u += (int64_t)s.blocks * kQkWaves) {
-    const int64_t n = s.splits == 1 ? u : (int64_t)((uint32_t)u / (uint32_t)s.splits);  // split calls have few tokens
-    const int first = (int)(u - n * s.splits) * s.unit_passes;
-    float cs[8], sn[8];
-    angles<T>(f, args.R ? args.positions[n] : 0, cs, sn);
-    const T* xr = x + n * s.ldx;
-    T* yr = y + n * s.ldy;
-    const int last_head = min((first + s.unit_passes) * kRows, s.heads);
-    for (int h = first * kRows + row; h - row < last_head; h += kRows) {
-      if (h >= last_head) continue;  // only whole rows of lanes leave, so the row sums below stay whole
-      float a[8], b[8];
-      zero8(a);
-      zero8(b);
-      const T* xp = xr + h * args.D;
-      if (c.has_a) load8(xp + c.a, a);
-      if (c.has_b) load8(xp + c.b, b);
-      float ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-      const float rstd = 1.0f / sqrtf(row_sum<kLanes>(ss) * inv_d + args.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= rstd * wa[i];
-        b[i] *= rstd * wb[i];
-      }
-      rotate<kInter, 1>(a, b, cs, sn);
-      T* yp = yr + h * args.D;
-      if (c.has_a) store8(yp + c.a, a);
-      if (c.has_b) store8(yp + c.b, b);
+  Passes at(s, args.N, (int64_t)block * kQkWaves + wave);
+  const auto fetch = [&](Raw<T>& a, Raw<T>& b) {
+    a = zero_raw<T>();
+    b = zero_raw<T>();
+    const int h = at.pass * kRows + row;
+    if (h < s.heads) {
+      const T* p = x + at.n * s.ldx + h * args.D;
+      if (c.has_a) a = load_raw(p + c.a);
+      if (c.has_b) b = load_raw(p + c.b);
     }
+  };
+  if (at.left == 0) return;
+  Raw<T> ra, rb;
+  fetch(ra, rb);
+  float cs[8], sn[8];
+  angles<T>(f, args.R ? args.positions[at.n] : 0, cs, sn);
+  for (;;) {
+    const int h = at.pass * kRows + row;
+    T* yp = y + at.n * s.ldy + h * args.D;
+    float a[8], b[8];
+    unpack8(ra, a);
+    unpack8(rb, b);
+    const bool more = at.next(), turned = more && at.pass == 0;
+    if (more) fetch(ra, rb);
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
+    const float rstd = 1.0f / sqrtf(row_sum<kLanes>(ss) * inv_d + args.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] *= rstd * wa[i];
+      b[i] *= rstd * wb[i];
+    }
+    rotate<kInter, 1>(a, b, cs, sn);
+    if (h < s.heads) {
+      if (c.has_a) store8<true>(yp + c.a, a);
+      if (c.has_b) store8<true>(yp + c.b, b);
+    }
+    if (!more) return;
+    if (turned) angles<T>(f, args.R ? args.positions[at.n] : 0, cs, sn);
   }
 }
 
@@ -258,44 +312,54 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_rope_bwd_kernel(QkArgs arg
   zero8(wb);
   zero8(da);
   zero8(db);
-  if (c.has_a) load8(s.w + c.a, wa);
-  if (c.has_b) load8(s.w + c.b, wb);
+  if (c.has_a) unpack8(load_raw(s.w + c.a), wa);
+  if (c.has_b) unpack8(load_raw(s.w + c.b), wb);
   load_freqs<T, kInter>(args.freqs, c, f);
   const T* x = static_cast<const T*>(s.x);
   const T* gy = static_cast<const T*>(s.gy);
   T* dx = static_cast<T*>(s.y);
-  const int64_t units = args.N * s.splits;
-  for (int64_t u = (int64_t)block * kQkWaves + wave; u < units; u += (int64_t)s.blocks * kQkWaves) {
-    const int64_t n = s.splits == 1 ? u : (int64_t)((uint32_t)u / (uint32_t)s.splits);  // split calls have few tokens
-    const int first = (int)(u - n * s.splits) * s.unit_passes;
-    float cs[8], sn[8];
-    angles<T>(f, args.R ? args.positions[n] : 0, cs, sn);
-    const int last_head = min((first + s.unit_passes) * kRows, s.heads);
-    for (int h = first * kRows + row; h - row < last_head; h += kRows) {
-      if (h >= last_head) continue;
-      float a[8], b[8], ga[8], gb[8];
-      zero8(a);
-      zero8(b);
-      zero8(ga);
-      zero8(gb);
-      const T* xp = x + n * s.ldx + h * args.D;
-      const T* gp = gy + n * s.ldg + h * args.D;
+  Passes at(s, args.N, (int64_t)block * kQkWaves + wave);
+  const auto fetch = [&](Raw<T>& a, Raw<T>& b, Raw<T>& ga, Raw<T>& gb) {
+    a = b = ga = gb = zero_raw<T>();
+    const int h = at.pass * kRows + row;
+    if (h < s.heads) {
+      const T *p = x + at.n * s.ldx + h * args.D, *q = gy + at.n * s.ldg + h * args.D;
       if (c.has_a) {
-        load8(xp + c.a, a);
-        load8(gp + c.a, ga);
+        a = load_raw(p + c.a);
+        ga = load_raw(q + c.a);
       }
       if (c.has_b) {
-        load8(xp + c.b, b);
-        load8(gp + c.b, gb);
+        b = load_raw(p + c.b);
+        gb = load_raw(q + c.b);
       }
+    }
+  };
+  bool more = at.left != 0;
+  if (more) {
+    Raw<T> ra, rb, rga, rgb;
+    fetch(ra, rb, rga, rgb);
+    float cs[8], sn[8];
+    angles<T>(f, args.R ? args.positions[at.n] : 0, cs, sn);
+    while (more) {
+      const int h = at.pass * kRows + row;
+      T* dp = dx + at.n * s.ldy + h * args.D;
+      float a[8], b[8], ga[8], gb[8];
+      unpack8(ra, a);
+      unpack8(rb, b);
+      unpack8(rga, ga);
+      unpack8(rgb, gb);
+      more = at.next();
+      if (more) fetch(ra, rb, rga, rgb);
       rotate<kInter, -1>(ga, gb, cs, sn);
+      if (more && at.pass == 0) angles<T>(f, args.R ? args.positions[at.n] : 0, cs, sn);
       float ss = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss += a[i] * a[i] + b[i] * b[i];
         dot += ga[i] * wa[i] * a[i] + gb[i] * wb[i] * b[i];
       }
-      const float rstd = 1.0f / sqrtf(row_sum<kLanes>(ss) * inv_d + args.eps);
+      const float norm = 1.0f / sqrtf(row_sum<kLanes>(ss) * inv_d + args.eps);
+      const float rstd = h < s.heads ? norm : 0.0f;  // lanes without a head add nothing to dw, whatever eps
       // with u = x rstd: dx = rstd g w - u (rstd mean(g w u)), and mean(g w u) = rstd dot / D
       const float m = row_sum<kLanes>(dot) * inv_d * rstd * rstd;
 #pragma unroll
@@ -306,9 +370,10 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_rope_bwd_kernel(QkArgs arg
         a[i] = rstd * (ga[i] * wa[i]) - ua * m;
         b[i] = rstd * (gb[i] * wb[i]) - ub * m;
       }
-      T* dp = dx + n * s.ldy + h * args.D;
-      if (c.has_a) store8(dp + c.a, a);
-      if (c.has_b) store8(dp + c.b, b);
+      if (h < s.heads) {
+        if (c.has_a) store8<false>(dp + c.a, a);
+        if (c.has_b) store8<false>(dp + c.b, b);
+      }
     }
   }
   // the rows of a wave, then the waves, in order
@@ -338,8 +403,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_rope_bwd_kernel(QkArgs arg
 }
 
 // dw[j] = the sum of `rows` partial rows, queries (blockIdx.y 0) or keys: 16
-// columns a workgroup, 16 threads a column, joined in a fixed order.
-constexpr int kRedCols = 16, kRedSlices = 16;
+// columns a workgroup, 64 threads a column, joined in a fixed order.
+constexpr int kRedCols = 16, kRedSlices = 64;
 __global__ __launch_bounds__(kRedCols* kRedSlices) void qk_norm_rope_reduce_kernel(const float* partial, float* dwq,
                                                                                    float* dwk, int rows_q, int rows_k,
                                                                                    int D) {
@@ -353,11 +418,11 @@ __global__ __launch_bounds__(kRedCols* kRedSlices) void qk_norm_rope_reduce_kern
     for (int r = slice; r < rows; r += kRedSlices) s += p[(int64_t)r * D + col];
   part[slice][threadIdx.x % kRedCols] = s;
   __syncthreads();
-  if (slice == 0 && col < D) {
-#pragma unroll
-    for (int i = 1; i < kRedSlices; ++i) s += part[i][threadIdx.x];
-    (keys ? dwk : dwq)[col] = s;
+  for (int half = kRedSlices / 2; half >= 1; half /= 2) {
+    if (slice < half) part[slice][threadIdx.x % kRedCols] += part[slice + half][threadIdx.x % kRedCols];
+    __syncthreads();
   }
+  if (slice == 0 && col < D) (keys ? dwk : dwq)[col] = part[0][threadIdx.x];
 }
 
 struct QkKernels {
@@ -393,31 +458,32 @@ int qk_lanes(int D, int R) {
   return lanes;
 }
 
-// Workgroups and units of the two sides.  A unit is one token's heads when
-// there are waves enough for one token each, or a single pass of the heads
-// when there are few tokens, so that a decode batch's heads run side by side.
-constexpr int64_t kQkMostBlocks = 2048;   // 8 workgroups (32 waves) a CU
-void qk_plan(Side (&side)[2], int64_t N, int lanes) {
+// Workgroups of the two sides: the passes over all heads in even shares, the
+// sides by their heads.  Forward: shares of about two passes and streaming
+// stores (8192 tokens, 40 + 8 heads of 128: 38.5 us, 5.2 TB/s, against 41.1 with
+// as many workgroups as fit the chip and 43.6 with plain stores).  Backward: as
+// many workgroups as fit the chip, three a CU, since each leaves a partial row
+// of dw, and shares of two passes at least for the same reason (40 + 40 heads:
+// 114 us; 124 with 1024 workgroups, 141 with streaming stores).
+constexpr int64_t kFwdBlocks = 5120, kBwdBlocks = 768;
+void qk_plan(Side (&side)[2], int64_t N, int lanes, int64_t most, int64_t least) {
   const int rows = 64 / lanes;
-  int64_t want[2];
+  int64_t passes[2], all = 0;
   for (int i = 0; i < 2; ++i) {
-    const int passes = (side[i].heads + rows - 1) / rows;
-    const bool split = N * kQkWaves <= kQkMostBlocks * kQkWaves / 2;
-    side[i].unit_passes = split ? 1 : passes;
-    side[i].splits = split ? passes : 1;
-    want[i] = (N * side[i].splits + kQkWaves - 1) / kQkWaves;
+    side[i].passes = (side[i].heads + rows - 1) / rows;
+    passes[i] = N * side[i].passes;
+    all += passes[i];
   }
-  const int64_t all = (int64_t)side[0].heads + side[1].heads;
+  const int64_t even = (all + most * kQkWaves - 1) / (most * kQkWaves), share = even > least ? even : least;
   for (int i = 0; i < 2; ++i) {
-    int64_t most = kQkMostBlocks * side[i].heads / all;
-    if (most < 1) most = 1;
-    side[i].blocks = (int)(want[i] < most ? want[i] : most);
+    side[i].share = (int)share;
+    side[i].blocks = (int)((passes[i] + share * kQkWaves - 1) / (share * kQkWaves));
   }
 }
 
 }  // namespace
 
-size_t qk_norm_rope_bwd_workspace(int64_t D) { return (size_t)(kQkMostBlocks + 2) * (size_t)D * sizeof(float); }
+size_t qk_norm_rope_bwd_workspace(int64_t D) { return (size_t)(kBwdBlocks + 2) * (size_t)D * sizeof(float); }
 
 hipError_t launch_qk_norm_rope_fwd(const QkCall& q, hipStream_t stream) {
   QkArgs a{};
@@ -428,7 +494,7 @@ hipError_t launch_qk_norm_rope_fwd(const QkCall& q, hipStream_t stream) {
   const int64_t heads[] = {q.Hq, q.Hk};
   for (int i = 0; i < 2; ++i) a.side[i] = Side{x[i], nullptr, w[i], y[i], ldx[i], 0, ldy[i], (int)heads[i], 0, 0, 0};
   const int lanes = qk_lanes((int)q.D, (int)q.R);
-  qk_plan(a.side, q.N, lanes);
+  qk_plan(a.side, q.N, lanes, kFwdBlocks, 1);
   a.positions = q.positions;
   a.freqs = reinterpret_cast<const uint64_t*>(q.freqs);
   a.N = q.N;
@@ -450,7 +516,7 @@ hipError_t launch_qk_norm_rope_bwd(const QkCall& q, hipStream_t stream) {
   const int64_t heads[] = {q.Hq, q.Hk};
   for (int i = 0; i < 2; ++i) a.side[i] = Side{x[i], gy[i], w[i], y[i], ldx[i], ldg[i], ldy[i], (int)heads[i], 0, 0, 0};
   const int lanes = qk_lanes((int)q.D, (int)q.R);
-  qk_plan(a.side, q.N, lanes);
+  qk_plan(a.side, q.N, lanes, kBwdBlocks, 2);
   a.positions = q.positions;
   a.freqs = reinterpret_cast<const uint64_t*>(q.freqs);
   a.partial = static_cast<float*>(q.workspace);

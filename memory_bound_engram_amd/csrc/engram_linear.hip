@@ -10,7 +10,7 @@
 // or with i (or j) contiguous (W in dx; dz and x in dW); the second kind is
 // turned on its way from LDS to the registers by the transposing LDS load.
 // Both operands go from memory straight into LDS, 64 values of c at a time,
-// two stages deep.  The products are fp32 sums over bf16 or fp16 operands on the matrix cores
+// two or four stages deep.  The products are fp32 sums over bf16 or fp16 operands on the matrix cores
 // (16x16x32); the one rounding is that of the outputs.  In the backward dz is
 // rounded to the operands' type where it differs from dy (an activation), as
 // it is an operand of two products; dbias is summed before that rounding.
@@ -131,8 +131,14 @@ struct Epilogue {
   int act;
 };
 
+__device__ __forceinline__ u32x4 load_residual(int64_t i, int64_t j, const Epilogue& e) {
+  return load16(static_cast<const uint16_t*>(e.residual) + i * e.ldr + j);
+}
+
+// Eight neighbouring sums to their end; `residual` is looked at if there is one.
 template <typename T>
-__device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], int64_t i, int64_t j, const Epilogue& e) {
+__device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], u32x4 residual, int64_t i, int64_t j,
+                                        const Epilogue& e) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] += bias[k];
   if (e.z) store16(static_cast<uint16_t*>(e.z) + i * e.ldz + j, pack8<T>(v));
@@ -143,7 +149,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], i
   }
   if (e.residual) {
     float r[8];
-    unpack8<T>(load16(static_cast<const uint16_t*>(e.residual) + i * e.ldr + j), r);
+    unpack8<T>(residual, r);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += r[k];
   }
@@ -286,17 +292,18 @@ struct Operand {
   };
 };
 
-// kI x kJ tiles, kWi x kWj waves.  Two stages in LDS, and half a stage's
+// kI x kJ tiles, kWi x kWj waves.  kDepth stages in LDS, and half a stage's
 // fragments ahead in registers: while one half is multiplied, the next half is
-// read; in the middle of a stage it is read out, and the stage after the next
-// is sent for into its place, one whole stage of products before its use.
-template <typename T, int kI, int kJ, int kWi, int kWj, bool kTurnA, bool kTurnB>
+// read; in the middle of a stage it is read out, and the stage kDepth further
+// on is sent for into its place, kDepth - 1 whole stages of products before its
+// use.
+template <typename T, int kI, int kJ, int kWi, int kWj, int kDepth, bool kTurnA, bool kTurnB>
 __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
   constexpr int kWaves = kWi * kWj, kMt = kI / kWi / 16, kNt = kJ / kWj / 16;
   using A = Operand<kI, kWaves, kMt, kTurnA, false>;
   using B = Operand<kJ, kWaves, kNt, kTurnB, !kTurnB>;
   constexpr uint32_t kStageBytes = (kI + kJ) * kBk * 2;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(kI + kJ) * kBk];
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kDepth][(kI + kJ) * kBk];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // Workgroups go round the eight XCDs; each takes a run of neighbouring
@@ -367,9 +374,9 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
   // All but this wave's `newer` youngest loads are in LDS and its reads done; then all waves'.
   auto meet = [&](auto newer) {
     constexpr int n = decltype(newer)::value;
-    static_assert(n < 16, "one field of the wait count");
+    static_assert(n < 64, "vmcnt counts to 63");
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070 | n);  // vmcnt n, lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);  // vmcnt n, lgkmcnt 0
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -378,25 +385,43 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
   constexpr std::integral_constant<int, 0> kFirst{};
   constexpr std::integral_constant<int, 1> kSecond{};
 
-  fill(0);
-  fill(kStageBytes);
-  meet(std::integral_constant<int, A::kLoads + B::kLoads>{});
+  constexpr int kInFlight = A::kLoads + B::kLoads;  // loads of one stage
+  const bool plain = !g.e.z && g.e.act == ENGRAM_ACT_NONE;
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) fill(s * kStageBytes);
+  if (!kTurnB && !cut && plain && g.e.residual) {
+    // nothing but a residual to add: the sums begin with it, loaded while the first stages are on
+    // their way (4000 x 5120 x 5120: 19 us more than without a residual; 31 when read at the end)
+#pragma unroll
+    for (int n = 0; n < kNt; n += 2)
+#pragma unroll
+      for (int m = 0; m < kMt; ++m) {
+        // places beyond the result take its last row or columns, which are not stored: no branch, so
+        // that all loads are on their way at once
+        const int64_t i = min(i0 + wi + m * 16 + lane % 16, g.I - 1);
+        const int64_t j = min(j0 + wj + n * 16 + 8 * (lane / 16), g.J - 8);
+        float r[8];
+        unpack8<T>(load_residual(i, j, g.e), r);
+        acc[m][n] = f32x4{r[0], r[1], r[2], r[3]};
+        acc[m][n + 1] = f32x4{r[4], r[5], r[6], r[7]};
+      }
+  }
+  meet(std::integral_constant<int, (kDepth - 1) * kInFlight>{});
   read(kFirst, 0);
   uint32_t stage = 0;
 #pragma nounroll
   for (int s = 0; s < stages; ++s) {
     read(kSecond, stage);
     multiply(kFirst);
-    meet(std::integral_constant<int, 0>{});  // stage s + 1 is there, stage s read out by all
+    meet(std::integral_constant<int, (kDepth - 2) * kInFlight>{});  // stage s + 1 is there, stage s read out by all
     fill(stage);
-    stage ^= kStageBytes;
+    stage = stage + kStageBytes == kDepth * kStageBytes ? 0 : stage + kStageBytes;
     read(kFirst, stage);
     multiply(kSecond);
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // the last fills, of nothing, must not outlive the workgroup's LDS
 
   // lane: row l of each 16; eight neighbouring columns of each 32 (a turned B: two fours, 16 apart)
-  const bool plain = !g.e.z && !g.e.residual && g.e.act == ENGRAM_ACT_NONE;
   if (cut || kTurnB || plain) {
     float* sums = cut ? g.partial + ((int64_t)(tile - g.whole) * g.parts + part) * kI * kJ : nullptr;
     constexpr int kApart = kTurnB ? 16 : 4;
@@ -432,7 +457,7 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
     }
     return;
   }
-  // With an activation, a residual or z the epilogue is long, and unrolled over
+  // With an activation or z the epilogue is long, and unrolled over
   // the accumulators it would be more code than the instruction cache holds: the
   // sums go through LDS, 32 columns of each wave at a time, and one loop ends them.
   // Piece p (four columns) of row r lies at p ^ (r & 7).
@@ -453,13 +478,25 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
       const int64_t j = j0 + wj + n * 16 + 8 * (lane % 4);
       float bias[8];
       load_bias(bias, j < g.J ? g.e.bias : nullptr, j);
+      constexpr int kAhead = 4;  // rows whose residuals are loaded together
 #pragma nounroll
-      for (int r = lane / 4; r < kRows; r += 16) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(mine + r * 32 + ((2 * (lane % 4)) ^ (r & 7)) * 4);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(mine + r * 32 + ((2 * (lane % 4) + 1) ^ (r & 7)) * 4);
-        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        const int64_t i = i0 + wi + r;
-        if (i < g.I && j < g.J) finish8<T>(v, bias, i, j, g.e);
+      for (int r0 = lane / 4; r0 < kRows; r0 += 16 * kAhead) {
+        u32x4 residual[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int64_t i = i0 + wi + r0 + 16 * k;
+          if (r0 + 16 * k < kRows && i < g.I && j < g.J && g.e.residual) residual[k] = load_residual(i, j, g.e);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int r = r0 + 16 * k;
+          if (r >= kRows) break;
+          const f32x4 a = *reinterpret_cast<const f32x4*>(mine + r * 32 + ((2 * (lane % 4)) ^ (r & 7)) * 4);
+          const f32x4 b = *reinterpret_cast<const f32x4*>(mine + r * 32 + ((2 * (lane % 4) + 1) ^ (r & 7)) * 4);
+          float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+          const int64_t i = i0 + wi + r;
+          if (i < g.I && j < g.J) finish8<T>(v, bias, residual[k], i, j, g.e);
+        }
       }
     }
   }
@@ -474,6 +511,8 @@ __global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs g) {
   tile_origin(g, g.whole + tile, kI, kJ, i0, j0);
   const int64_t i = i0 + at / kJ, j = j0 + at % kJ;
   if (i >= g.I || j >= g.J) return;
+  u32x4 residual = {0, 0, 0, 0};
+  if (g.e.residual) residual = load_residual(i, j, g.e);
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bias[8];
   const float* p = g.partial + (int64_t)tile * g.parts * kI * kJ + at;
   for (int s = 0; s < g.parts; ++s, p += kI * kJ) {
@@ -485,7 +524,7 @@ __global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs g) {
     }
   }
   load_bias(bias, g.e.bias, j);
-  finish8<T>(v, bias, i, j, g.e);
+  finish8<T>(v, bias, residual, i, j, g.e);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -615,7 +654,9 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, co
   }
   float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]}, bias[8];
   load_bias(bias, e.bias, j);
-  finish8<T>(v, bias, row, j, e);
+  u32x4 residual = {0, 0, 0, 0};
+  if (e.residual) residual = load_residual(row, j, e);
+  finish8<T>(v, bias, residual, row, j, e);
 }
 
 // ---------------------------------------------------------------- the activation's gradient and dbias
@@ -673,16 +714,27 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* partial, fl
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a product is cut into workgroups.  Tiles are 256 x 256, one to a CU, or
-// 128 x 128, two to a CU; few rows take 64 x 128 or 32 x 128, three or four to a
-// CU, whose LDS then holds more of W on its way.  Tiles that fill whole rounds
-// of the chip's places are made whole; those of the last, partial round are cut
-// along the contraction into as many parts as there are places for, at least
-// four stages each.
+// 128 x 128, two to a CU with two stages each or one with four: where fewer
+// tiles than two to a CU are to be had, the deeper one keeps as much on its way
+// (128 x 2560 x 25600: 28 us against 36).  Few rows take 64 x 128 or 32 x 128,
+// three or four to a CU, whose LDS then holds more of W on its way.  Tiles that
+// fill whole rounds of the chip's places are made whole; those of the last,
+// partial round are cut along the contraction into as many parts as there are
+// places for, at least four stages each (512 x 5120 x 5120 in 128 x 128 tiles:
+// 47 us against 55 uncut; 4000 x 5120 x 5120: 196 against 245).
+// The cheapest by the costs below is taken, which were fitted to all three
+// shapes over fourteen sizes (256^2, 128^2 and 128^2 deep, us: 4000 x 5120 x 5120
+// 197, 208, 247; 2048 x 5120 x 5120 126, 110, 133; 1000 x 1368 x 5120 41, 27, 34;
+// 2000 x 640 x 6000 24, 35, 32; 700 x 700 x 700 21, 12, 13).
 struct Shape {
   int i, j, places;
-  double stage;  // microseconds of a stage with all places taken
+  double stage, round;  // microseconds of a stage with all places taken, and of a round besides its stages
 };
-constexpr Shape kShapes[] = {{256, 256, 256, 1.40}, {128, 128, 512, 0.84}, {64, 128, 768, 0.80}, {32, 128, 1024, 0.80}};
+constexpr Shape kShapes[] = {{256, 256, 256, 1.55, 8.0},
+                             {128, 128, 512, 1.00, 3.0},
+                             {128, 128, 256, 0.60, 6.0},
+                             {64, 128, 768, 0.80, 2.0},
+                             {32, 128, 1024, 0.80, 2.0}};
 
 struct Plan {
   int shape;
@@ -708,18 +760,22 @@ Plan plan_with(int shape, int64_t I, int64_t J, int64_t C) {
   p.c_part = part_stages * kBk;
   p.cut = parts > 1 ? (int)last : 0;
   p.whole = (int)tiles - p.cut;
-  // microseconds: a stage of a full CU, and the cut tiles' sums written and read again
+  // microseconds; the cut tiles' sums are written and read again by a second launch
   const double round = s.stage * stages;
-  p.cost = up(p.whole, s.places) * round;
-  if (p.cut) p.cost += round / (double)parts + 6.0 + p.cut * (double)parts * s.i * s.j * 8.0 / 4.0e6;
+  p.cost = up(p.whole, s.places) * (round + s.round);
+  if (p.cut) p.cost += round / (double)parts + 6.0 + p.cut * (double)parts * s.i * s.j * 8.0 / 3.0e6;
   return p;
 }
 
 Plan plan_of(int64_t I, int64_t J, int64_t C) {
-  if (I <= 32) return plan_with(3, I, J, C);
-  if (I <= 64) return plan_with(2, I, J, C);
-  const Plan a = plan_with(0, I, J, C), b = plan_with(1, I, J, C);
-  return a.cost <= b.cost ? a : b;
+  if (I <= 32) return plan_with(4, I, J, C);
+  if (I <= 64) return plan_with(3, I, J, C);
+  Plan best = plan_with(0, I, J, C);
+  for (int shape = 1; shape <= 2; ++shape) {
+    const Plan p = plan_with(shape, I, J, C);
+    if (p.cost < best.cost) best = p;
+  }
+  return best;
 }
 
 size_t plan_bytes(int64_t I, int64_t J, int64_t C) {
@@ -727,10 +783,10 @@ size_t plan_bytes(int64_t I, int64_t J, int64_t C) {
   return (size_t)p.cut * (size_t)p.parts * kShapes[p.shape].i * kShapes[p.shape].j * sizeof(float);
 }
 
-template <typename T, bool kTurnA, bool kTurnB, int kI, int kJ, int kWi, int kWj>
+template <typename T, bool kTurnA, bool kTurnB, int kI, int kJ, int kWi, int kWj, int kDepth>
 hipError_t launch_tiles(const Plan& p, GemmArgs& g, hipStream_t stream) {
   void* args[] = {&g};
-  const hipError_t e = hipLaunchKernel((const void*)&gemm_kernel<T, kI, kJ, kWi, kWj, kTurnA, kTurnB>,
+  const hipError_t e = hipLaunchKernel((const void*)&gemm_kernel<T, kI, kJ, kWi, kWj, kDepth, kTurnA, kTurnB>,
                                        dim3((unsigned)(p.whole + p.cut * p.parts)), dim3(kWi * kWj * 64), args, 0, stream);
   if (e != hipSuccess || p.cut == 0) return e;
   return hipLaunchKernel((const void*)&gemm_join_kernel<T, kI, kJ>, dim3(kI * kJ / 8 / kJoinThreads, (unsigned)p.cut),
@@ -746,10 +802,11 @@ hipError_t launch_gemm(GemmArgs g, hipStream_t stream) {
   g.parts = p.parts;
   g.c_part = p.c_part;
   switch (p.shape) {
-    case 0: return launch_tiles<T, kTurnA, kTurnB, 256, 256, 2, 4>(p, g, stream);
-    case 1: return launch_tiles<T, kTurnA, kTurnB, 128, 128, 2, 2>(p, g, stream);
-    case 2: return launch_tiles<T, kTurnA, kTurnB, 64, 128, 1, 4>(p, g, stream);
-    default: return launch_tiles<T, kTurnA, kTurnB, 32, 128, 1, 4>(p, g, stream);
+    case 0: return launch_tiles<T, kTurnA, kTurnB, 256, 256, 2, 4, 2>(p, g, stream);
+    case 1: return launch_tiles<T, kTurnA, kTurnB, 128, 128, 2, 2, 2>(p, g, stream);
+    case 2: return launch_tiles<T, kTurnA, kTurnB, 128, 128, 2, 2, 4>(p, g, stream);
+    case 3: return launch_tiles<T, kTurnA, kTurnB, 64, 128, 1, 4, 2>(p, g, stream);
+    default: return launch_tiles<T, kTurnA, kTurnB, 32, 128, 1, 4, 2>(p, g, stream);
   }
 }
 

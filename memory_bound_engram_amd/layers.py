@@ -208,9 +208,9 @@ def engram_linear_bwd(grad_y, x, w, grad_x, grad_w, workspace, z=None, grad_bias
     code = _act(act)
     if code and z is None:
         raise ValueError(f"z: the backward of {act} needs the forward's z")
-    pg, ldgy = a.rows("grad_y", grad_y, dt, (N, M), M)
     px, ldx = a.rows("x", x, _HALVES, (N, K), K)
     pw = a.dense("w", w, dt, (M, K))
+    pg, ldgy = a.rows("grad_y", grad_y, dt, (N, M), M)
     pz, ldz = a.rows("z", z, dt, (N, M), M)
     pgx, ldgx = a.rows("grad_x", grad_x, dt, (N, K), K)
     pgw = a.dense("grad_w", grad_w, dt, (M, K))

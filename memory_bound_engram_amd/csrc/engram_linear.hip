@@ -106,7 +106,7 @@ __device__ __forceinline__ void act8(float (&v)[8]) {
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
-    case ENGRAM_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case ENGRAM_ACT_RELU: return z <= 0.0f ? 0.0f : 1.0f;
     case ENGRAM_ACT_SILU: {
       if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;
       const float p = sigmoid(z);
@@ -680,8 +680,9 @@ __global__ __launch_bounds__(kGradThreads) void act_grad_kernel(const uint16_t* 
       if (act != ENGRAM_ACT_NONE) {
         float zz[8];
         unpack8<T>(load16_stream(z + n * ldz + j), zz);
+        // (relu passes nothing on below zero, also of an infinite gradient, whose product with 0 is NaN)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= act_slope(zz[k], act);
+        for (int k = 0; k < 8; ++k) v[k] = act == ENGRAM_ACT_RELU && zz[k] <= 0.0f ? 0.0f : v[k] * act_slope(zz[k], act);
         store16(dz + n * M + j, pack8<T>(v));
       }
 #pragma unroll

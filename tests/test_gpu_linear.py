@@ -252,6 +252,19 @@ def test_activations_at_the_ends(gpu, act):
     assert torch.allclose(gb, torch.tensor([0, 0, 0, half, half, 1, 1, 1], device=gpu), atol=1e-6), gb
 
 
+def test_relu_masks_infinite_gradients(gpu):
+    """Where z is at most 0 nothing passes, also of an infinity or NaN in grad_y; a NaN in z passes on."""
+    inf, nan = math.inf, math.nan
+    z = torch.tensor([[-1.0, -0.0, 0.0, 2.0, -inf, inf, nan, 1.0]], device=gpu).to(BF)
+    gy = torch.tensor([[inf, nan, -inf, 3.0, nan, 5.0, 7.0, -inf]], device=gpu).to(BF)
+    w = torch.eye(8, device=gpu).to(BF)
+    gb = poisoned((8,), torch.float32, gpu)
+    ws = buffer(eg.engram_linear_bwd_workspace_bytes(1, 8, 8), gpu)
+    eg.engram_linear_bwd(gy, torch.zeros((1, 8), dtype=BF, device=gpu), w, None, None, ws, z=z, grad_bias=gb, act="relu")
+    torch.cuda.synchronize()
+    assert gb.tolist() == [0.0, 0.0, 0.0, 3.0, 0.0, 5.0, 7.0, -inf], gb
+
+
 def test_into_kv_and_through_the_gate(gpu):
     """The projections written straight into kv's columns feed the gate; the
     gate's grad_kv goes back through them: each step as if done alone."""

@@ -123,7 +123,7 @@ def test_correct_arguments_are_refused_only_for_their_device(f):
         getattr(eg, f)(**CALLS[f]())
     with pytest.raises(AssertionError, match="reached the library"):  # and pass every check if they say they are there
         with pytest.MonkeyPatch.context() as m:
-            m.setattr(torch.cuda, "current_device", lambda: 0)
+            m.setattr(eg.layers, "_device", lambda: 0)
             getattr(eg, f)(**{n: gpu(t) if isinstance(t, torch.Tensor) else t for n, t in CALLS[f]().items()}, stream=0)
 
 

@@ -25,7 +25,14 @@
 // call has too few heads and sequences to fill the chip, the axis is cut into
 // segments: a first kernel walks each segment for its state alone, a second
 // joins the states from left to right, and the walk starts each segment from
-// its joined state.
+// its joined state.  The backward's three walks (and its two state passes) are
+// one launch each: they read the same rows, which the caches then serve, and
+// short calls pay for one launch (300 tokens, 40 heads: 35 us, 66 apart).
+//
+// Bounds.  The forward of 41444 tokens in 7 sequences, 40 heads of 128 x 128,
+// takes 700 us: the walk 440 for the 1.7 GB it reads and writes, 3.9 TB/s (411
+// with the state's products left out: memory bounds it), the state pass 200
+// for the 0.6 GB that it reads again (143 without its products), the join 10.
 //
 // Rounding.  bf16 operands enter the matrix cores as they are; sums are fp32.
 // The scores (times their power of the decay) and X are rounded to bf16 where
@@ -199,6 +206,13 @@ struct WalkArgs {
   bool state_t, carry_t;       // state_in/state_out, carry are stored [Dc][Da]
   int e;
   float s_intra, s_inter, s_upd;
+};
+
+// Walks over the same tokens and heads that one launch makes.
+constexpr int kMostWalks = 3;
+struct Walks {
+  WalkArgs w[kMostWalks];
+  int n, pairs;  // walks; segments times heads of each
 };
 
 namespace {
@@ -384,6 +398,8 @@ struct Walk {
   // Walk the rows [pos, stop) of one sequence, chunk by chunk.
   static __device__ __forceinline__ void rows(Lds& lds, State& X, int64_t pos, int64_t stop, int head, const float ld,
                                               const Powers& pw, int& parity, const WalkArgs& w, uint32_t wave, uint32_t lane0) {
+    const Columns<kDa> bs(lane0);
+    const AccOrder<kDa> as(lane0);
     int64_t single = pos;  // rows before this one are walked one at a time
     int L = (int)(stop - pos < kChunk ? stop - pos : kChunk), at_b = 0;
     auto get_b = [&](int to, int64_t at, int n, uint32_t lane) {
@@ -466,7 +482,6 @@ struct Walk {
         f32x4 y[4];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4{0, 0, 0, 0};
-        const AccOrder<kDa> as(lane);
         unrolled<kDa / 32>([&](auto kk) {
           constexpr int kKk = decltype(kk)::value;
           __builtin_amdgcn_sched_barrier(0);
@@ -511,7 +526,6 @@ struct Walk {
       for (int dt = 0; dt < kDt; ++dt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) X[dt][r] = fmaf(X[dt][r], less_one, X[dt][r]);
-      const Columns<kDa> bs(lane);
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         bf16x8 cs[3];
@@ -539,11 +553,12 @@ struct Walk {
     __syncthreads();  // the tiles are read out
   }
 
-  static __device__ __forceinline__ void run(const WalkArgs& w) {
+  // pair: the segment and the head
+  static __device__ __forceinline__ void run(const WalkArgs& w, int pair) {
     __shared__ __attribute__((aligned(16))) Lds lds;
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int head = blockIdx.x % w.H;
-    const int64_t seg = blockIdx.x / w.H;
+    const int head = pair % w.H;
+    const int64_t seg = pair / w.H;
     const float ld = uniform(w.log_decay[head]) * kLog2e;  // to base 2
     const Sequences seqs{w.cu, w.N, w.B, w.turned};
     const int64_t from = seg * w.seg, to = from + w.seg < w.N ? from + w.seg : w.N;
@@ -579,8 +594,10 @@ struct Walk {
 };
 
 template <int kDa, int kDc, bool kStateOnly>
-__global__ __launch_bounds__(kDc * 4, kDc / 32) void decay_walk_kernel(WalkArgs w) {
-  Walk<kDa, kDc, kStateOnly>::run(w);
+__global__ __launch_bounds__(kDc * 4, kDc / 32) void decay_walk_kernel(Walks s) {
+  // the walks of a pair run on one XCD (workgroups go round the eight) at about the same time
+  const int walk = blockIdx.x / 8 % s.n, pair = blockIdx.x / (8 * s.n) * 8 + blockIdx.x % 8;
+  if (pair < s.pairs) Walk<kDa, kDc, kStateOnly>::run(s.w[walk], pair);
 }
 
 // The states that segments start from: carry[j] holds what segment j - 1 alone
@@ -731,12 +748,27 @@ WalkKernel walk_kernel(int Da, int Dc) {
 
 int64_t segments(int64_t N, int64_t seg) { return (N + seg - 1) / seg; }
 
+// The walks of one call; those of the same widths in one launch.
 template <bool kStateOnly>
-hipError_t launch_walk(WalkArgs w, hipStream_t stream) {
-  const WalkKernel k = walk_kernel<kStateOnly>(w.Da, w.Dc);
-  const int64_t n = segments(w.N, w.seg) - (kStateOnly ? 1 : 0);  // the last segment leaves no state to another
-  void* args[] = {&w};
-  return hipLaunchKernel(k.kernel, dim3((unsigned)(n * w.H)), dim3((unsigned)k.threads), args, 0, stream);
+hipError_t launch_walks(const WalkArgs* w, int n, hipStream_t stream) {
+  bool done[kMostWalks] = {};
+  for (int i = 0; i < n; ++i) {
+    if (done[i]) continue;
+    const WalkKernel k = walk_kernel<kStateOnly>(w[i].Da, w[i].Dc);
+    Walks s{};
+    for (int j = i; j < n; ++j)
+      if (walk_kernel<kStateOnly>(w[j].Da, w[j].Dc).kernel == k.kernel) {
+        done[j] = true;
+        s.w[s.n++] = w[j];
+      }
+    // (the last segment leaves no state to another)
+    s.pairs = (int)((segments(w[i].N, w[i].seg) - (kStateOnly ? 1 : 0)) * w[i].H);
+    void* args[] = {&s};
+    const hipError_t e =
+        hipLaunchKernel(k.kernel, dim3((unsigned)((s.pairs + 7) / 8 * 8 * s.n)), dim3((unsigned)k.threads), args, 0, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 hipError_t launch_join(WalkArgs w, hipStream_t stream) {
   void* args[] = {&w};
@@ -745,28 +777,36 @@ hipError_t launch_join(WalkArgs w, hipStream_t stream) {
                          dim3(kJoinThreads), args, 0, stream);
 }
 // The states of a cut axis, and the states of empty sequences.
-hipError_t launch_carries(const WalkArgs& w, hipStream_t stream) {
-  hipError_t e = hipSuccess;
-  if (segments(w.N, w.seg) > 1) e = launch_walk<true>(w, stream);
-  if (e == hipSuccess && (segments(w.N, w.seg) > 1 || w.state_out)) e = launch_join(w, stream);
+hipError_t launch_carries(const WalkArgs* w, int n, hipStream_t stream) {
+  const bool cut = segments(w[0].N, w[0].seg) > 1;
+  hipError_t e = cut ? launch_walks<true>(w, n, stream) : hipSuccess;
+  for (int i = 0; i < n && e == hipSuccess; ++i)
+    if (cut || w[i].state_out) e = launch_join(w[i], stream);
   return e;
 }
 
 }  // namespace
 
 // Tokens of a segment: as many segments as fit the chip at once (two
-// workgroups a CU), since one more would be a second round.
-int64_t decay_segment(int64_t N, int64_t H) {
+// workgroups a CU) for all walks of a call, since one more would be a second
+// round (9500 tokens, 32 heads of 128 x 128, backward: 337 us with the three
+// walks in one round of 5 segments, 367 in three rounds of 15, 385 in three
+// launches; 41444 tokens, 40 heads, forward: 710 us with the 12 segments that fit,
+// 774 with 6, 737 with 25).
+int64_t decay_segment(int64_t N, int64_t H, int64_t walks) {
   constexpr int64_t kPlaces = 512;
-  const int64_t want = H < kPlaces ? kPlaces / H : 1;  // segments
+  const int64_t want = walks * H < kPlaces ? kPlaces / (walks * H) : 1;  // segments
   int64_t seg = (N + want - 1) / want;
   seg = (seg + kChunk - 1) / kChunk * kChunk;
   return seg < 2 * kChunk ? 2 * kChunk : seg;
 }
 
-size_t decay_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv) {
-  return (size_t)segments(N, decay_segment(N, H)) * (size_t)H * (size_t)Dk * (size_t)Dv * sizeof(float);
+// A state for each segment and head: of the forward, and of one direction of the backward.
+size_t carry_bytes(int64_t N, int64_t H, int64_t Dk, int64_t Dv, int64_t walks) {
+  return (size_t)segments(N, decay_segment(N, H, walks)) * (size_t)H * (size_t)Dk * (size_t)Dv * sizeof(float);
 }
+size_t decay_fwd_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv) { return carry_bytes(N, H, Dk, Dv, 1); }
+size_t decay_bwd_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv) { return 2 * carry_bytes(N, H, Dk, Dv, 3); }
 
 hipError_t launch_decay_fwd(const DecayCall& d, hipStream_t stream) {
   WalkArgs w{};
@@ -774,22 +814,22 @@ hipError_t launch_decay_fwd(const DecayCall& d, hipStream_t stream) {
   w.lda = d.ldq; w.ldb = d.ldk; w.ldc = d.ldv; w.ldy = d.ldo;
   w.log_decay = d.log_decay; w.cu = d.cu; w.state_in = d.state_in; w.state_out = d.state_out;
   w.carry = static_cast<float*>(d.workspace);
-  w.N = d.N; w.seg = decay_segment(d.N, d.H);
+  w.N = d.N; w.seg = decay_segment(d.N, d.H, 1);
   w.B = (int)d.B; w.H = (int)d.H; w.Da = (int)d.Dk; w.Dc = (int)d.Dv;
   w.e = 1;
   w.s_intra = w.s_inter = d.scale;
   w.s_upd = 1.0f;
-  hipError_t e = launch_carries(w, stream);
-  return e == hipSuccess ? launch_walk<false>(w, stream) : e;
+  const hipError_t e = launch_carries(&w, 1, stream);
+  return e == hipSuccess ? launch_walks<false>(&w, 1, stream) : e;
 }
 
 hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream) {
-  // dq: forward in time, the state transposed
-  WalkArgs w{};
+  WalkArgs w{}, all[3];
   w.log_decay = d.log_decay; w.cu = d.cu;
-  w.carry = static_cast<float*>(d.workspace);
-  w.N = d.N; w.seg = decay_segment(d.N, d.H);
+  w.N = d.N; w.seg = decay_segment(d.N, d.H, 3);
   w.B = (int)d.B; w.H = (int)d.H;
+  // dq: forward in time, the state transposed
+  w.carry = static_cast<float*>(d.workspace);
   w.a = d.grad_o; w.b = d.v; w.c = d.k; w.y = d.grad_q;
   w.lda = d.ldgo; w.ldb = d.ldv; w.ldc = d.ldk; w.ldy = d.ldgq;
   w.Da = (int)d.Dv; w.Dc = (int)d.Dk;
@@ -797,10 +837,9 @@ hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream) {
   w.e = 1;
   w.s_intra = w.s_inter = d.scale;
   w.s_upd = 1.0f;
-  hipError_t e = launch_carries(w, stream);
-  if (e == hipSuccess) e = launch_walk<false>(w, stream);
-  if (e != hipSuccess) return e;
+  all[0] = w;
   // dv: against time; this walk's last states are the gradients of state_in
+  w.carry += carry_bytes(d.N, d.H, d.Dk, d.Dv, 3) / sizeof(float);
   w.turned = true;
   w.a = d.k; w.b = d.q; w.c = d.grad_o; w.y = d.grad_v;
   w.lda = d.ldk; w.ldb = d.ldq; w.ldc = d.ldgo; w.ldy = d.ldgv;
@@ -809,15 +848,15 @@ hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream) {
   w.e = 0;
   w.s_inter = 1.0f;
   w.s_upd = d.scale;
-  e = launch_carries(w, stream);
-  if (e == hipSuccess) e = launch_walk<false>(w, stream);
-  if (e != hipSuccess) return e;
+  all[1] = w;
   // dk: the same states, transposed
   w.a = d.v; w.b = d.grad_o; w.c = d.q; w.y = d.grad_k;
   w.lda = d.ldv; w.ldb = d.ldgo; w.ldc = d.ldq; w.ldy = d.ldgk;
   w.Da = (int)d.Dv; w.Dc = (int)d.Dk;
   w.state_out = nullptr; w.state_t = true; w.carry_t = true;
-  return launch_walk<false>(w, stream);
+  all[2] = w;
+  const hipError_t e = launch_carries(all, 2, stream);
+  return e == hipSuccess ? launch_walks<false>(all, 3, stream) : e;
 }
 
 hipError_t launch_decay_step(const DecayCall& d, hipStream_t stream) {

@@ -99,7 +99,8 @@ struct DecayCall {
   int64_t ldq, ldk, ldv, ldo, ldgo, ldgq, ldgk, ldgv;
   float scale;
 };
-size_t decay_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv);
+size_t decay_fwd_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv);
+size_t decay_bwd_workspace(int64_t N, int64_t H, int64_t Dk, int64_t Dv);
 hipError_t launch_decay_fwd(const DecayCall& d, hipStream_t stream);
 hipError_t launch_decay_bwd(const DecayCall& d, hipStream_t stream);
 hipError_t launch_decay_step(const DecayCall& d, hipStream_t stream);

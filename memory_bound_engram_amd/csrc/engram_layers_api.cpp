@@ -219,11 +219,12 @@ engram_status engram_rope_freqs(double theta, int64_t R, int64_t* freqs) {
 
 size_t engram_decay_attn_fwd_workspace_bytes(int64_t N, int64_t B, int64_t H, int64_t Dk, int64_t Dv) {
   if (!decay_sizes_ok(N, B, H, Dk, Dv) || !decay_dims_ok(Dk, Dv)) return 0;
-  return engram::decay_workspace(N, H, Dk, Dv);
+  return engram::decay_fwd_workspace(N, H, Dk, Dv);
 }
 
 size_t engram_decay_attn_bwd_workspace_bytes(int64_t N, int64_t B, int64_t H, int64_t Dk, int64_t Dv) {
-  return engram_decay_attn_fwd_workspace_bytes(N, B, H, Dk, Dv);
+  if (!decay_sizes_ok(N, B, H, Dk, Dv) || !decay_dims_ok(Dk, Dv)) return 0;
+  return engram::decay_bwd_workspace(N, H, Dk, Dv);
 }
 
 engram_status engram_decay_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -242,7 +243,7 @@ engram_status engram_decay_attn_fwd(const void* q, const void* k, const void* v,
   const Rows ins[] = {heads(q, N, ldq, H, Dk), heads(k, N, ldk, H, Dk),      heads(v, N, ldv, H, Dv),
                       flat(log_decay, H * 4),  flat(cu_seqlens, (B + 1) * 8), flat(state_in, states)};
   const Rows outs[] = {heads(o, N, ldo, H, Dv), flat(state_out, states),
-                       flat(workspace, (int64_t)engram::decay_workspace(N, H, Dk, Dv))};
+                       flat(workspace, (int64_t)engram::decay_fwd_workspace(N, H, Dk, Dv))};
   if (any_overlap(ins, 6, outs, 3)) return ENGRAM_ERR_OVERLAP;
   engram::DecayCall d{};
   d.q = static_cast<const uint16_t*>(q); d.k = static_cast<const uint16_t*>(k); d.v = static_cast<const uint16_t*>(v);
@@ -275,7 +276,8 @@ engram_status engram_decay_attn_bwd(const void* grad_o, const void* q, const voi
                       heads(v, N, ldv, H, Dv), flat(log_decay, H * 4), flat(cu_seqlens, (B + 1) * 8),
                       flat(state_in, states), flat(grad_state_out, states)};
   const Rows outs[] = {heads(grad_q, N, ldgq, H, Dk), heads(grad_k, N, ldgk, H, Dk), heads(grad_v, N, ldgv, H, Dv),
-                       flat(grad_state_in, states), flat(workspace, (int64_t)engram::decay_workspace(N, H, Dk, Dv))};
+                       flat(grad_state_in, states),
+                       flat(workspace, (int64_t)engram::decay_bwd_workspace(N, H, Dk, Dv))};
   if (any_overlap(ins, 8, outs, 5)) return ENGRAM_ERR_OVERLAP;
   engram::DecayCall d{};
   d.grad_o = static_cast<const uint16_t*>(grad_o);

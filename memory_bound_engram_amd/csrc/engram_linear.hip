@@ -720,9 +720,9 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // (128 x 2560 x 25600: 28 us against 36).  Few rows take 64 x 128 or 32 x 128,
 // three or four to a CU, whose LDS then holds more of W on its way.  Tiles that
 // fill whole rounds of the chip's places are made whole; those of the last,
-// partial round are cut along the contraction into as many parts as there are
-// places for, at least four stages each (512 x 5120 x 5120 in 128 x 128 tiles:
-// 47 us against 55 uncut; 4000 x 5120 x 5120: 196 against 245).
+// partial round may be cut along the contraction, into parts of at least four
+// stages (4000 x 5120 x 5120: 202 us against 234 uncut; 4096 x 25600 x 2560, 160
+// tiles of 256^2 in three parts: 557 against 612).
 // The cheapest by the costs below is taken, which were fitted to all three
 // shapes over fourteen sizes (256^2, 128^2 and 128^2 deep, us: 4000 x 5120 x 5120
 // 197, 208, 247; 2048 x 5120 x 5120 126, 110, 133; 1000 x 1368 x 5120 41, 27, 34;
@@ -736,6 +736,8 @@ constexpr Shape kShapes[] = {{256, 256, 256, 1.55, 8.0},
                              {128, 128, 256, 0.60, 6.0},
                              {64, 128, 768, 0.80, 2.0},
                              {32, 128, 1024, 0.80, 2.0}};
+
+constexpr int64_t kMostFill = 3;
 
 struct Plan {
   int shape;
@@ -752,19 +754,23 @@ Plan plan_with(int shape, int64_t I, int64_t J, int64_t C) {
   p.tj = (int)up(J, s.j);
   const int64_t tiles = (int64_t)p.ti * p.tj, stages = up(C, kBk);
   const int64_t last = tiles % s.places;
-  int64_t parts = last ? s.places / last : 1;
-  if (parts > stages / 4) parts = stages / 4;
-  if (parts < 1) parts = 1;
-  const int64_t part_stages = up(stages, parts);
-  parts = up(stages, part_stages);
-  p.parts = (int)parts;
-  p.c_part = part_stages * kBk;
-  p.cut = parts > 1 ? (int)last : 0;
+  // microseconds: full rounds, then the last tiles in as many parts as is cheapest; cut tiles' sums
+  // are written and read again by a second launch
+  const double whole = (double)(tiles / s.places) * (s.stage * stages + s.round);
+  for (int64_t fill = 0; fill <= kMostFill; ++fill) {
+    int64_t n = fill && last ? fill * s.places / last : 1;  // not cut, or to fill one, two, ... rounds
+    if (n > stages / 4) n = stages / 4;
+    if (n < 1) n = 1;
+    const int64_t part_stages = up(stages, n), parts = up(stages, part_stages);
+    const double rounds = (double)up(last * parts, s.places), bytes = (double)(last * parts) * s.i * s.j * 8.0;
+    const double cost = whole + rounds * s.stage * part_stages + (parts > 1 ? 8.0 + bytes / 4.0e6 : rounds * s.round);
+    if (fill && cost >= p.cost) continue;
+    p.cost = cost;
+    p.parts = (int)parts;
+    p.c_part = part_stages * kBk;
+    p.cut = parts > 1 ? (int)last : 0;
+  }
   p.whole = (int)tiles - p.cut;
-  // microseconds; the cut tiles' sums are written and read again by a second launch
-  const double round = s.stage * stages;
-  p.cost = up(p.whole, s.places) * (round + s.round);
-  if (p.cut) p.cost += round / (double)parts + 6.0 + p.cut * (double)parts * s.i * s.j * 8.0 / 3.0e6;
   return p;
 }
 

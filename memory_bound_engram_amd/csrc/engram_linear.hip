@@ -592,7 +592,7 @@ __global__ __launch_bounds__(kVecThreads) void vector_kernel(const uint16_t* x, 
 // y for N <= 16 rows of x and a small W.  A workgroup has 16 rows of W; its waves
 // take every kWaves-th piece of 64 contraction values, straight from memory into
 // the matrix cores, and join in LDS: one launch, where tiles would need a second
-// one to join a split contraction (13 x 5120 x 1368: 12.5 us against 15.5; at
+// one to join a split contraction (13 x 5120 x 1368: 12.0 us against 15.5; at
 // 131 MB of W the tiles' whole lines win, 33 us against 39).
 template <typename T, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, const uint16_t* w, int64_t ldx, int N,
@@ -606,29 +606,24 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, co
   const uint16_t* xr = x + (int64_t)min(l, N - 1) * ldx + 8 * g;
   f32x4 acc = {0, 0, 0, 0};
   const int pieces = (int)(K / 64);
-  constexpr int kAhead = 8;  // pieces whose loads are in flight together
-  int p = wave;
-  for (; p + (kAhead - 1) * kWaves < pieces; p += kAhead * kWaves) {
+  constexpr int kAhead = kWaves == 16 ? 6 : 8;  // pieces whose loads are in flight together, as registers allow
+  for (int p = wave; p < pieces; p += kAhead * kWaves) {
     u32x4 fw[kAhead][2], fx[kAhead][2];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
+    for (int u = 0; u < kAhead; ++u) {
+      if (p + u * kWaves >= pieces) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t at = (int64_t)(p + u * kWaves) * 64 + 32 * h;
         fw[u][h] = load16(wr + at);
         fx[u][h] = load16(xr + at);
       }
+    }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
+    for (int u = 0; u < kAhead; ++u) {
+      if (p + u * kWaves >= pieces) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) acc = T::mfma(fw[u][h], fx[u][h], acc);
-  }
-#pragma nounroll
-  for (; p < pieces; p += kWaves) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t at = (int64_t)p * 64 + 32 * h;
-      acc = T::mfma(load16(wr + at), load16(xr + at), acc);
     }
   }
   if (wave == pieces % kWaves) {  // what is left of K, a multiple of 8 below 64
@@ -706,6 +701,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* partial, fl
   const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (col >= M) return;
   float s = 0.0f;
+#pragma unroll 16  // so many loads on their way (M = 25600: 5 us, 17 one by one)
   for (int i = 0; i < slices; ++i) s += partial[i * M + col];
   db[col] = s;
 }

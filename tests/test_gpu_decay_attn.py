@@ -259,6 +259,45 @@ def test_later_rows_and_other_sequences_do_not_reach_back(gpu, bad):
             assert torch.equal(o[keep].view(torch.int16), clean[keep].view(torch.int16))
 
 
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_gradients_do_not_reach_forward(gpu, bad):
+    """The same of the backward: what is not finite at a token t reaches dq from t on (through k
+    and v) and dk and dv up to t (through q and grad_o), in its own sequence and head."""
+    lens, t = [150, 90], 100
+    c = case(lens, 2, 64, 64, gpu, False, seed=11)
+    clean = run_bwd(c, gpu)[:3]
+    bounds = bwd_bounds(c)[:3]
+    for what in ("do", "q", "k", "v"):
+        x = c[what].clone()
+        x[t, 1, 3] = bad
+        got = run_bwd(dict(c, **{what: x}), gpu)[:3]
+        for i, (name, g, keep) in enumerate(zip(("dq", "dk", "dv"), got, clean)):
+            assert torch.equal(g[:, 0].view(torch.int16), keep[:, 0].view(torch.int16)), (what, name)
+            assert torch.equal(g[150:].view(torch.int16), keep[150:].view(torch.int16)), (what, name)
+            rows = torch.ones(150, dtype=torch.bool)
+            reached = what in ("k", "v") if name == "dq" else what in ("q", "do")
+            if reached:
+                rows[(slice(t, None) if name == "dq" else slice(0, t + 1))] = False
+            rows[t] = False
+            want, bound = bounds[i]
+            check(f"{name} with {what}", g[:150][rows.to(gpu)], want[:150][rows].to(gpu), bound[:150][rows].to(gpu))
+
+
+@pytest.mark.parametrize("lens,h,dk,dv", [([70, 3], 600, 8, 8), ([900, 500], 40, 16, 24), ([400], 200, 72, 8)])
+def test_heads_that_fill_the_chip(gpu, lens, h, dk, dv):
+    """Many heads: the axis in few segments of many chunks each, or in one; other numbers of
+    them forward and backward."""
+    print(f"decay lens={lens} h={h} dk={dk} dv={dv}", flush=True)
+    c = case(lens, h, dk, dv, gpu, True, tail=2, seed=12)
+    m = sum(lens)
+    o, out = run_fwd(c, gpu)
+    (o64, oerr), (s64, serr) = fwd_bounds(c)
+    check("o", o[:m], o64.to(gpu), oerr.to(gpu))
+    check("state_out", out, s64.to(gpu), serr.to(gpu))
+    for i, (name, g, (want, bound)) in enumerate(zip(("dq", "dk", "dv", "ds_in"), run_bwd(c, gpu), bwd_bounds(c))):
+        check(name, g[:m] if i < 3 else g, want.to(gpu), bound.to(gpu))
+
+
 def test_bounds_of_sequences_that_lead_nowhere(gpu):
     """cu_seqlens of any content leads to no access outside the arrays: the call ends, and
     what belongs to nobody else is not written."""

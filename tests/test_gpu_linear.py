@@ -92,6 +92,11 @@ FWD = [
     (1025, 136, 392, BF, "gelu", True, True, False),
     (2049, 72, 6408, BF, "none", True, True, True),       # wide tiles
     (3333, 200, 4104, FP, "silu", False, False, False),
+    (3333, 200, 4104, FP, "none", True, True, False),     # nothing but a residual (and bias) to add: wide tiles,
+    (1500, 1032, 2568, BF, "none", False, True, False),   # ... two of 128 x 128 to a CU,
+    (190, 264, 520, BF, "none", True, True, False),       # ... one,
+    (100, 5000, 264, FP, "none", False, True, False),     # ... a split contraction
+    (600, 5120, 264, BF, "none", False, False, False),    # parts for more than one round
 ]
 
 

@@ -160,9 +160,10 @@ if _torch is not None:
 
 
 def _shape(name, t, dims):
-    if t.dim() != dims:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dims}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: {len(shape)} dimensions, expected {dims}")
+    return shape
 
 
 def _act(act):

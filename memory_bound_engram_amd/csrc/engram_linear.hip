@@ -589,36 +589,39 @@ __global__ __launch_bounds__(kVecThreads) void vector_kernel(const uint16_t* x, 
     static_cast<uint16_t*>(e.y)[n * e.ldy + m] = (uint16_t)T::pack(finish1<T>(mine, n, m, e), 0.0f);
 }
 
-// y for N <= 16 rows of x and a small W.  A workgroup has 16 rows of W; its waves
+// y for N <= 16 rows of x and a small W.  A workgroup has kR rows of W; its waves
 // take every kWaves-th piece of 64 contraction values, straight from memory into
 // the matrix cores, and join in LDS: one launch, where tiles would need a second
-// one to join a split contraction (13 x 5120 x 1368: 12.0 us against 15.5; at
-// 131 MB of W the tiles' whole lines win, 33 us against 39).
-template <typename T, int kWaves>
+// one to join a split contraction (13 x 5120 x 1368: 9.8 us against 15.5; at
+// 131 MB of W the tiles' whole lines win, 33 us against 39).  What a CU can ask
+// its cache for bounds it, 64 bytes of a row at a time: lanes whose rows are not
+// there ask for nothing (their sums, of whatever is in their registers, are in
+// rows and columns of the product that nobody reads).
+template <typename T, int kWaves, int kR>
 __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, const uint16_t* w, int64_t ldx, int N,
                                                            int64_t K, int64_t M, Epilogue e) {
   __shared__ f32x4 part[kWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane % 16, g = lane / 16;
-  const int64_t m0 = (int64_t)blockIdx.x * 16;
-  // rows behind the last one read the last one again; their sums are not stored
-  const uint16_t* wr = w + min(m0 + l, M - 1) * K + 8 * g;
-  const uint16_t* xr = x + (int64_t)min(l, N - 1) * ldx + 8 * g;
+  const int64_t m0 = (int64_t)blockIdx.x * kR;
+  const bool has_w = l < kR && m0 + l < M, has_x = l < N;
+  const uint16_t* wr = w + (has_w ? m0 + l : 0) * K + 8 * g;
+  const uint16_t* xr = x + (has_x ? (int64_t)l : 0) * ldx + 8 * g;
   f32x4 acc = {0, 0, 0, 0};
   const int pieces = (int)(K / 64);
   constexpr int kAhead = kWaves == 16 ? 6 : 8;  // pieces whose loads are in flight together, as registers allow
   for (int p = wave; p < pieces; p += kAhead * kWaves) {
     u32x4 fw[kAhead][2], fx[kAhead][2];
+    const auto load = [&](u32x4 (&to)[kAhead][2], const uint16_t* from) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (p + u * kWaves >= pieces) break;
+      for (int u = 0; u < kAhead; ++u) {
+        if (p + u * kWaves >= pieces) break;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = (int64_t)(p + u * kWaves) * 64 + 32 * h;
-        fw[u][h] = load16(wr + at);
-        fx[u][h] = load16(xr + at);
+        for (int h = 0; h < 2; ++h) to[u][h] = load16(from + (int64_t)(p + u * kWaves) * 64 + 32 * h);
       }
-    }
+    };
+    if (has_w) load(fw, wr);
+    if (has_x) load(fx, xr);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (p + u * kWaves >= pieces) break;
@@ -640,7 +643,7 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, co
   // lane: row of x l, four neighbouring rows of W; two lanes' fours make eight columns of y
   const int row = threadIdx.x % 16, half = threadIdx.x / 16;
   const int64_t j = m0 + 8 * half;
-  if (half >= 2 || row >= N || j >= M) return;
+  if (half >= kR / 8 || row >= N || j >= M) return;
   f32x4 s0 = part[0][row + 32 * half], s1 = part[0][row + 32 * half + 16];
 #pragma unroll 4
   for (int v = 1; v < kWaves; ++v) {
@@ -830,6 +833,12 @@ hipError_t launch_vector(const LinearCall& l, const Epilogue& e, hipStream_t str
                          dim3(kVecThreads), args, 0, stream);
 }
 
+template <typename T, int kWaves, int kR>
+hipError_t launch_rows(int64_t M, void** args, hipStream_t stream) {
+  return hipLaunchKernel((const void*)&rows_kernel<T, kWaves, kR>, dim3((unsigned)up(M, kR)), dim3(kWaves * 64), args, 0,
+                         stream);
+}
+
 template <typename T>
 hipError_t linear_fwd(const LinearCall& l, hipStream_t stream) {
   const Epilogue e{l.bias, l.residual, l.z, l.y, l.ldr, l.ldz, l.ldy, l.act};
@@ -847,10 +856,11 @@ hipError_t linear_fwd(const LinearCall& l, hipStream_t stream) {
     int N = (int)l.N;
     Epilogue ep = e;
     void* args[] = {&x, &w, &ldx, &N, &K, &M, &ep};
-    const unsigned grid = (unsigned)up(M, 16);
-    // waves of a workgroup: enough of them on the chip to keep its memory busy
-    if (grid >= 1024) return hipLaunchKernel((const void*)&rows_kernel<T, 4>, dim3(grid), dim3(256), args, 0, stream);
-    return hipLaunchKernel((const void*)&rows_kernel<T, 16>, dim3(grid), dim3(1024), args, 0, stream);
+    // waves of a workgroup: enough of them on the chip to keep its memory busy; rows of W: fewer where
+    // workgroups with 16 would leave half of the CUs idle (13 x 5120 x 1368: 9.8 us against 11.4)
+    if (M > 16 * 1024) return launch_rows<T, 4, 16>(M, args, stream);
+    if (M > 16 * 128) return launch_rows<T, 16, 16>(M, args, stream);
+    return launch_rows<T, 16, 8>(M, args, stream);
   }
   GemmArgs g{};
   g.a = static_cast<const uint16_t*>(l.x);

@@ -30,9 +30,9 @@
 // short calls pay for one launch (300 tokens, 40 heads: 35 us, 66 apart).
 //
 // Bounds.  The forward of 41444 tokens in 7 sequences, 40 heads of 128 x 128,
-// takes 700 us: the walk 440 for the 1.7 GB it reads and writes, 3.9 TB/s (411
-// with the state's products left out: memory bounds it), the state pass 200
-// for the 0.6 GB that it reads again (143 without its products), the join 10.
+// takes 692 us: the walk 430 for the 1.7 GB it reads and writes, 3.9 TB/s (20
+// less with the state's products left out: memory bounds it), the state pass 200
+// for the 0.5 GB that it reads again (143 without its products), the join 10.
 //
 // Rounding.  bf16 operands enter the matrix cores as they are; sums are fp32.
 // The scores (times their power of the decay) and X are rounded to bf16 where
@@ -49,6 +49,7 @@ namespace engram {
 namespace {
 
 constexpr int kChunk = 64;
+constexpr int kStreamed = 2;  // buffer stores: the line is not kept in the caches
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -265,24 +266,38 @@ struct Walk {
     int bad[2];
   };
 
+  // The 16-byte pieces of a tile that a lane moves, kMoves of them: the q-th lies
+  // at (q kWaves + wave) 1024 + 16 lane in the tile, and `at` bytes from the
+  // chunk's first row in memory (kBeyond if it is no part of it).
+  template <int kD>
+  struct Pieces {
+    static constexpr uint32_t kMoves = kD * kChunk / 8 / kThreads;
+    uint32_t at[kMoves];
+    __device__ __forceinline__ Pieces(int64_t ld, int d, int L, const WalkArgs& w, uint32_t wave, uint32_t lane) {
+      // a lane's rows are kRows apart, a multiple of 32 or of 16, with which the order of the pieces
+      // does not (or, at 16, by half of them) change
+      constexpr uint32_t kRows = kThreads / (kD / 8);
+      const uint32_t line = (uint32_t)ld * 2;
+      const uint32_t t0 = (wave * 64 + lane) / (kD / 8), piece = (wave * 64 + lane) % (kD / 8) ^ turn<kD>(t0);
+      const uint32_t first = token_of(t0, L, w) * line, step = w.turned ? 0 - kRows * line : kRows * line;
+#pragma unroll
+      for (uint32_t q = 0; q < kMoves; ++q) {
+        const uint32_t col = (piece ^ turn<kD>(q * kRows)) * 8;
+        const bool in = (t0 + q * kRows >= kChunk - (uint32_t)L) & (col < (uint32_t)d);
+        at[q] = in ? first + q * step + col * 2 : kBeyond;
+      }
+    }
+  };
   // Rows pos .. pos + L - 1 of the head, straight into LDS as the tile's last L
   // rows, the rows before them zero.
   template <int kD>
   static __device__ __forceinline__ void fetch(const uint16_t* tile, const uint16_t* x, int64_t ld, int head, int d,
                                                int64_t pos, int L, const WalkArgs& w, uint32_t wave, uint32_t lane) {
     const u32x4 src = buffer_words(x + (w.turned ? w.N - pos - L : pos) * ld + (int64_t)head * d);
-    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile, line = (uint32_t)ld * 2;
-    // a lane's rows are kRows apart, a multiple of 32 or of 16, with which the order of the pieces
-    // does not (or, at 16, by half of them) change
-    constexpr uint32_t kLoads = kD * kChunk / 8 / kThreads, kRows = kThreads / (kD / 8);
-    const uint32_t t0 = (wave * 64 + lane) / (kD / 8), piece = (wave * 64 + lane) % (kD / 8) ^ turn<kD>(t0);
-    const uint32_t first = token_of(t0, L, w) * line, step = w.turned ? 0 - kRows * line : kRows * line;
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile;
+    const Pieces<kD> p(ld, d, L, w, wave, lane);
 #pragma unroll
-    for (uint32_t q = 0; q < kLoads; ++q) {
-      const uint32_t col = (piece ^ turn<kD>(q * kRows)) * 8;
-      const bool in = (t0 + q * kRows >= kChunk - (uint32_t)L) & (col < (uint32_t)d);
-      load_to_lds(to + (q * kWaves + wave) * 1024, src, in ? first + q * step + col * 2 : kBeyond);
-    }
+    for (uint32_t q = 0; q < p.kMoves; ++q) load_to_lds(to + (q * kWaves + wave) * 1024, src, p.at[q]);
   }
   // The token of a tile's row t, from the chunk's first token in memory.
   static __device__ __forceinline__ uint32_t token_of(uint32_t t, int L, const WalkArgs& w) {
@@ -502,23 +517,25 @@ struct Walk {
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int tt = 2 * kt; tt < 4; ++tt) y[tt] = mfma(cf[kt], frag_rows<kChunk>(lds.p, 16 * tt, 32 * kt, lane), y[tt]);
-        const __amdgpu_buffer_rsrc_t dst =
-            buffer_of(w.y + (w.turned ? w.N - pos - L : pos) * w.ldy + (int64_t)head * w.Dc);
-        const uint32_t n = 16 * wave + 4 * g, line = (uint32_t)w.ldy * 2;
-        const uint32_t first = token_of(l, L, w) * line + 2 * n;
-        const bool in = n < (uint32_t)w.Dc;
-        const uint32_t step = w.turned ? 0 - 16 * line : 16 * line;
+        // y goes out through c's tile, which is in registers: a wave has sixteen columns, 32 bytes of a
+        // row, and whole lines are fewer requests and need not stay in the caches (41444 tokens, 40 heads
+        // of 128 x 128: 692 us against 707; backward of 9500 tokens, 32 heads: 307 against 328)
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
-          __builtin_amdgcn_raw_buffer_store_b64(
-              pack4(y[tt]), dst, (int)(((16 * tt + l >= kChunk - (uint32_t)L) & in) ? first + tt * step : kBeyond), 0, 0);
-      }
-      if constexpr (!kStateOnly) {
-        __syncthreads();  // a and c are read out
-        if (next < stop) {
-          get_c(0, next, next_L, lane);
-          get_a(next, next_L, lane);
-        }
+          *reinterpret_cast<u32x2*>(lds.c[0] + place<kDc>(16 * tt + l, 16 * wave + 4 * g)) = pack4(y[tt]);
+        __syncthreads();  // y is there, a read out
+        if (next < stop) get_a(next, next_L, lane);
+        const Pieces<kDc> out(w.ldy, w.Dc, L, w, wave, lane);
+        u32x4 rows[out.kMoves];
+#pragma unroll
+        for (uint32_t q = 0; q < out.kMoves; ++q) rows[q] = load16(lds.c[0] + (q * kWaves + wave) * 512 + 8 * lane);
+        __syncthreads();  // y is read out
+        if (next < stop) get_c(0, next, next_L, lane);
+        const __amdgpu_buffer_rsrc_t dst =
+            buffer_of(w.y + (w.turned ? w.N - pos - L : pos) * w.ldy + (int64_t)head * w.Dc);
+#pragma unroll
+        for (uint32_t q = 0; q < out.kMoves; ++q)
+          __builtin_amdgcn_raw_buffer_store_b128(rows[q], dst, (int)out.at[q], 0, kStreamed);
       }
       // X = lam^L X + s_upd sum_s lam^(L-e-s) b_s c_s^T
       const float less_one = L == kChunk ? pw.less_one : uniform(expm1f(ld * (kLn2 * (float)L)));
@@ -789,7 +806,7 @@ hipError_t launch_carries(const WalkArgs* w, int n, hipStream_t stream) {
 
 // Tokens of a segment: as many segments as fit the chip at once (two
 // workgroups a CU) for all walks of a call, since one more would be a second
-// round (9500 tokens, 32 heads of 128 x 128, backward: 337 us with the three
+// round (9500 tokens, 32 heads of 128 x 128, backward, before whole-line stores: 337 us with the three
 // walks in one round of 5 segments, 367 in three rounds of 15, 385 in three
 // launches; 41444 tokens, 40 heads, forward: 710 us with the 12 segments that fit,
 // 774 with 6, 737 with 25).

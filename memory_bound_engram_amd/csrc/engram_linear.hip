@@ -440,10 +440,15 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
           *reinterpret_cast<f32x4*>(p + kApart) = acc[m][n + 1];
           continue;
         }
-        uint16_t* p = static_cast<uint16_t*>(g.e.y) + (i0 + ii) * g.e.ldy + j0 + jj;
+        uint16_t* p = static_cast<uint16_t*>(g.e.y) + (i0 + ii) * g.e.ldy + j0;
         if constexpr (kTurnB) {
-          if (j0 + jj < g.J) *reinterpret_cast<u32x2*>(p) = pack4<T>(acc[m][n]);
-          if (j0 + jj + 16 < g.J) *reinterpret_cast<u32x2*>(p + 16) = pack4<T>(acc[m][n + 1]);
+          // four columns of each of two sixteens become eight neighbours of one: every other sixteen
+          // lanes change over (25600 x 4096 x 2560: 450 us against 458 with stores of four)
+          const u32x2 x = pack4<T>(acc[m][n]), y = pack4<T>(acc[m][n + 1]);
+          const u32x2 u = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+          const u32x2 v = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+          const int j = wj + n * 16 + 16 * (lane / 16 % 2) + 8 * (lane / 32);
+          if (j0 + j < g.J) store16(p + j, u32x4{u[0], v[0], u[1], v[1]});
         } else if (j0 + jj < g.J) {
           float v[8];
 #pragma unroll
@@ -451,7 +456,7 @@ __global__ __launch_bounds__(kWi* kWj * 64) void gemm_kernel(GemmArgs g) {
             v[k] = acc[m][n][k] + bias[k];
             v[k + 4] = acc[m][n + 1][k] + bias[k + 4];
           }
-          store16(p, pack8<T>(v));
+          store16(p + jj, pack8<T>(v));
         }
       }
     }

@@ -806,10 +806,10 @@ hipError_t launch_carries(const WalkArgs* w, int n, hipStream_t stream) {
 
 // Tokens of a segment: as many segments as fit the chip at once (two
 // workgroups a CU) for all walks of a call, since one more would be a second
-// round (9500 tokens, 32 heads of 128 x 128, backward, before whole-line stores: 337 us with the three
+// round (9500 tokens, 32 heads of 128 x 128, backward: 337 us with the three
 // walks in one round of 5 segments, 367 in three rounds of 15, 385 in three
-// launches; 41444 tokens, 40 heads, forward: 710 us with the 12 segments that fit,
-// 774 with 6, 737 with 25).
+// launches; 41444 tokens, 40 heads, forward: 710 us with the 12 segments that
+// fit, 774 with 6, 737 with 25; all before y went out in whole lines).
 int64_t decay_segment(int64_t N, int64_t H, int64_t walks) {
   constexpr int64_t kPlaces = 512;
   const int64_t want = walks * H < kPlaces ? kPlaces / (walks * H) : 1;  // segments

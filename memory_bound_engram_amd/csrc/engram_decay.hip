@@ -42,6 +42,7 @@
 // bf16 values, 24 bits, which is all of it (two leave 2.5e-6 of the state).
 #include "engram_device.h"
 #include "engram_launch.h"
+#include "engram_layers_device.h"
 
 #include <utility>
 
@@ -184,10 +185,6 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
   const int32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | lo);
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0x80000000u, 0x00020000);
 }
 
 }  // namespace

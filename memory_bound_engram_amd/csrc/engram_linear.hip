@@ -19,6 +19,7 @@
 // own takes whole rows of it with plain fp32 products.
 #include "engram_device.h"
 #include "engram_launch.h"
+#include "engram_layers_device.h"
 
 #include <type_traits>
 

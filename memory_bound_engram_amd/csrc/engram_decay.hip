@@ -167,6 +167,30 @@ __device__ __forceinline__ float decay_power(float log2_decay, int steps) {
 }
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
+// The power of the decay that a state is multiplied with, chunk after chunk.
+// One fp32 value of it is off by up to 3e-8, for every chunk to the same side; so
+// what each rounding drops is carried into the next chunk's, and the product of
+// all of them stays within 6e-8.  Below 1/2 there is nothing to carry: the
+// product vanishes before it would show.  (lam^steps - 1, added to the state in
+// place of a factor, would keep the digits near 1 as well, but lose those of a
+// small power, a hundredth of 3e-6, and turn an infinite state into NaN.)
+struct Power {
+  float near, rest, inverse;  // lam^steps rounded, what that dropped and 1 over it
+  __device__ __forceinline__ void set(float log2_decay, float steps) {
+    const float x = log2_decay * steps, less_one = expm1f(x * kLn2);
+    const bool small = !(x >= -1.0f);
+    near = small ? __builtin_amdgcn_exp2f(x) : 1.0f + less_one;
+    inverse = small ? 0.0f : __builtin_amdgcn_rcpf(near);
+    rest = small ? 0.0f : (less_one - (near - 1.0f)) * inverse;  // the difference is exact
+  }
+  // The factor, given what the factors before it dropped, and what is dropped now (both relative).
+  __device__ __forceinline__ float factor(float& dropped) const {
+    const float all = dropped + rest, f = fmaf(near, all, near);
+    dropped = all - (f - near) * inverse;
+    return f;
+  }
+};
+
 // The lane's number as a value the compiler knows nothing of: what is computed
 // from it stays where it is used, instead of moving out of loops and being
 // spilled.
@@ -181,6 +205,7 @@ __device__ __forceinline__ float afresh(float v) {
 
 // A value that all lanes share, in a scalar register.
 __device__ __forceinline__ float uniform(float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); }
+__device__ __forceinline__ Power uniform(Power p) { return Power{uniform(p.near), uniform(p.rest), uniform(p.inverse)}; }
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
   const int32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
@@ -370,14 +395,15 @@ struct Walk {
     float tiles[3];      // lam^(16 i)
     float rows[2];       // s_upd lam^(57-e-32kt-8g)
     float eight[8];      // lam^i
-    float less_one;      // lam^64 - 1
+    Power chunk;         // lam^64
     __device__ __forceinline__ void set(float ld, const WalkArgs& w, uint32_t lane0) {
       const int lane = (int)lane0, g = lane / 16, l = lane % 16;
       below = w.s_intra * decay_power(ld, 13 + l - 4 * g);
       for (int i = 0; i < 3; ++i) tiles[i] = uniform(decay_power(ld, 16 * i));
       for (int kt = 0; kt < 2; ++kt) rows[kt] = w.s_upd * decay_power(ld, kChunk - 7 - w.e - 32 * kt - 8 * g);
       for (int i = 0; i < 8; ++i) eight[i] = uniform(decay_power(ld, i));
-      less_one = uniform(expm1f(ld * (kLn2 * (float)kChunk)));
+      chunk.set(ld, kChunk);
+      chunk = uniform(chunk);
     }
   };
 
@@ -413,6 +439,7 @@ struct Walk {
     const Columns<kDa> bs(lane0);
     const AccOrder<kDa> as(lane0);
     int64_t single = pos;  // rows before this one are walked one at a time
+    float dropped = 0.0f;  // by the factors of X so far
     int L = (int)(stop - pos < kChunk ? stop - pos : kChunk), at_b = 0;
     auto get_b = [&](int to, int64_t at, int n, uint32_t lane) {
       fetch<kDa>(lds.b[to], w.b, w.ldb, head, w.Da, at, n, w, wave, lane);
@@ -535,11 +562,13 @@ struct Walk {
           __builtin_amdgcn_raw_buffer_store_b128(rows[q], dst, (int)out.at[q], 0, kStreamed);
       }
       // X = lam^L X + s_upd sum_s lam^(L-e-s) b_s c_s^T
-      const float less_one = L == kChunk ? pw.less_one : uniform(expm1f(ld * (kLn2 * (float)L)));
+      Power power = pw.chunk;
+      if (L != kChunk) power.set(ld, (float)L);
+      const float keep = uniform(power.factor(dropped));
 #pragma unroll
       for (int dt = 0; dt < kDt; ++dt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) X[dt][r] = fmaf(X[dt][r], less_one, X[dt][r]);
+        for (int r = 0; r < 4; ++r) X[dt][r] *= keep;
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         bf16x8 cs[3];
@@ -635,15 +664,18 @@ __global__ __launch_bounds__(kJoinThreads) void decay_join_kernel(WalkArgs w) {
     }
     return;
   }
-  const float less_one = expm1f(w.log_decay[head] * (float)w.seg);
+  Power power;
+  power.set(w.log_decay[head] * kLog2e, (float)w.seg);
+  float dropped = 0.0f;
   const int64_t first = start / w.seg + 1, last = (end - 1) / w.seg;
   f32x4 x = {0, 0, 0, 0};
   for (int64_t j = first; j <= last; ++j) {
     f32x4* p = reinterpret_cast<f32x4*>(w.carry + (j * w.H + head) * state + at);
     f32x4 own = *p;
     if (j > first && (j - 1) * w.seg > start) {
+      const float keep = power.factor(dropped);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) own[r] += fmaf(x[r], less_one, x[r]);
+      for (int r = 0; r < 4; ++r) own[r] += keep * x[r];
       *p = own;
     }
     x = own;

@@ -1,0 +1,59 @@
+"""The decay attention's states, which the caller gets in fp32: what a state keeps
+of its past under every decay, held relative to that itself (no larger terms
+beside it that would hide it), and infinite states."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from layers_util import F32, check
+from test_gpu_decay_attn import case, run_bwd, run_fwd
+
+pytestmark = pytest.mark.gpu
+RATES = [0.0, -1e-6, -0.002, -0.01, -0.05, -0.2, -0.5, -1.0, -math.inf]
+
+
+def kept(c):
+    """lam^length for each sequence and head, and its relative error: the exponent |log lam| length is a
+    product of three fp32 values (the logarithm to base 2, a constant's rounding and the steps), each step of
+    64 rows is an exponential (two steps of fp32) and two roundings, a border between segments as much again."""
+    ld = c["ld"].double().cpu()
+    t = torch.tensor(c["lens"], dtype=torch.float64)[:, None]
+    x = torch.where(t == 0, torch.zeros_like(t), torch.nan_to_num(ld, neginf=-1e300)[None] * t)
+    chunks = 2 * (t / 64 + 2)
+    return torch.exp(x)[..., None, None], F32 * (4 * torch.where(x < -1e3, 0 * x, -x) + 4 * chunks)[..., None, None]
+
+
+@pytest.mark.parametrize("lens", [[1], [64], [63, 0, 65], [200], [700, 130]])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 40)])
+def test_a_state_that_only_decays(gpu, lens, dk, dv):
+    """Keys (backward: queries) of zeros add nothing, so the last state is the first one's share; below
+    2^-126, the smallest normal value, a power may be zero."""
+    print(f"decay states lens={lens} dk={dk} dv={dv}", flush=True)
+    c = case(lens, len(RATES), dk, dv, gpu, True, ld=torch.tensor(RATES), seed=21)
+    c["k"].zero_()
+    _, out = run_fwd(c, gpu)
+    share, err = kept(c)
+    s0 = c["s0"].double().cpu()
+    check("state_out", out, (share * s0).to(gpu), (err * share * s0.abs() + 2.0 ** -126 * s0.abs()).to(gpu))
+    c["q"].zero_()
+    gin = run_bwd(c, gpu)[3]
+    ds = c["ds"].double().cpu()
+    check("grad_state_in", gin, (share * ds).to(gpu), (err * share * ds.abs() + 2.0 ** -126 * ds.abs()).to(gpu))
+
+
+@pytest.mark.parametrize("lens", [[40], [150, 90], [400]])
+def test_infinite_states(gpu, lens):
+    """An infinity in a carried state stays one, of its sign, and no other entry changes."""
+    c = case(lens, 2, 64, 64, gpu, True, ld=torch.tensor([-0.01, -0.4]), seed=22)
+    _, clean = run_fwd(c, gpu)
+    clean_in = run_bwd(c, gpu)[3]
+    c["s0"][0, 1, 3, 5], c["s0"][0, 0, 7, 9] = math.inf, -math.inf
+    c["ds"][0, 1, 3, 5], c["ds"][0, 0, 7, 9] = math.inf, -math.inf
+    _, out = run_fwd(c, gpu)
+    gin = run_bwd(c, gpu)[3]
+    for got, want in ((out, clean), (gin, clean_in)):
+        want[0, 1, 3, 5], want[0, 0, 7, 9] = math.inf, -math.inf
+        assert torch.equal(got, want), (got != want).nonzero()

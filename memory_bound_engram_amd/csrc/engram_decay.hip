@@ -39,7 +39,7 @@
 // they become operands of the products that give y, which is rounded to bf16
 // itself.  The products that update X, which all later chunks read and the
 // caller gets in fp32, take c times its power of the decay as the sum of three
-// bf16 values, 24 bits, which is all of it (two leave 2.5e-6 of the state).
+// bf16 values, 24 bits, to its last one (two leave 2.5e-6 of the state).
 #include "engram_device.h"
 #include "engram_launch.h"
 #include "engram_layers_device.h"
@@ -408,12 +408,19 @@ struct Walk {
   };
 
   // Eight values of c times their powers of the decay, each as three bf16
-  // values: the upper eight bits of what is left, three times.  kInf: they may
-  // be infinite, and then have no further parts.
+  // values: the upper eight bits of what is left, three times.  What a part
+  // leaves is taken 2^-24 of the part too large, an error of at most the last
+  // bit, so that all three have one sign and none is 0 beside one that is not:
+  // an infinity in b makes the state infinite, not NaN as times 0.  kInf: the
+  // values may be infinite, as all three parts then are.
   template <bool kInf>
   static __device__ __forceinline__ void split(bf16x8 (&to)[3], bf16x8 c, float up, const Powers& pw) {
     const u32x4 raw = __builtin_bit_cast(u32x4, c);
     u32x4 part[3];
+    const auto left = [](float x) {
+      const float r = fmaf(__uint_as_float(__float_as_uint(x) & 0xffff0000u), -0x1.fffffep-1f, x);
+      return kInf && r != r ? x : r;
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float x0 = bf_lo(raw[i]) * (up * pw.eight[7 - 2 * i]), x1 = bf_hi(raw[i]) * (up * pw.eight[6 - 2 * i]);
@@ -421,12 +428,8 @@ struct Walk {
       for (int k = 0; k < 3; ++k) {
         part[k][i] = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
         if (k == 2) break;
-        x0 -= __uint_as_float(__float_as_uint(x0) & 0xffff0000u);
-        x1 -= __uint_as_float(__float_as_uint(x1) & 0xffff0000u);
-        if (kInf) {
-          x0 = x0 == x0 ? x0 : 0.0f;
-          x1 = x1 == x1 ? x1 : 0.0f;
-        }
+        x0 = left(x0);
+        x1 = left(x1);
       }
     }
 #pragma unroll

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from layers_util import F32, check
-from test_gpu_decay_attn import case, run_bwd, run_fwd
+from test_gpu_decay_attn import case, recurrence, reversed_recurrence, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
 RATES = [0.0, -1e-6, -0.002, -0.01, -0.05, -0.2, -0.5, -1.0, -math.inf]
@@ -57,3 +57,36 @@ def test_infinite_states(gpu, lens):
     for got, want in ((out, clean), (gin, clean_in)):
         want[0, 1, 3, 5], want[0, 0, 7, 9] = math.inf, -math.inf
         assert torch.equal(got, want), (got != want).nonzero()
+
+
+@pytest.mark.parametrize("what", ["k", "v", "q", "do"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("at", [100, 149])
+def test_an_infinity_enters_a_state(gpu, what, bad, at):
+    """What the recurrence in 64 bits makes of a value that is not finite: infinities of either sign in
+    the states and, behind (backward: before) that token, in the results that read them, NaN where it has
+    NaN.  One state row or column is reached, the other entries are held to no bound here.
+    (An infinite v in its own row: the recurrence sums q_d (k_d v), infinities of both signs, the chunk
+    has (q . k) v, one infinity; both are the formula, so that row only has to be not finite.)"""
+    lens = [150, 90]
+    c = case(lens, 2, 64, 64, gpu, True, ld=torch.tensor([-0.02, -0.3]), seed=23)
+    c[what][at, 1, 3] = bad
+    do, q, k, v, ld, s0, ds = (c[s].cpu() for s in ("do", "q", "k", "v", "ld", "s0", "ds"))
+    if what in "kv":
+        o, out = run_fwd(c, gpu)
+        want_o, want = recurrence(q, k, v, ld, lens, c["scale"], s0)
+        rows, got_o = slice(at, 150), o
+    else:
+        _, gk, gv, out = run_bwd(c, gpu)
+        _, want_k, want_v, want = reversed_recurrence(do, q, k, v, ld, lens, c["scale"], s0, ds)
+        rows, got_o, want_o = slice(0, at + 1), gk if what == "do" else gv, want_k if what == "do" else want_v
+    assert not torch.isfinite(want[0, 1]).all() and not torch.isfinite(want_o[rows, 1]).all()
+
+    def wild(t):  # what is not finite, and which of the three
+        return torch.where(torch.isfinite(t), torch.zeros_like(t), torch.where(torch.isnan(t), 2 + 0 * t.nan_to_num(0, 0, 0), t.sign()))
+    assert torch.equal(wild(out.double().cpu()), wild(want))
+    have, need = wild(got_o[rows, 1].double().cpu()), wild(want_o[rows, 1])
+    if what == "v":
+        assert torch.equal(have[0] != 0, need[0] != 0)
+        have, need = have[1:], need[1:]
+    assert torch.equal(have, need)

@@ -12,6 +12,7 @@ from layers_util import F32, check
 from test_gpu_decay_attn import case, recurrence, reversed_recurrence, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
 RATES = [0.0, -1e-6, -0.002, -0.01, -0.05, -0.2, -0.5, -1.0, -math.inf]
 
 
@@ -90,3 +91,29 @@ def test_an_infinity_enters_a_state(gpu, what, bad, at):
         assert torch.equal(have[0] != 0, need[0] != 0)
         have, need = have[1:], need[1:]
     assert torch.equal(have, need)
+
+
+@pytest.mark.parametrize("lens", [[128], [64], [37], [100, 28]])
+@pytest.mark.parametrize("d", [128, 64])
+def test_a_state_keeps_24_bits(gpu, lens, d):
+    """With keys (backward: queries) of a one and zeros, no two of d neighbours the same, a state's entry
+    is the sum of one product or two (at d = 64), a value times a power of the decay.  It is held to the
+    power's own error -- its exponent's roundings, two steps of fp32 for each of a chunk's three factors and
+    their products, and for each chunk behind -- and the last bits of the product and its three parts."""
+    c = case(lens, len(RATES), d, d, gpu, True, ld=torch.tensor(RATES), seed=24)
+    c["s0"], c["ds"] = c["s0"] * 0, c["ds"] * 0
+    t = torch.arange(c["n"], device=gpu) % d
+    for s in "kq":
+        c[s] = torch.nn.functional.one_hot(t, d)[:, None].expand(-1, len(RATES), -1).to(BF).contiguous()
+    c["scale"] = 1.0
+    _, out = run_fwd(c, gpu)
+    gin = run_bwd(c, gpu)[3]
+    do, q, k, v, ld, s0, ds = (c[s].cpu() for s in ("do", "q", "k", "v", "ld", "s0", "ds"))
+    _, want = recurrence(q, k, v, ld, lens, 1.0, s0)
+    *_, want_in = reversed_recurrence(do, q, k, v, ld, lens, 1.0, s0, ds)
+    _, size = recurrence(q, k, v.abs(), ld, lens, 1.0, s0)
+    *_, size_in = reversed_recurrence(do.abs(), q, k, v, ld, lens, 1.0, s0, ds)
+    rate = torch.where(ld < -1e3, torch.zeros_like(ld), -ld).double()[:, None, None]
+    err = F32 * (4 * rate * max(lens) + 16)
+    check("state_out", out, want.to(gpu), (err * size + 2.0 ** -126 * 8).to(gpu))
+    check("grad_state_in", gin, want_in.to(gpu), (err * size_in + 2.0 ** -126 * 8).to(gpu))

@@ -167,8 +167,8 @@ __device__ __forceinline__ void angles(const uint64_t (&f)[8], int64_t pos, floa
   }
 }
 
-// Turn the lane's eight pairs by +phi (kSign 1) or -phi (kSign -1); lanes that
-// do not turn have cos 1 and sin 0.
+// Turn the lane's eight pairs by +phi (kSign 1) or -phi (kSign -1); for the lanes
+// that turn only: a turn by nothing would multiply an infinity by a sine of 0.
 template <bool kInter, int kSign>
 __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8]) {
 #pragma unroll
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_rope_fwd_kernel(QkArgs arg
       a[i] *= rstd * wa[i];
       b[i] *= rstd * wb[i];
     }
-    rotate<kInter, 1>(a, b, cs, sn);
+    if (c.turns) rotate<kInter, 1>(a, b, cs, sn);
     if (h < s.heads) {
       if (c.has_a) store8<true>(yp + c.a, a);
       if (c.has_b) store8<true>(yp + c.b, b);
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_rope_bwd_kernel(QkArgs arg
       unpack8(rgb, gb);
       more = at.next();
       if (more) fetch(ra, rb, rga, rgb);
-      rotate<kInter, -1>(ga, gb, cs, sn);
+      if (c.turns) rotate<kInter, -1>(ga, gb, cs, sn);
       if (more && at.pass == 0) angles<T>(f, args.R ? args.positions[at.n] : 0, cs, sn);
       float ss = 0.0f, dot = 0.0f;
 #pragma unroll

@@ -608,8 +608,7 @@ __global__ __launch_bounds__(kVecThreads) void vector_kernel(const uint16_t* x, 
 // one to join a split contraction (13 x 5120 x 1368: 9.8 us against 15.5; at
 // 131 MB of W the tiles' whole lines win, 33 us against 39).  What a CU can ask
 // its cache for bounds it, 64 bytes of a row at a time: lanes whose rows are not
-// there ask for nothing (their sums, of whatever is in their registers, are in
-// rows and columns of the product that nobody reads).
+// there load from beyond their buffer, which is zero and asks for nothing.
 template <typename T, int kWaves, int kR>
 __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, const uint16_t* w, int64_t ldx, int N,
                                                            int64_t K, int64_t M, Epilogue e) {
@@ -617,24 +616,28 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, co
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane % 16, g = lane / 16;
   const int64_t m0 = (int64_t)blockIdx.x * kR;
-  const bool has_w = l < kR && m0 + l < M, has_x = l < N;
-  const uint16_t* wr = w + (has_w ? m0 + l : 0) * K + 8 * g;
-  const uint16_t* xr = x + (has_x ? (int64_t)l : 0) * ldx + 8 * g;
+  const __amdgpu_buffer_rsrc_t wb = buffer_of(w + m0 * K), xb = buffer_of(x);
+  const uint32_t wr = l < kR && m0 + l < M ? (uint32_t)(l * (int)K + 8 * g) * 2 : kBeyond;
+  const uint32_t xr = l < N ? (uint32_t)(l * (int)ldx + 8 * g) * 2 : kBeyond;
+  const auto load = [](__amdgpu_buffer_rsrc_t from, uint32_t at, int k) {  // contraction values from k on
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, (int)at, 2 * k, 0));
+  };
   f32x4 acc = {0, 0, 0, 0};
   const int pieces = (int)(K / 64);
-  constexpr int kAhead = kWaves == 16 ? 6 : 8;  // pieces whose loads are in flight together, as registers allow
+  // pieces whose loads are in flight together: as registers allow, or (four waves, more than 16384 rows of a
+  // small W) the four at most that a wave has
+  constexpr int kAhead = kWaves == 16 ? 6 : 4;
   for (int p = wave; p < pieces; p += kAhead * kWaves) {
     u32x4 fw[kAhead][2], fx[kAhead][2];
-    const auto load = [&](u32x4 (&to)[kAhead][2], const uint16_t* from) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (p + u * kWaves >= pieces) break;
+    for (int u = 0; u < kAhead; ++u) {
+      if (p + u * kWaves >= pieces) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) to[u][h] = load16(from + (int64_t)(p + u * kWaves) * 64 + 32 * h);
+      for (int h = 0; h < 2; ++h) {
+        fw[u][h] = load(wb, wr, (p + u * kWaves) * 64 + 32 * h);
+        fx[u][h] = load(xb, xr, (p + u * kWaves) * 64 + 32 * h);
       }
-    };
-    if (has_w) load(fw, wr);
-    if (has_x) load(fx, xr);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (p + u * kWaves >= pieces) break;
@@ -645,10 +648,9 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(const uint16_t* x, co
   if (wave == pieces % kWaves) {  // what is left of K, a multiple of 8 below 64
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t at = (int64_t)pieces * 64 + 32 * h;
+      const int at = pieces * 64 + 32 * h;
       const bool in = at + 8 * g < K;
-      const u32x4 zero = {0, 0, 0, 0};
-      acc = T::mfma(in ? load16(wr + at) : zero, in ? load16(xr + at) : zero, acc);
+      acc = T::mfma(load(wb, in ? wr : kBeyond, at), load(xb, in ? xr : kBeyond, at), acc);
     }
   }
   part[wave][lane] = acc;

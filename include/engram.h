@@ -311,7 +311,9 @@ size_t engram_linear_fwd_workspace_bytes(int64_t N, int64_t K, int64_t M);
  *   grad_bias [M] fp32, out, or NULL (not wanted)
  *   workspace     engram_linear_bwd_workspace_bytes(N, K, M) bytes
  * At least one of the three outputs.  With an activation dz is rounded to the
- * element type before the two products (grad_bias sums it unrounded).
+ * element type before the two products (grad_bias sums it unrounded): in fp16 a
+ * dz above 65504 becomes infinite there (act' reaches 1.13, so a grad_y from
+ * 58000 on can), and one below 2^-14 keeps fewer digits, as any fp16 value.
  */
 engram_status engram_linear_bwd(const void *grad_y, const void *x, const void *w, const void *z, void *grad_x,
                                 void *grad_w, float *grad_bias, void *workspace, int64_t N, int64_t K, int64_t M,

@@ -206,7 +206,9 @@ def engram_linear_fwd(x, w, y, workspace=None, bias=None, residual=None, z=None,
 def engram_linear_bwd(grad_y, x, w, grad_x, grad_w, workspace, z=None, grad_bias=None, act="none", stream=None) -> None:
     """Enqueue the linear layer's backward: grad_x [N,K], grad_w [M,K] (each
     may be None: not wanted) and grad_bias [M] fp32 from grad_y [N,M], x, w and,
-    with an activation, the forward's z.  The residual's gradient is grad_y."""
+    with an activation, the forward's z.  The residual's gradient is grad_y.
+    With an activation the products take its gradient in x's type, in fp16 within
+    that type's range."""
     a = _Args()
     N, K = _shape("x", x, 2)
     M = _shape("w", w, 2)[0]

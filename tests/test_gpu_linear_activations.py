@@ -71,3 +71,25 @@ def test_slopes(gpu, act, dt):
     torch.cuda.synchronize()
     _, p, rest = ACTS[act][0](z[0].double())  # the slope is the sum of two terms, of opposite signs below 0
     check(act, gb, p + rest, REL * (p + rest.abs()) + NORMAL * (1 + z[0].double().abs().clamp(max=128)))
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_range_of_the_activations_gradient(gpu, dt):
+    """The products take grad_y act'(z) in the element type: within bf16's range wherever grad_y is, in
+    fp16 infinite above 65504 and in whole steps of 2^-24 below 2^-14; grad_bias takes it in fp32."""
+    z = torch.tensor([[1.5, -1.5, 0.0, 1.5, -5.0, 0.5, 3.0, 30.0]], device=gpu).to(dt)
+    gy = torch.tensor([[65000.0, 65000.0, 65000.0, -65000.0, 2.0 ** -12, 2.0 ** -24, 2.0 ** -20, 65504.0]], device=gpu).to(dt)
+    w = torch.eye(8, device=gpu).to(dt)
+    x = torch.ones((1, 8), dtype=dt, device=gpu)
+    gw, gb = poisoned((8, 8), dt, gpu), poisoned((8,), torch.float32, gpu)
+    eg.engram_linear_bwd(gy, x, w, None, gw, buffer(eg.engram_linear_bwd_workspace_bytes(1, 8, 8), gpu), z=z, grad_bias=gb,
+                         act="gelu")
+    torch.cuda.synchronize()
+    _, p, rest = gelu(z[0].double())
+    dz = gy[0].double() * (p + rest)
+    check("grad_bias", gb, dz, REL * gy[0].double().abs() * (p + rest.abs()))
+    kept = dz.to(dt).double()
+    assert torch.isinf(kept).tolist() == [dt == FP, False, False, dt == FP, False, False, False, False]
+    # rounded here and, a little off by REL, there: a step apart at most
+    step = 2 * HALF_STEP[dt] * kept.abs().nan_to_num(0, 0, 0) + TINY[dt]
+    check("grad_w", gw, kept[:, None].expand(8, 8), step[:, None].expand(8, 8))

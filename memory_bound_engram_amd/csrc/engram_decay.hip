@@ -29,10 +29,14 @@
 // one launch each: they read the same rows, which the caches then serve, and
 // short calls pay for one launch (300 tokens, 40 heads: 35 us, 66 apart).
 //
-// Bounds.  The forward of 41444 tokens in 7 sequences, 40 heads of 128 x 128,
-// takes 692 us: the walk 430 for the 1.7 GB it reads and writes, 3.9 TB/s (20
-// less with the state's products left out: memory bounds it), the state pass 200
-// for the 0.5 GB that it reads again (143 without its products), the join 10.
+// Bounds.  The forward of 29623 tokens in 7 sequences, 40 heads of 128 x 128,
+// takes 443 us: the state pass 138 for the 0.43 GB that it moves (it reads the
+// part of k and v that goes on into another segment), the join 10, the walk 298
+// for 1.28 GB.  By the counters nothing bounds the walk alone: 4.3 TB/s are three
+// quarters of a copy's rate, the vector ALUs work 56% of the time and the matrix
+// cores 26%; a chunk's loads are sent for one chunk ahead, and a workgroup meets
+// four times a chunk.  Many sequences of a few tokens are slow, as a workgroup
+// walks its segment's one behind the other (64 of 2 tokens, 8 heads: 438 us).
 //
 // Rounding.  bf16 operands enter the matrix cores as they are; sums are fp32.
 // The scores (times their power of the decay) and X are rounded to bf16 where
@@ -71,7 +75,8 @@ __device__ __forceinline__ bf16x8 join8(u32x2 lo, u32x2 hi) {
 // read at once (rows 0-3 and 12-15 of one piece with rows 4-11 of the next, or
 // the other way round) and thirty-two of an 8-byte or transposing one (sixteen
 // rows of one piece; or rows 0-3 of two eights in different halves of 16); with
-// this order the lanes of each kind find their values in different banks.
+// this order the lanes of each kind find their values in different banks (counted:
+// no conflicts in the state pass, 9% of the LDS cycles in the walk).
 template <int kD>
 __device__ __forceinline__ uint32_t turn(uint32_t row) {
   const uint32_t b2 = row >> 2 & 1, b3 = row >> 3 & 1, b4 = row >> 4 & 1;
@@ -837,11 +842,13 @@ hipError_t launch_carries(const WalkArgs* w, int n, hipStream_t stream) {
 }  // namespace
 
 // Tokens of a segment: as many segments as fit the chip at once (two
-// workgroups a CU) for all walks of a call, since one more would be a second
-// round (9500 tokens, 32 heads of 128 x 128, backward: 337 us with the three
-// walks in one round of 5 segments, 367 in three rounds of 15, 385 in three
-// launches; 41444 tokens, 40 heads, forward: 710 us with the 12 segments that
-// fit, 774 with 6, 737 with 25; all before y went out in whole lines).
+// workgroups a CU, which is what the LDS of the 128 x 128 walk lets in; narrower
+// heads are cut alike, though more of their workgroups would fit) for all walks
+// of a call, since one more would be a second round (9500 tokens, 32 heads of
+// 128 x 128, backward: 337 us with the three walks in one round of 5 segments,
+// 367 in three rounds of 15, 385 in three launches; 41444 tokens, 40 heads,
+// forward: 710 us with the 12 segments that fit, 774 with 6, 737 with 25; all
+// before y went out in whole lines).
 int64_t decay_segment(int64_t N, int64_t H, int64_t walks) {
   constexpr int64_t kPlaces = 512;
   const int64_t want = walks * H < kPlaces ? kPlaces / (walks * H) : 1;  // segments

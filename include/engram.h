@@ -400,7 +400,8 @@ engram_status engram_rope_freqs(double theta, int64_t R, int64_t *freqs);
  *   B * H <= ENGRAM_DECAY_STATES_MAX; Dk, Dv multiples of 8, 8..ENGRAM_DECAY_D_MAX
  *   scale finite
  * States and sums are fp32 throughout; scores and states are rounded to bf16
- * as operands of the products that give o.
+ * as operands of the products that give o.  A power of the decay below 2^-126
+ * may count as 0.
  */
 #define ENGRAM_DECAY_ROWS_MAX 16777216
 #define ENGRAM_DECAY_HEADS_MAX 1024

@@ -445,6 +445,108 @@ engram_status engram_decay_attn_step(const void *q, const void *k, const void *v
                                      int64_t Dv, int64_t slots_total, int64_t ldq, int64_t ldk, int64_t ldv,
                                      int64_t ldo, float scale, void *stream);
 
+/* ==========================================================================
+ * The rest of a block around the gate: the layer norm in front of its
+ * projections (layer_norm), and a token mixer that keeps one value for each
+ * channel (gated_scan).  The common contract of the layers above holds for
+ * these too: rows may lie apart, 16-byte alignment, a workspace for each
+ * call that may run at the same time, the same errors.
+ * ========================================================================== */
+
+/*
+ * Layer norm of each row:
+ *   mean = sum_j x_j / D, rstd = (sum_j (x_j - mean)^2 / D + eps)^(-1/2),
+ *   y = (x - mean) rstd w + b
+ *   x [N][D]    in, leading dimension ldx
+ *   w, b [D]    fp32, in; b may be NULL (zero)
+ *   y [N][D]    out, leading dimension ldy
+ *   saved [N][2] fp32, out: mean and rstd for the backward, or NULL (not wanted)
+ *   N 1..ENGRAM_NORM_ROWS_MAX; D a multiple of 8, 8..ENGRAM_NORM_D_MAX;
+ *   0 <= eps <= 1
+ *   dtype       ENGRAM_BF16, ENGRAM_FP16 or ENGRAM_FP32, of x and y
+ * Everything is fp32 up to the one rounding of y.
+ */
+#define ENGRAM_NORM_ROWS_MAX 2097152
+#define ENGRAM_NORM_D_MAX 16384
+engram_status engram_layer_norm_fwd(const void *x, const float *w, const float *b, void *y, float *saved, int64_t N,
+                                    int64_t D, int64_t ldx, int64_t ldy, float eps, int dtype, void *stream);
+
+/*
+ * Backward of the above for the gradient grad_y of y, from the forward's x, w
+ * and saved; with u = (x - mean) rstd and g = grad_y w:
+ *   grad_x = rstd (g - mean_j(g) - u mean_j(g u)) + grad_residual,
+ *   grad_w = sum over rows of grad_y u,  grad_b = sum over rows of grad_y
+ *   grad_y, x     [N][D] in, leading dimensions ldgy, ldx
+ *   grad_residual [N][D] in, leading dimension ldgr, or NULL (zero; ldgr not
+ *                 looked at): the gradient that reaches x past the norm
+ *   grad_x        [N][D] out, leading dimension ldgx
+ *   grad_w, grad_b [D] fp32, out, or NULL (not wanted): sums in a fixed order
+ *   workspace     engram_layer_norm_bwd_workspace_bytes(N, D) bytes
+ */
+engram_status engram_layer_norm_bwd(const void *grad_y, const void *x, const float *w, const float *saved,
+                                    const void *grad_residual, void *grad_x, float *grad_w, float *grad_b,
+                                    void *workspace, int64_t N, int64_t D, int64_t ldgy, int64_t ldx, int64_t ldgr,
+                                    int64_t ldgx, int dtype, void *stream);
+
+/* Scratch bytes of engram_layer_norm_bwd; 0 for sizes the call rejects. */
+size_t engram_layer_norm_bwd_workspace_bytes(int64_t N, int64_t D);
+
+/*
+ * Gated recurrence of each channel.  For every sequence, with
+ * f_t = sigmoid(gate_t):
+ *   h_t = f_t h_{t-1} + (1 - f_t) u_t
+ *   gate, u [N][D]  in, leading dimensions ldg, ldu: the tokens of all
+ *                   sequences one behind the other
+ *   cu_seqlens [B+1] int64, in, device memory, as in engram_decay_attn_fwd:
+ *                   rows behind the last sequence are left as they are
+ *   state_in  [B][D] fp32, in: h before each sequence's first token, or NULL
+ *                   (zero)
+ *   h [N][D]        out, leading dimension ldh
+ *   state_out [B][D] fp32, out: h behind each sequence's last token, or NULL
+ *                   (not wanted)
+ *   workspace       engram_gated_scan_fwd_workspace_bytes(N, B, D) bytes
+ *   N 1..ENGRAM_SCAN_ROWS_MAX; B 1..ENGRAM_SCAN_STATES_MAX; D a multiple of 8,
+ *   8..ENGRAM_SCAN_D_MAX; N * D <= ENGRAM_SCAN_VALUES_MAX
+ *   dtype           ENGRAM_BF16, ENGRAM_FP16 or ENGRAM_FP32, of gate, u and h
+ * States are fp32 throughout, and f and 1 - f are each accurate relative to
+ * themselves down to 2^-126; below that they, and products of factors f, may
+ * count as 0.
+ */
+#define ENGRAM_SCAN_ROWS_MAX 16777216
+#define ENGRAM_SCAN_STATES_MAX 4194304
+#define ENGRAM_SCAN_D_MAX 65536
+#define ENGRAM_SCAN_VALUES_MAX 34359738368 /* N * D */
+engram_status engram_gated_scan_fwd(const void *gate, const void *u, const int64_t *cu_seqlens, const float *state_in,
+                                    void *h, float *state_out, void *workspace, int64_t N, int64_t B, int64_t D,
+                                    int64_t ldg, int64_t ldu, int64_t ldh, int dtype, void *stream);
+size_t engram_gated_scan_fwd_workspace_bytes(int64_t N, int64_t B, int64_t D);
+
+/*
+ * Backward of the above: from the gradient grad_h of h and grad_state_out of
+ * state_out (NULL: zero), the gradients of gate, u and of state_in (NULL: not
+ * wanted).  h is the forward's (rounded) output: gate's gradient takes h_{t-1}
+ * from it, and from state_in (NULL: zero) at a sequence's first token.
+ * Rows behind the last sequence are left as they are in the gradients.
+ */
+engram_status engram_gated_scan_bwd(const void *grad_h, const void *gate, const void *u, const void *h,
+                                    const int64_t *cu_seqlens, const float *state_in, const float *grad_state_out,
+                                    void *grad_gate, void *grad_u, float *grad_state_in, void *workspace, int64_t N,
+                                    int64_t B, int64_t D, int64_t ldgh, int64_t ldg, int64_t ldu, int64_t ldh,
+                                    int64_t ldgg, int64_t ldgu, int dtype, void *stream);
+size_t engram_gated_scan_bwd_workspace_bytes(int64_t N, int64_t B, int64_t D);
+
+/*
+ * One token for each row of a decode batch, the states updated in place:
+ *   gate, u, h [B][D]     as above with rows of the batch for tokens
+ *   state [slots_total][D] fp32, in and out: a pool of states
+ *   slots [B]             int64, in, device memory, as in engram_decay_attn_step
+ *   B 1..ENGRAM_SCAN_STEP_ROWS_MAX; D, dtype as above; slots_total 1..
+ */
+#define ENGRAM_SCAN_STEP_ROWS_MAX 4096
+engram_status engram_gated_scan_step(const void *gate, const void *u, float *state, const int64_t *slots, void *h,
+                                     int64_t B, int64_t D, int64_t slots_total, int64_t ldg, int64_t ldu, int64_t ldh,
+                                     int dtype, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *engram_status_string(int status);
 

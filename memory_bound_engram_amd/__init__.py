@@ -308,7 +308,9 @@ def engram_gateconv_bwd(dY, H, k, v, rms_w_h, rms_w_v, conv_w, vhat, alpha, rrms
 
 from . import layers as _layers  # noqa: E402  (needs the names above)
 from .layers import *  # noqa: E402,F401,F403
+from . import block as _block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
 
 __all__ = ["engram_gate_bwd_noalloc", "engram_gateconv_fwd", "engram_gateconv_bwd", "engram_gateconv_bwd_workspace_bytes", "engram_gate_bwd_with_norm_weights", "engram_fused_weight", "engram_gate_fwd", "engram_gate_bwd", "engram_gate_bwd_workspace_bytes", "EngramError", "lib",
            "LIB_PATH"]
-__all__ += _layers.__all__
+__all__ += _layers.__all__ + _block.__all__

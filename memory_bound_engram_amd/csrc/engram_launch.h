@@ -121,4 +121,38 @@ size_t linear_bwd_workspace(int64_t N, int64_t K, int64_t M);
 hipError_t launch_linear_fwd(const LinearCall& l, hipStream_t stream);
 hipError_t launch_linear_bwd(const LinearCall& l, hipStream_t stream);
 
+// Layer norm: one call's arguments.
+struct NormCall {
+  const void *x, *grad_y, *grad_residual;
+  const float *w, *b;
+  void *y, *grad_x;
+  float *saved, *grad_w, *grad_b;
+  void* workspace;
+  int64_t N, D, ldx, ldy, ldgy, ldgr, ldgx;
+  float eps;
+  int dtype;
+};
+size_t layer_norm_bwd_workspace(int64_t N, int64_t D);
+hipError_t launch_layer_norm_fwd(const NormCall& c, hipStream_t stream);
+hipError_t launch_layer_norm_bwd(const NormCall& c, hipStream_t stream);
+
+// Gated scan: one call's arguments.
+struct ScanCall {
+  const void *gate, *u, *h_in, *grad_h;
+  const int64_t* cu;            // forward, backward: [B + 1]
+  const float *state_in, *grad_state_out;
+  float *state_out, *grad_state_in;
+  void *h, *grad_gate, *grad_u;
+  void* workspace;
+  float* pool;                  // step: [n_slots] states, and each row's slot
+  const int64_t* slots;
+  int64_t n_slots;
+  int64_t N, B, D, ldg, ldu, ldh, ldgh, ldgg, ldgu;
+  int dtype;
+};
+size_t scan_workspace(int64_t N, int64_t D);
+hipError_t launch_scan_fwd(const ScanCall& c, hipStream_t stream);
+hipError_t launch_scan_bwd(const ScanCall& c, hipStream_t stream);
+hipError_t launch_scan_step(const ScanCall& c, hipStream_t stream);
+
 }  // namespace engram

@@ -1,0 +1,37 @@
+// engram_sequences.h -- the sequences that a cu_seqlens array cuts the tokens
+// into, as kernels look them up (gfx950, internal).
+#pragma once
+
+#include "engram_device.h"
+
+namespace engram {
+
+// The array is the caller's and lies in device memory: bounds are clamped to the
+// tokens there are, so that no content of it leads out of the arrays.  Everything
+// here is the same in all lanes of a wave.
+struct Sequences {
+  const int64_t* cu;  // [B + 1]
+  int64_t N;
+  int B;
+  __device__ __forceinline__ int64_t bound(int i) const {
+    int64_t v = cu[i];
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const int32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    v = (int64_t)(((uint64_t)(uint32_t)hi << 32) | lo);
+    return v < 0 ? 0 : (v > N ? N : v);
+  }
+  __device__ __forceinline__ int64_t start(int i) const { return bound(i); }
+  __device__ __forceinline__ int64_t end(int i) const { return bound(i + 1); }
+  // the first sequence that ends behind a token (B if none does)
+  __device__ int first_behind(int64_t token) const {
+    int lo = 0, hi = B;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (end(mid) > token) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  }
+};
+
+}  // namespace engram

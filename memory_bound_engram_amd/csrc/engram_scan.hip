@@ -15,23 +15,26 @@
 //
 // Mapping.  One pass: each value is read once and written once, so HBM bounds the
 // kernel.  The axis of time is cut into chunks; a workgroup takes one chunk of
-// 512 channels, a lane eight channels of kTokens tokens.  It walks its tokens from
+// 256 channels, a lane four channels of kTokens tokens.  It walks its tokens from
 // a state of zero, keeping x_t = local state and P_t = product of the factors in
 // registers, so that the state that comes in, once known, is one fma a value.
 // What a chunk does to the state, (P, x) at its end, goes to the other workgroups
-// through memory: the chunks of a group of eight publish theirs; the group's last
-// publishes the state behind it.  A chunk's incoming state is that behind the group before,
-// carried through the chunks of its own group in order: eight hops for 4096
-// tokens, and always the same sums in the same order.
+// through memory, in two levels: the last of a group of eight chunks joins its
+// group's and publishes that, and the last of eight groups the state behind them.
+// A chunk's incoming state is the one behind the eight groups before its own,
+// carried through the groups and then the chunks before it, always in the same
+// order: one hop from workgroup to workgroup for every 64 chunks.
 //
 // Waiting.  A workgroup waits for words that others write.  Chunks are dealt by a
 // ticket (a counter in the workspace), so all chunks before a workgroup's own
-// belong to workgroups that run already.  It publishes its own (P, x) before it
-// waits for anything, and then waits for lower tickets only; so by induction over
-// the tickets every wait ends.  A word is 8 bytes and says by itself whether it
-// is there: all ones before (a launch of its own fills them), never all ones after (P
-// is no NaN but the one below, and the state's second half is 0); no order of
-// different words is assumed.
+// belong to workgroups that run already.  A chunk's (P, x) is published before its
+// workgroup waits for anything; a group's after waiting for chunks of lower
+// tickets only; a state after waiting for those, groups of lower tickets and the
+// state of a lower ticket.  So all chunks' words come, then all groups', then, by
+// induction, all states: every wait ends.  A word is 8 bytes and says by itself
+// whether it is there: all ones before (a launch of its own fills them), never all
+// ones after (P is no NaN but the one below, and the state's second half is 0); no
+// order of different words is assumed.
 #include "engram_device.h"
 #include "engram_launch.h"
 #include "engram_sequences.h"
@@ -42,15 +45,16 @@ namespace {
 
 constexpr int kWaves = 8;                    // of a workgroup
 constexpr int kThreads = kWaves * 64;
-constexpr int kTile = 64 * 8;                // channels of a workgroup
-constexpr int kGroup = 8;                    // chunks of a group: a wave looks at one
+constexpr int kCh = 4;                       // channels of a lane
+constexpr int kTile = 64 * kCh;              // channels of a workgroup
+constexpr int kGroup = 8;                    // chunks of a group, groups of a span: a wave looks at one of each
 constexpr uint64_t kAbsent = ~0ull;
 constexpr float kLog2e = 1.44269504f;
 
 // Tokens of a lane: as many as the registers of two workgroups a CU hold.
 template <typename T>
 constexpr int tokens_of() {
-  return sizeof(T) == 4 ? 2 : 4;
+  return sizeof(T) == 4 ? 4 : 8;
 }
 
 // (P, x): what tokens do to a state y, x + P y; kFresh in P: a sequence begins
@@ -96,10 +100,9 @@ struct ScanArgs {
   int B, D, tiles, chunks;
 };
 
-constexpr int kTicketWords = 16;  // a line of its own
-__device__ __host__ __forceinline__ int64_t chunk_word(int chunk, int tile, int tiles) {
-  return kTicketWords + ((int64_t)chunk * tiles + tile) * kTile;
-}
+// Words: the ticket in a line of its own; then, a tile's words for each, the chunks,
+// the groups and the spans (the state before each).
+constexpr int kTicketWords = 16;
 
 __global__ void scan_clear_kernel(uint64_t* words, int64_t n) {
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 2;
@@ -108,33 +111,48 @@ __global__ void scan_clear_kernel(uint64_t* words, int64_t n) {
   store16(words + i, u32x4{v, v, v, v});
 }
 
-// Eight words of a lane, 64 apart, once they are there.
-__device__ __forceinline__ void wait_words(const uint64_t* p, uint64_t (&v)[8]) {
+typedef uint64_t Words[kCh];
+typedef f32x2 Ends[kCh];
+// A lane's words, 64 apart, once they are there.
+__device__ __forceinline__ void wait_words(const uint64_t* p, f32x2 (*to)[64], int lane) {
+  Words v;
   for (;;) {
     bool there = true;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[k] = __hip_atomic_load(p + 64 * k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int k = 0; k < kCh; ++k) {
+      v[k] = __hip_atomic_load(p + 64 * k + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       there &= v[k] != kAbsent;
     }
-    if (there) return;
+    if (there) break;
     __builtin_amdgcn_s_sleep(1);
   }
+#pragma unroll
+  for (int k = 0; k < kCh; ++k)
+    to[k][lane] = f32x2{__uint_as_float((uint32_t)(v[k] >> 32)), __uint_as_float((uint32_t)v[k])};
 }
 __device__ __forceinline__ uint64_t word_of(float lo, float hi) {
   return (uint64_t)__float_as_uint(lo) | (uint64_t)__float_as_uint(hi) << 32;
 }
 
-__device__ __forceinline__ void load_state(const float* p, bool mine, float (&v)[8]) {
-  if (p && mine) unpack8(load_raw(p), v);
-  else unpack8(zero_raw<float>(), v);
+__device__ __forceinline__ void publish(uint64_t* p, const Ends& v, int lane) {
+#pragma unroll
+  for (int k = 0; k < kCh; ++k) {
+    const float P = v[k][0] == v[k][0] ? v[k][0] : __uint_as_float(0x7fc00000u);  // no word is kAbsent
+    __hip_atomic_store(p + 64 * k + lane, word_of(v[k][1], P), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+__device__ __forceinline__ void load_state(const float* p, bool mine, float (&v)[kCh]) {
+  if (p && mine) unpack4(load_raw4(p), v);
+  else unpack4(zero_raw4<float>(), v);
 }
 
 template <typename T, bool kBack>
 __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   constexpr int kTok = tokens_of<T>(), kChunk = kTok * kWaves;
-  __shared__ f32x2 ends[kWaves][8][64];   // (P, x) of each wave's tokens
-  __shared__ f32x2 looked[kGroup][8][64];  // of the group's chunks before this one; last, the state behind the group before
+  __shared__ f32x2 ends[kWaves][kCh][64];        // (P, x) of each wave's tokens
+  __shared__ f32x2 looked[2][kGroup][kCh][64];   // of the chunks before this one in its group; of the groups before it
+                                                 // in its span, and the state before the span as the last
   __shared__ uint32_t dealt;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t ticket = blockIdx.x;
@@ -144,7 +162,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
     __syncthreads();
     ticket = __builtin_amdgcn_readfirstlane(dealt);
   }
-  const int chunk = (int)(ticket / a.tiles), tile = (int)(ticket % a.tiles), ch = tile * kTile + lane * 8;
+  const int chunk = (int)(ticket / a.tiles), tile = (int)(ticket % a.tiles), ch = tile * kTile + lane * kCh;
   const bool mine = ch < a.D;
 
   // The wave's tokens, in the order of the walk: step i is token first + i, or first - i.
@@ -153,9 +171,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   const auto token = [&](int i) { return kBack ? first - i : first + i; };
   const auto there = [&](int i) { return walked + i < a.N; };
   const auto get = [&](const void* p, int64_t ld, int64_t t, bool in) {
-    return in && mine ? load_raw(static_cast<const T*>(p) + t * ld + ch) : zero_raw<T>();
+    return in && mine ? load_raw4(static_cast<const T*>(p) + t * ld + ch) : zero_raw4<T>();
   };
-  Raw<T> gate[kTok], in[kTok];  // in: u, or the gradient of h
+  Raw4<T> gate[kTok], in[kTok];  // in: u, or the gradient of h
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     gate[i] = get(a.gate, a.ldg, token(i), there(i));
@@ -189,25 +207,25 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   // The tokens from a state of zero.  Forward: x = h, and P behind the token.
   // Backward: x = dh; P, before the token in the walk (dh needs the e of the token
   // walked before), is made again with the gates below.
-  float x[kTok][8], P[kBack ? 1 : kTok][8];
-  f32x2 last[8];
+  float x[kTok][kCh], P[kBack ? 1 : kTok][kCh];
+  f32x2 last[kCh];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) last[k] = f32x2{1.0f, 0.0f};
+  for (int k = 0; k < kCh; ++k) last[k] = f32x2{1.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     if (!there(i)) continue;  // a token that is not there leaves the state as it is
     if (enters >> i & 1) {
       const float* from = kBack ? a.state_end : a.state_in;
-      float s[8];
+      float s[kCh];
       load_state(from ? from + (int64_t)seq[i] * a.D + ch : nullptr, mine, s);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) last[k] = f32x2{0.0f, s[k]};
+      for (int k = 0; k < kCh; ++k) last[k] = f32x2{0.0f, s[k]};
     }
-    float g[8], v[8];
-    unpack8(gate[i], g);
-    unpack8(in[i], v);
+    float g[kCh], v[kCh];
+    unpack4(gate[i], g);
+    unpack4(in[i], v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kCh; ++k) {
       const Gate q(g[k]);
       if constexpr (kBack) {
         x[i][k] = v[k] + last[k][1];
@@ -220,60 +238,68 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) ends[wave][k][lane] = f32x2{enters ? kFresh : last[k][0], last[k][1]};
+  for (int k = 0; k < kCh; ++k) ends[wave][k][lane] = f32x2{enters ? kFresh : last[k][0], last[k][1]};
   __syncthreads();
 
-  // What the chunk does, for the others; what theirs do, from them.
-  if (a.words) {
-    const int group = chunk / kGroup, r = chunk % kGroup;
-    const bool state = wave == kWaves - 1;
-    if (state) {
-      uint64_t* to = a.words + chunk_word(chunk, tile, a.tiles) + lane;
+  // What the waves before this one do; with the last one's, the chunk.
+  Ends before;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f32x2 all = ends[0][k][lane];
-#pragma unroll 1
-        for (int w = 1; w < kWaves; ++w) all = joined(all, ends[w][k][lane]);
-        const float p = all[0] == all[0] ? all[0] : __uint_as_float(0x7fc00000u);  // no word is kAbsent
-        __hip_atomic_store(to + 64 * k, word_of(all[1], p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
-    if (state ? group > 0 : wave < r) {
-      uint64_t v[8];
-      const int64_t word = state ? chunk_word(a.chunks + group, tile, a.tiles) : chunk_word(group * kGroup + wave, tile, a.tiles);
-      wait_words(a.words + word + lane, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        looked[wave][k][lane] = f32x2{__uint_as_float((uint32_t)(v[k] >> 32)), __uint_as_float((uint32_t)v[k])};
-    }
-    __syncthreads();
-  }
-  float carry[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) carry[k] = 0.0f;
-  if (a.words) {
-    if (chunk >= kGroup)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) carry[k] = looked[kGroup - 1][k][lane][1];
-#pragma unroll 1
-    for (int j = 0; j < chunk % kGroup; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) carry[k] = through(looked[j][k][lane], carry[k]);
-  }
+  for (int k = 0; k < kCh; ++k) before[k] = f32x2{1.0f, 0.0f};
 #pragma unroll 1
   for (int w = 0; w < wave; ++w)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) carry[k] = through(ends[w][k][lane], carry[k]);
-  if (a.words && wave == kWaves - 1 && chunk % kGroup == kGroup - 1 && chunk + 1 < a.chunks) {
-    uint64_t* to = a.words + chunk_word(a.chunks + chunk / kGroup + 1, tile, a.tiles) + lane;
+    for (int k = 0; k < kCh; ++k) before[k] = joined(before[k], ends[w][k][lane]);
+  float carry[kCh];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      __hip_atomic_store(to + 64 * k, word_of(through(ends[wave][k][lane], carry[k]), 0.0f), __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
+  for (int k = 0; k < kCh; ++k) carry[k] = 0.0f;
+  if (a.words) {
+    const int group = chunk / kGroup, r = chunk % kGroup, span = group / kGroup, g = group % kGroup;
+    const int groups = (a.chunks + kGroup - 1) / kGroup;
+    const bool writer = wave == kWaves - 1;
+    const auto words = [&](int i) { return a.words + kTicketWords + ((int64_t)i * a.tiles + tile) * kTile; };
+    Ends all;
+    if (writer) {
+#pragma unroll
+      for (int k = 0; k < kCh; ++k) all[k] = joined(before[k], ends[wave][k][lane]);
+      publish(words(chunk), all, lane);
+    }
+    if (wave < r) wait_words(words(group * kGroup + wave), looked[0][wave], lane);
+    __syncthreads();
+    Ends chunks;
+#pragma unroll
+    for (int k = 0; k < kCh; ++k) chunks[k] = f32x2{1.0f, 0.0f};
+#pragma unroll 1
+    for (int j = 0; j < r; ++j)
+#pragma unroll
+      for (int k = 0; k < kCh; ++k) chunks[k] = joined(chunks[k], looked[0][j][k][lane]);
+    if (writer && r == kGroup - 1) {
+#pragma unroll
+      for (int k = 0; k < kCh; ++k) all[k] = joined(chunks[k], all[k]);
+      publish(words(a.chunks + group), all, lane);
+    }
+    if (writer ? span > 0 : wave < g)
+      wait_words(words(writer ? a.chunks + groups + span : a.chunks + span * kGroup + wave), looked[1][wave], lane);
+    __syncthreads();
+    if (span > 0)
+#pragma unroll
+      for (int k = 0; k < kCh; ++k) carry[k] = looked[1][kGroup - 1][k][lane][1];
+#pragma unroll 1
+    for (int j = 0; j < g; ++j)
+#pragma unroll
+      for (int k = 0; k < kCh; ++k) carry[k] = through(looked[1][j][k][lane], carry[k]);
+    if (writer && r == kGroup - 1 && g == kGroup - 1) {
+#pragma unroll
+      for (int k = 0; k < kCh; ++k) all[k] = f32x2{0.0f, through(all[k], carry[k])};
+      publish(words(a.chunks + groups + span + 1), all, lane);
+    }
+#pragma unroll
+    for (int k = 0; k < kCh; ++k) carry[k] = through(chunks[k], carry[k]);
   }
+#pragma unroll
+  for (int k = 0; k < kCh; ++k) carry[k] = through(before[k], carry[k]);
 
   // The state that comes in, applied, and the results.
-  Raw<T> us[2], hs[2];  // backward: of two tokens, the next two's on their way
+  Raw4<T> us[2], hs[2];  // backward: of two tokens, the next two's on their way
   const auto fetch = [&](int i) {
     us[i % 2] = get(a.u, a.ldu, token(i), seq[i] >= 0);
     hs[i % 2] = get(a.h_in, a.ldh, token(i) - 1, seq[i] >= 0 && !(leaves >> i & 1));
@@ -286,21 +312,21 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   for (int i = 0; i < kTok; ++i) {
     if (enters >> i & 1)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) carry[k] = 0.0f;
-    float v[8];
+      for (int k = 0; k < kCh; ++k) carry[k] = 0.0f;
+    float v[kCh];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = kBack ? x[i][k] + carry[k] : fmaf(P[kBack ? 0 : i][k], carry[k], x[i][k]);
+    for (int k = 0; k < kCh; ++k) v[k] = kBack ? x[i][k] + carry[k] : fmaf(P[kBack ? 0 : i][k], carry[k], x[i][k]);
     const int64_t own = (int64_t)seq[i] * a.D + ch;
     const bool leaving = leaves >> i & 1;
     if constexpr (kBack) {
-      float g[8], u[8], h[8], dg[8], du[8], e[8];
-      unpack8(gate[i], g);
-      unpack8(us[i % 2], u);
+      float g[kCh], u[kCh], h[kCh], dg[kCh], du[kCh], e[kCh];
+      unpack4(gate[i], g);
+      unpack4(us[i % 2], u);
       if (leaving) load_state(a.state_in ? a.state_in + own : nullptr, mine, h);
-      else unpack8(hs[i % 2], h);
+      else unpack4(hs[i % 2], h);
       if (i + 2 < kTok) fetch(i + 2);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kCh; ++k) {
         const Gate q(g[k]);
         du[k] = q.n * v[k];
         dg[k] = du[k] * (h[k] - u[k]) * (q.keeps ? 1.0f - q.s : q.s);
@@ -308,13 +334,13 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
         carry[k] = q.f_times(carry[k]);
       }
       if (seq[i] >= 0 && mine) {
-        store8<true>(static_cast<T*>(a.out) + token(i) * a.ldout + ch, dg);
-        store8<true>(static_cast<T*>(a.out2) + token(i) * a.ldout2 + ch, du);
-        if (leaving && a.state_out) store8<false>(a.state_out + own, e);
+        store4<true>(static_cast<T*>(a.out) + token(i) * a.ldout + ch, dg);
+        store4<true>(static_cast<T*>(a.out2) + token(i) * a.ldout2 + ch, du);
+        if (leaving && a.state_out) store4<false>(a.state_out + own, e);
       }
     } else if (seq[i] >= 0 && mine) {
-      store8<true>(static_cast<T*>(a.out) + token(i) * a.ldout + ch, v);
-      if (leaving && a.state_out) store8<false>(a.state_out + own, v);
+      store4<true>(static_cast<T*>(a.out) + token(i) * a.ldout + ch, v);
+      if (leaving && a.state_out) store4<false>(a.state_out + own, v);
     }
   }
 
@@ -323,9 +349,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
     const float* from = kBack ? a.state_end : a.state_in;
     for (int64_t b = chunk + (int64_t)a.chunks * wave; b < a.B; b += (int64_t)a.chunks * kWaves) {
       if (seqs.start((int)b) < seqs.end((int)b)) continue;
-      float s[8];
+      float s[kCh];
       load_state(from ? from + b * a.D + ch : nullptr, true, s);
-      store8<false>(a.state_out + b * a.D + ch, s);
+      store4<false>(a.state_out + b * a.D + ch, s);
     }
   }
 }
@@ -354,7 +380,7 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(StepArgs a) {
   const bool mine = ch < a.D;
   float* state = a.pool + slot * a.D + ch;
   float s[8];
-  load_state(state, mine, s);
+  if (mine) unpack8(load_raw<float>(state), s);
   if (threadIdx.x < 2) next_row[threadIdx.x] = a.B;
   __syncthreads();
   bool behind = false;
@@ -401,7 +427,8 @@ const void* scan_of(bool back) {
 int tokens_of_chunk(int dtype) { return (dtype == ENGRAM_FP32 ? tokens_of<float>() : tokens_of<bf16_t>()) * kWaves; }
 int64_t tiles_of(int64_t D) { return (D + kTile - 1) / kTile; }
 int64_t words_of(int64_t chunks, int64_t tiles) {
-  return kTicketWords + (chunks + (chunks + kGroup - 1) / kGroup) * tiles * kTile;
+  const int64_t groups = (chunks + kGroup - 1) / kGroup, spans = groups / kGroup + 1;
+  return kTicketWords + (chunks + groups + spans) * tiles * kTile;
 }
 
 hipError_t launch_scan(ScanArgs a, int dtype, bool back, void* workspace, hipStream_t stream) {

@@ -138,8 +138,8 @@ def check_backward(c, h, dev):
     assert torch.isnan(gg[m:]).all() and torch.isnan(gu[m:]).all()
 
 
-# chunks have 16 or 32 tokens, groups eight chunks: 128 or 256 tokens
-LENS = [[1], [3], [4], [32], [33], [16, 16, 1], [255], [256], [257], [1, 0, 3, 64, 129, 0, 2], [0, 0, 5], [0], [700],
+# chunks have 32 tokens (fp32) or 64, groups eight chunks: 256 or 512 tokens
+LENS = [[1], [3], [8], [32], [33], [64], [65], [16, 16, 1], [255], [256], [257], [512], [513], [1, 0, 3, 64, 129, 0, 2], [0, 0, 5], [0], [700],
         [1] * 70, [300, 0, 1, 511, 7]]
 
 
@@ -155,8 +155,9 @@ def test_forward_and_backward(gpu, lens, dtype):
 
 @pytest.mark.parametrize("dtype", [BF, F4], ids=["bf16", "fp32"])
 def test_many_chunks(gpu, dtype):
-    """Far more workgroups than the chip holds at once, and several groups of chunks in one sequence."""
-    c = case([3000, 900, 41], 4104, dtype, gpu, True, seed=2)
+    """Far more workgroups than the chip holds at once, and several spans of eight groups (2048 or 4096 tokens) in one
+    sequence, one that begins inside a span and one that ends with one."""
+    c = case([9000, 3288, 41], 2056, dtype, gpu, True, seed=2)
     h = check_forward(c, gpu)
     check_backward(c, h, gpu)
 

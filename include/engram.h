@@ -447,8 +447,9 @@ engram_status engram_decay_attn_step(const void *q, const void *k, const void *v
 
 /* ==========================================================================
  * The rest of a block around the gate: the layer norm in front of its
- * projections (layer_norm), and a token mixer that keeps one value for each
- * channel (gated_scan).  The common contract of the layers above holds for
+ * projections (layer_norm), and two token mixers beside the decay attention:
+ * one that is exact over the recent past (window_attn) and one that keeps one
+ * value for each channel (gated_scan).  The common contract of the layers above holds for
  * these too: rows may lie apart, 16-byte alignment, a workspace for each
  * call that may run at the same time, the same errors.
  * ========================================================================== */
@@ -490,6 +491,57 @@ engram_status engram_layer_norm_bwd(const void *grad_y, const void *x, const flo
 
 /* Scratch bytes of engram_layer_norm_bwd; 0 for sizes the call rejects. */
 size_t engram_layer_norm_bwd_workspace_bytes(int64_t N, int64_t D);
+
+/*
+ * Softmax attention over a sliding window and the first tokens of a sequence.
+ * Token i sees the tokens j <= i of its sequence with i - j < window or
+ * j < sinks; query head h reads key head h / (Hq / Hk):
+ *   o_i = sum_j exp(scale q_i . k_j - lse_i) v_j,
+ *   lse_i = ln sum_j exp(scale q_i . k_j)           (sums over the j it sees)
+ *   q [N][Hq][D], k, v [N][Hk][D]  in, leading dimensions ldq, ldk, ldv: the
+ *                 tokens of all sequences one behind the other
+ *   cu_seqlens [B+1] int64, in, device memory, as in engram_decay_attn_fwd:
+ *                 rows behind the last sequence are left as they are
+ *   o [N][Hq][D]  out, leading dimension ldo
+ *   lse [N][Hq]   fp32, out: for the backward, or NULL (not wanted)
+ *   N 1..ENGRAM_WINDOW_ROWS_MAX; Hk 1..Hq, Hq a multiple of Hk, at most
+ *   ENGRAM_WINDOW_HEADS_MAX; N * Hq <= ENGRAM_WINDOW_HEAD_ROWS_MAX; B >= 1,
+ *   B * Hk <= ENGRAM_WINDOW_SEQ_HEADS_MAX; D a multiple of 8,
+ *   8..ENGRAM_WINDOW_D_MAX; window >= 1 (N or more: all of the past);
+ *   sinks 0..ENGRAM_WINDOW_SINKS_MAX; scale positive and finite
+ *   dtype         ENGRAM_BF16 or ENGRAM_FP16, of q, k, v and o
+ * Scores, maxima and sums are fp32; the softmax's weights are rounded to the
+ * element type as operands of the product with v.  What a token does not see
+ * does not reach it, infinite or NaN as it may be.
+ */
+#define ENGRAM_WINDOW_ROWS_MAX 4194304
+#define ENGRAM_WINDOW_HEADS_MAX 1024
+#define ENGRAM_WINDOW_HEAD_ROWS_MAX 536870912 /* N * Hq */
+#define ENGRAM_WINDOW_SEQ_HEADS_MAX 4194304   /* B * Hk */
+#define ENGRAM_WINDOW_D_MAX 128
+#define ENGRAM_WINDOW_SINKS_MAX 128
+engram_status engram_window_attn_fwd(const void *q, const void *k, const void *v, const int64_t *cu_seqlens, void *o,
+                                     float *lse, int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                                     int64_t window, int64_t sinks, int64_t ldq, int64_t ldk, int64_t ldv, int64_t ldo,
+                                     float scale, int dtype, void *stream);
+
+/*
+ * Backward of the above for the gradient grad_o of o, from the forward's
+ * inputs, o and lse: the gradients of q, k and v, those of k and v summed over
+ * the query heads that read them.  Rows behind the last sequence are left as
+ * they are in the gradients.
+ *   grad_o, o [N][Hq][D]  in, leading dimensions ldgo, ldo
+ *   grad_q, grad_k, grad_v  out, as q, k, v, leading dimensions ldgq, ldgk, ldgv
+ *   workspace  engram_window_attn_bwd_workspace_bytes(...) bytes
+ */
+engram_status engram_window_attn_bwd(const void *grad_o, const void *q, const void *k, const void *v, const void *o,
+                                     const float *lse, const int64_t *cu_seqlens, void *grad_q, void *grad_k,
+                                     void *grad_v, void *workspace, int64_t N, int64_t B, int64_t Hq, int64_t Hk,
+                                     int64_t D, int64_t window, int64_t sinks, int64_t ldgo, int64_t ldq, int64_t ldk,
+                                     int64_t ldv, int64_t ldo, int64_t ldgq, int64_t ldgk, int64_t ldgv, float scale,
+                                     int dtype, void *stream);
+size_t engram_window_attn_bwd_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window,
+                                              int64_t sinks);
 
 /*
  * Gated recurrence of each channel.  For every sequence, with

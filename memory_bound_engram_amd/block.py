@@ -1,4 +1,4 @@
-"""Binding of the rest of a block around the gate: layer_norm, gated_scan.
+"""Binding of the rest of a block around the gate: layer_norm, window_attn, gated_scan.
 
 In the manner of the layers' binding, whose checks it shares: every tensor's
 element type, shape, layout and device is checked (ValueError otherwise, before
@@ -17,6 +17,8 @@ from memory_bound_engram_amd.layers import _Args, _shape
 _P, _I64, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 
 NORM_ROWS_MAX, NORM_D_MAX = 2097152, 16384
+WINDOW_ROWS_MAX, WINDOW_HEADS_MAX, WINDOW_HEAD_ROWS_MAX = 4194304, 1024, 536870912
+WINDOW_SEQ_HEADS_MAX, WINDOW_D_MAX, WINDOW_SINKS_MAX = 4194304, 128, 128
 SCAN_ROWS_MAX, SCAN_STATES_MAX, SCAN_D_MAX, SCAN_VALUES_MAX = 16777216, 4194304, 65536, 34359738368
 SCAN_STEP_ROWS_MAX = 4096
 
@@ -25,14 +27,16 @@ def _declare(lib):
     for name, args in {
         "engram_layer_norm_fwd": [_P] * 5 + [_I64] * 4 + [_F, _INT, _P],
         "engram_layer_norm_bwd": [_P] * 9 + [_I64] * 6 + [_INT, _P],
+        "engram_window_attn_fwd": [_P] * 6 + [_I64] * 11 + [_F, _INT, _P],
+        "engram_window_attn_bwd": [_P] * 11 + [_I64] * 15 + [_F, _INT, _P],
         "engram_gated_scan_fwd": [_P] * 7 + [_I64] * 6 + [_INT, _P],
         "engram_gated_scan_bwd": [_P] * 11 + [_I64] * 9 + [_INT, _P],
         "engram_gated_scan_step": [_P] * 5 + [_I64] * 6 + [_INT, _P],
     }.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = _INT
-    for name, n in {"engram_layer_norm_bwd_workspace_bytes": 2, "engram_gated_scan_fwd_workspace_bytes": 3,
-                    "engram_gated_scan_bwd_workspace_bytes": 3}.items():
+    for name, n in {"engram_layer_norm_bwd_workspace_bytes": 2, "engram_window_attn_bwd_workspace_bytes": 7,
+                    "engram_gated_scan_fwd_workspace_bytes": 3, "engram_gated_scan_bwd_workspace_bytes": 3}.items():
         getattr(lib, name).argtypes = [_I64] * n
         getattr(lib, name).restype = ctypes.c_size_t
 
@@ -40,7 +44,7 @@ def _declare(lib):
 _declare(_eg.lib)
 
 if _layers._torch is not None:
-    from memory_bound_engram_amd.layers import _CODE, _F32, _FLOATS, _INTS
+    from memory_bound_engram_amd.layers import _CODE, _F32, _FLOATS, _HALVES, _INTS
 
 
 def engram_layer_norm_fwd(x, w, y, b=None, saved=None, eps=1e-5, stream=None) -> None:
@@ -79,6 +83,57 @@ def engram_layer_norm_bwd(grad_y, x, w, saved, grad_x, workspace, grad_w=None, g
     ws = a.workspace(workspace, _eg.lib.engram_layer_norm_bwd_workspace_bytes(N, D))
     a.call(_eg.lib.engram_layer_norm_bwd, (pg, px, pw, ps, pr, pgx, pgw, pgb, ws, N, D, ldgy, ldx, ldgr, ldgx, _CODE[x.dtype]),
            stream)
+
+
+def _window_inputs(a, q, k, v):
+    N, Hq, D = _shape("q", q, 3)
+    Hk = _shape("k", k, 3)[1]
+    dt = (q.dtype,)
+    pq, ldq = a.rows("q", q, _HALVES, (N, Hq, D), Hq * D)
+    pk, ldk = a.rows("k", k, dt, (N, Hk, D), Hk * D)
+    pv, ldv = a.rows("v", v, dt, (N, Hk, D), Hk * D)
+    return (N, Hq, Hk, D), dt, (pq, pk, pv), (ldq, ldk, ldv)
+
+
+def engram_window_attn_fwd(q, k, v, cu_seqlens, o, window, sinks=0, lse=None, scale=1.0, stream=None) -> None:
+    """Enqueue softmax attention of each token over the last `window` tokens of
+    its sequence, itself among them, and its first `sinks` ones, over the
+    sequences that cu_seqlens [B+1] int64 (on the GPU) cuts the tokens into.
+    q, o [N,Hq,D], k, v [N,Hk,D] bf16 or fp16, tokens may be apart, Hq a multiple
+    of Hk.  lse [N,Hq] fp32, if given, takes the logarithms of the softmax's sums
+    for the backward."""
+    a = _Args()
+    (N, Hq, Hk, D), dt, ptrs, lds = _window_inputs(a, q, k, v)
+    B = _shape("cu_seqlens", cu_seqlens, 1)[0] - 1
+    pcu = a.dense("cu_seqlens", cu_seqlens, _INTS, (B + 1,))
+    po, ldo = a.rows("o", o, dt, (N, Hq, D), Hq * D)
+    pl = a.dense("lse", lse, _F32, (N, Hq))
+    a.call(_eg.lib.engram_window_attn_fwd, (*ptrs, pcu, po, pl, N, B, Hq, Hk, D, window, sinks, *lds, ldo, scale,
+           _CODE[q.dtype]), stream)
+
+
+def engram_window_attn_bwd_workspace_bytes(N: int, B: int, Hq: int, Hk: int, D: int, window: int, sinks: int) -> int:
+    """Scratch bytes of the window attention's backward."""
+    return int(_eg.lib.engram_window_attn_bwd_workspace_bytes(N, B, Hq, Hk, D, window, sinks))
+
+
+def engram_window_attn_bwd(grad_o, q, k, v, o, lse, cu_seqlens, grad_q, grad_k, grad_v, workspace, window, sinks=0,
+                           scale=1.0, stream=None) -> None:
+    """Enqueue the backward: the gradients of q, k and v (the latter two summed
+    over the query heads that read them) from grad_o and the forward's inputs, o
+    and lse."""
+    a = _Args()
+    (N, Hq, Hk, D), dt, ptrs, lds = _window_inputs(a, q, k, v)
+    B = _shape("cu_seqlens", cu_seqlens, 1)[0] - 1
+    pgo, ldgo = a.rows("grad_o", grad_o, dt, (N, Hq, D), Hq * D)
+    po, ldo = a.rows("o", o, dt, (N, Hq, D), Hq * D)
+    pl, pcu = a.dense("lse", lse, _F32, (N, Hq)), a.dense("cu_seqlens", cu_seqlens, _INTS, (B + 1,))
+    pgq, ldgq = a.rows("grad_q", grad_q, dt, (N, Hq, D), Hq * D)
+    pgk, ldgk = a.rows("grad_k", grad_k, dt, (N, Hk, D), Hk * D)
+    pgv, ldgv = a.rows("grad_v", grad_v, dt, (N, Hk, D), Hk * D)
+    ws = a.workspace(workspace, _eg.lib.engram_window_attn_bwd_workspace_bytes(N, B, Hq, Hk, D, window, sinks))
+    a.call(_eg.lib.engram_window_attn_bwd, (pgo, *ptrs, po, pl, pcu, pgq, pgk, pgv, ws, N, B, Hq, Hk, D, window, sinks,
+           ldgo, *lds, ldo, ldgq, ldgk, ldgv, scale, _CODE[q.dtype]), stream)
 
 
 def engram_gated_scan_fwd_workspace_bytes(N: int, B: int, D: int) -> int:
@@ -149,5 +204,6 @@ def engram_gated_scan_step(gate, u, state, slots, h, stream=None) -> None:
 
 
 __all__ = ["engram_layer_norm_fwd", "engram_layer_norm_bwd", "engram_layer_norm_bwd_workspace_bytes",
+           "engram_window_attn_fwd", "engram_window_attn_bwd", "engram_window_attn_bwd_workspace_bytes",
            "engram_gated_scan_fwd", "engram_gated_scan_bwd", "engram_gated_scan_step",
            "engram_gated_scan_fwd_workspace_bytes", "engram_gated_scan_bwd_workspace_bytes"]

@@ -1,5 +1,5 @@
 // engram_block_api.cpp -- the C entry points of the rest of a block around the
-// gate (layer_norm, gated_scan): argument validation on the host, then kernel
+// gate (layer_norm, window_attn, gated_scan): argument validation on the host, then kernel
 // launches on the caller's stream.  Nothing here allocates, copies or
 // synchronises.
 #include <hip/hip_runtime.h>
@@ -30,6 +30,17 @@ bool float_kind_ok(int dtype) { return dtype >= ENGRAM_BF16 && dtype <= ENGRAM_F
 int64_t bytes_of(int dtype) { return dtype == ENGRAM_FP32 ? 4 : 2; }
 
 bool norm_sizes_ok(int64_t N, int64_t D) { return in(N, 1, ENGRAM_NORM_ROWS_MAX) && in(D, 8, ENGRAM_NORM_D_MAX); }
+
+bool half_kind_ok(int dtype) { return dtype == ENGRAM_BF16 || dtype == ENGRAM_FP16; }
+
+bool window_sizes_ok(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks) {
+  return in(N, 1, ENGRAM_WINDOW_ROWS_MAX) && in(Hq, 1, ENGRAM_WINDOW_HEADS_MAX) && in(Hk, 1, Hq) && Hq % Hk == 0 &&
+         N <= ENGRAM_WINDOW_HEAD_ROWS_MAX / Hq && in(B, 1, ENGRAM_WINDOW_SEQ_HEADS_MAX / Hk) &&
+         in(D, 8, ENGRAM_WINDOW_D_MAX) && window >= 1 && in(sinks, 0, ENGRAM_WINDOW_SINKS_MAX);
+}
+bool scale_ok(float scale) { return scale > 0.0f && isfinite(scale); }
+
+Rows heads(const void* p, int64_t rows, int64_t ld, int64_t H, int64_t D) { return Rows{p, rows, ld * 2, H * D * 2}; }
 
 bool scan_sizes_ok(int64_t N, int64_t B, int64_t D) {
   return in(N, 1, ENGRAM_SCAN_ROWS_MAX) && in(B, 1, ENGRAM_SCAN_STATES_MAX) && in(D, 8, ENGRAM_SCAN_D_MAX) &&
@@ -93,6 +104,71 @@ engram_status engram_layer_norm_bwd(const void* grad_y, const void* x, const flo
   c.grad_x = grad_x; c.grad_w = grad_w; c.grad_b = grad_b; c.workspace = workspace;
   c.N = N; c.D = D; c.ldgy = ldgy; c.ldx = ldx; c.ldgr = ldgr; c.ldgx = ldgx; c.dtype = dtype;
   return launched(engram::launch_layer_norm_bwd(c, (hipStream_t)stream));
+}
+
+size_t engram_window_attn_bwd_workspace_bytes(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window,
+                                              int64_t sinks) {
+  if (!window_sizes_ok(N, B, Hq, Hk, D, window, sinks) || D % 8) return 0;
+  return engram::window_bwd_workspace(N, B, Hq, Hk, D, window, sinks);
+}
+
+engram_status engram_window_attn_fwd(const void* q, const void* k, const void* v, const int64_t* cu_seqlens, void* o,
+                                     float* lse, int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window,
+                                     int64_t sinks, int64_t ldq, int64_t ldk, int64_t ldv, int64_t ldo, float scale,
+                                     int dtype, void* stream) {
+  if (!q || !k || !v || !cu_seqlens || !o) return ENGRAM_ERR_NULL;
+  if (!half_kind_ok(dtype)) return ENGRAM_ERR_KIND;
+  if (!window_sizes_ok(N, B, Hq, Hk, D, window, sinks) || !ld_in_range(ldq, Hq * D) || !ld_in_range(ldk, Hk * D) ||
+      !ld_in_range(ldv, Hk * D) || !ld_in_range(ldo, Hq * D) || !scale_ok(scale))
+    return ENGRAM_ERR_N_RANGE;
+  if ((D | ldq | ldk | ldv | ldo) % 8 || !aligned8(cu_seqlens)) return ENGRAM_ERR_ALIGN;
+  const void* ptrs[] = {q, k, v, o, lse};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ENGRAM_ERR_ALIGN;
+  const Rows ins[] = {heads(q, N, ldq, Hq, D), heads(k, N, ldk, Hk, D), heads(v, N, ldv, Hk, D),
+                      flat(cu_seqlens, (B + 1) * 8)};
+  const Rows outs[] = {heads(o, N, ldo, Hq, D), flat(lse, N * Hq * 4)};
+  if (any_overlap(ins, 4, outs, 2)) return ENGRAM_ERR_OVERLAP;
+  engram::WindowCall w{};
+  w.q = static_cast<const uint16_t*>(q); w.k = static_cast<const uint16_t*>(k); w.v = static_cast<const uint16_t*>(v);
+  w.cu = cu_seqlens; w.o = static_cast<uint16_t*>(o); w.lse = lse;
+  w.N = N; w.B = B; w.Hq = Hq; w.Hk = Hk; w.D = D; w.window = window; w.sinks = sinks;
+  w.ldq = ldq; w.ldk = ldk; w.ldv = ldv; w.ldo = ldo; w.scale = scale; w.dtype = dtype;
+  return launched(engram::launch_window_fwd(w, (hipStream_t)stream));
+}
+
+engram_status engram_window_attn_bwd(const void* grad_o, const void* q, const void* k, const void* v, const void* o,
+                                     const float* lse, const int64_t* cu_seqlens, void* grad_q, void* grad_k,
+                                     void* grad_v, void* workspace, int64_t N, int64_t B, int64_t Hq, int64_t Hk,
+                                     int64_t D, int64_t window, int64_t sinks, int64_t ldgo, int64_t ldq, int64_t ldk,
+                                     int64_t ldv, int64_t ldo, int64_t ldgq, int64_t ldgk, int64_t ldgv, float scale,
+                                     int dtype, void* stream) {
+  if (!grad_o || !q || !k || !v || !o || !lse || !cu_seqlens || !grad_q || !grad_k || !grad_v || !workspace)
+    return ENGRAM_ERR_NULL;
+  if (!half_kind_ok(dtype)) return ENGRAM_ERR_KIND;
+  if (!window_sizes_ok(N, B, Hq, Hk, D, window, sinks) || !ld_in_range(ldgo, Hq * D) || !ld_in_range(ldq, Hq * D) ||
+      !ld_in_range(ldk, Hk * D) || !ld_in_range(ldv, Hk * D) || !ld_in_range(ldo, Hq * D) || !ld_in_range(ldgq, Hq * D) ||
+      !ld_in_range(ldgk, Hk * D) || !ld_in_range(ldgv, Hk * D) || !scale_ok(scale))
+    return ENGRAM_ERR_N_RANGE;
+  if ((D | ldgo | ldq | ldk | ldv | ldo | ldgq | ldgk | ldgv) % 8 || !aligned8(cu_seqlens)) return ENGRAM_ERR_ALIGN;
+  const void* ptrs[] = {grad_o, q, k, v, o, lse, grad_q, grad_k, grad_v, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ENGRAM_ERR_ALIGN;
+  const Rows ins[] = {heads(grad_o, N, ldgo, Hq, D), heads(q, N, ldq, Hq, D), heads(k, N, ldk, Hk, D),
+                      heads(v, N, ldv, Hk, D), heads(o, N, ldo, Hq, D), flat(lse, N * Hq * 4),
+                      flat(cu_seqlens, (B + 1) * 8)};
+  const Rows outs[] = {heads(grad_q, N, ldgq, Hq, D), heads(grad_k, N, ldgk, Hk, D), heads(grad_v, N, ldgv, Hk, D),
+                       flat(workspace, (int64_t)engram::window_bwd_workspace(N, B, Hq, Hk, D, window, sinks))};
+  if (any_overlap(ins, 7, outs, 4)) return ENGRAM_ERR_OVERLAP;
+  engram::WindowCall w{};
+  w.grad_o = static_cast<const uint16_t*>(grad_o); w.q = static_cast<const uint16_t*>(q);
+  w.k = static_cast<const uint16_t*>(k); w.v = static_cast<const uint16_t*>(v); w.o_in = static_cast<const uint16_t*>(o);
+  w.lse_in = lse; w.cu = cu_seqlens; w.grad_q = static_cast<uint16_t*>(grad_q);
+  w.grad_k = static_cast<uint16_t*>(grad_k); w.grad_v = static_cast<uint16_t*>(grad_v); w.workspace = workspace;
+  w.N = N; w.B = B; w.Hq = Hq; w.Hk = Hk; w.D = D; w.window = window; w.sinks = sinks;
+  w.ldgo = ldgo; w.ldq = ldq; w.ldk = ldk; w.ldv = ldv; w.ldo = ldo; w.ldgq = ldgq; w.ldgk = ldgk; w.ldgv = ldgv;
+  w.scale = scale; w.dtype = dtype;
+  return launched(engram::launch_window_bwd(w, (hipStream_t)stream));
 }
 
 size_t engram_gated_scan_fwd_workspace_bytes(int64_t N, int64_t B, int64_t D) { return scan_workspace_bytes(N, B, D); }

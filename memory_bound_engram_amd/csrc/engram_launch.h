@@ -136,6 +136,23 @@ size_t layer_norm_bwd_workspace(int64_t N, int64_t D);
 hipError_t launch_layer_norm_fwd(const NormCall& c, hipStream_t stream);
 hipError_t launch_layer_norm_bwd(const NormCall& c, hipStream_t stream);
 
+// Window attention: one call's arguments.
+struct WindowCall {
+  const uint16_t *q, *k, *v, *o_in, *grad_o;
+  const int64_t* cu;            // forward, backward: [B + 1]
+  const float* lse_in;
+  uint16_t *o, *grad_q, *grad_k, *grad_v;
+  float* lse;
+  void* workspace;
+  int64_t N, B, Hq, Hk, D, window, sinks;
+  int64_t ldq, ldk, ldv, ldo, ldgo, ldgq, ldgk, ldgv;
+  float scale;
+  int dtype;
+};
+size_t window_bwd_workspace(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks);
+hipError_t launch_window_fwd(const WindowCall& w, hipStream_t stream);
+hipError_t launch_window_bwd(const WindowCall& w, hipStream_t stream);
+
 // Gated scan: one call's arguments.
 struct ScanCall {
   const void *gate, *u, *h_in, *grad_h;

@@ -1,0 +1,742 @@
+// engram_window.hip -- softmax attention over a sliding window and the first
+// tokens of each sequence: forward and backward over ragged sequences (gfx950).
+//
+// Token i of a sequence sees token j <= i if i - j < W (the window) or j < S (the
+// sinks); query head h reads key head h / G.  With c = scale log2(e):
+//   s_ij = q_i . k_j,  lse_i = ln sum_j exp(scale s_ij),  p_ij = exp(scale s_ij - lse_i)
+//   o_i = sum_j p_ij v_j
+// Backward, with delta_i = do_i . o_i and d_ij = p_ij (do_i . v_j - delta_i):
+//   dq_i = scale sum_j d_ij k_j,  dk_j = scale sum_i d_ij q_i,  dv_j = sum_i p_ij do_i
+// the sums over i also over the G query heads of the key head.
+//
+// Mapping.  The rows of a sequence and key head are its (token, query head) pairs,
+// token after token, so that a narrow window, a short sequence or a few heads
+// still make whole tiles.  A workgroup of four waves takes 128 rows, a wave 32;
+// the keys that any of them sees, first the sinks that lie before the window,
+// come through LDS in tiles of 64, straight from memory, one tile ahead.  Scores
+// are computed transposed, so a lane has one row, and rows and columns of the
+// softmax stay where the products leave them: its maximum and sum are a lane's own,
+// and the weights, rounded, are the next product's operand without going through
+// LDS.
+//
+// The backward has two such kernels: over the keys of 128 rows for dq (and
+// delta, which it leaves for the other), and over the rows of 128 keys for dk and
+// dv: seven products where five are the least, but no sums of atomics and no partial
+// sums in memory.  Sinks are seen by all rows behind the window as well; those
+// rows' part of their dk and dv is summed in pieces of the sequence by a
+// launch of its own and added by the workgroup that has the sinks' window part.
+//
+// Rounding.  Sums, maxima and the softmax are fp32.  p and d are rounded to the
+// element type as operands of the second products; the sum of p is taken
+// unrounded.  (fp16: p <= 1, and what is below 2^-24 of the largest may vanish; d
+// beyond 65504 becomes infinite.)
+//
+// Where p is 0 because j is not seen, the product with v_j would still be NaN if
+// v_j is not finite.  Results that come out not finite are computed again by the
+// definition, row by row, over what is seen alone.
+#include "engram_launch.h"
+#include "engram_sequences.h"
+#include "engram_window_tiles.h"
+
+namespace engram {
+namespace {
+
+constexpr int kWaves = 4, kThreads = kWaves * 64;
+constexpr int kRows = 128;  // (token, head) pairs, or keys, of a workgroup
+constexpr int kKeys = 64;   // of a tile
+
+struct WindowArgs {
+  const uint16_t *q, *k, *v, *o, *grad_o;
+  const int64_t* cu;
+  const float* lse_in;
+  uint16_t *out, *grad_k, *grad_v;  // out: o, or the gradient of q
+  float* lse;                       // forward: written if not null
+  float* delta;                     // backward: [N][Hq]
+  float* sums;                      // backward: the sinks' sums over pieces of the sequences
+  int64_t N, ldq, ldk, ldv, ldo, ldgo, ldout, ldgk, ldgv;
+  int B, Hk, G, D, W, S;
+  int tiles;                        // workgroups of a key head
+  int piece;                        // backward: tokens of a piece (sinks)
+  float scale;
+  Divide by_G;
+};
+
+// The workgroups of all key heads, those of a head neighbours on one XCD
+// (workgroups go round the eight), so that its L2 serves the keys they share.
+__device__ __forceinline__ int neighbours(int block, int blocks) {
+  const int each = blocks / 8, rest = blocks % 8, x = block % 8;
+  return x * each + (x < rest ? x : rest) + block / 8;
+}
+
+// Which sequence a workgroup is in, and which tile of it: sequence b has the
+// numbers from first_tile(b) on, as many as its tiles of `unit` rows at least
+// (`per` rows a token).
+__device__ __forceinline__ int64_t first_tile(const Sequences& seqs, int b, int64_t per, int64_t unit) {
+  return seqs.start(b) * per / unit + b;
+}
+__device__ __forceinline__ int sequence_of(const Sequences& seqs, int64_t id, int64_t per, int64_t unit, int64_t* tile) {
+  int lo = 0, hi = seqs.B - 1;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (first_tile(seqs, mid, per, unit) <= id) lo = mid;
+    else hi = mid - 1;
+  }
+  *tile = id - first_tile(seqs, lo, per, unit);  // negative before the first sequence
+  return lo;
+}
+
+__device__ __forceinline__ bool sees(int t, int j, int W, int S) { return j <= t && (j > t - W || j < S); }
+
+// The keys of a run of tokens, as tiles of kKeys: the sinks before the window, then the window.
+struct KeyTiles {
+  int sinks, from, to, n_sinks, n;  // the window is from .. to
+  __device__ __forceinline__ KeyTiles(int first, int last, int W, int S) {
+    from = first - W + 1 > 0 ? first - W + 1 : 0;
+    to = last + 1;
+    sinks = S < from ? S : from;
+    if (sinks == from) sinks = from = 0;  // they meet
+    n_sinks = (sinks + kKeys - 1) / kKeys;
+    n = n_sinks + (to - from + kKeys - 1) / kKeys;
+  }
+  __device__ __forceinline__ int start(int i) const { return i < n_sinks ? i * kKeys : from + (i - n_sinks) * kKeys; }
+  __device__ __forceinline__ int end(int i) const { return i < n_sinks ? sinks : to; }  // of the run the tile is in
+};
+
+// A workgroup's rows of a sequence and key head.
+struct RowTile {
+  int64_t base;      // the sequence's first token
+  int length, head;  // tokens; key head
+  int t0;            // the first row's token
+  uint32_t x0;       // and head
+  int rows;          // there are, kRows at most
+  __device__ __forceinline__ uint32_t token(uint32_t row, const WindowArgs& a, uint32_t* g) const {
+    const uint32_t x = x0 + row, t = a.by_G(x);
+    *g = x - t * (uint32_t)a.G;
+    return t;
+  }
+};
+
+__device__ __forceinline__ bool row_tile(const WindowArgs& a, RowTile* r) {
+  const int at = neighbours(blockIdx.x, gridDim.x);
+  const Sequences seqs{a.cu, a.N, a.B};
+  int64_t tile;
+  const int b = sequence_of(seqs, at % a.tiles, a.G, kRows, &tile);
+  r->head = at / a.tiles;
+  r->base = seqs.start(b);
+  const int64_t length = seqs.end(b) - r->base, first = tile * kRows, all = length * a.G;
+  if (tile < 0 || length <= 0 || first >= all) return false;
+  r->length = (int)length;
+  r->t0 = (int)(first / a.G);
+  r->x0 = (uint32_t)(first % a.G);
+  r->rows = (int)(all - first < kRows ? all - first : kRows);
+  return true;
+}
+
+// A lane's row of 8-value pieces, as the operand of kD / 16 products.
+template <int kD>
+__device__ __forceinline__ void load_row(u32x4 (&to)[kD / 16], const uint16_t* p, bool there, int D, int h) {
+#pragma unroll
+  for (int kk = 0; kk < kD / 16; ++kk) {
+    const u32x4 zero = {0, 0, 0, 0};
+    to[kk] = there && 16 * kk + 8 * h < D ? load16(p + 16 * kk + 8 * h) : zero;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float one_value(uint16_t v) {
+  if constexpr (__is_same(T, bf16_t)) return __uint_as_float((uint32_t)v << 16);
+  else return (float)__builtin_bit_cast(_Float16, v);
+}
+template <typename T>
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b) {
+  float x[8], y[8], s = 0.0f;
+  unpack8(Raw<T>{{a}}, x);
+  unpack8(Raw<T>{{b}}, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+  return s;
+}
+// The product of two rows, by one lane.
+template <typename T>
+__device__ __forceinline__ float dot_row(const uint16_t* a, const uint16_t* b, int D) {
+  float s = 0.0f;
+  for (int d = 0; d < D; d += 8) s += dot8<T>(load16(a + d), load16(b + d));
+  return s;
+}
+
+// Between a wave's writes to LDS and its lanes' reads of each other's.
+__device__ __forceinline__ void between_lanes() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Accumulators as rows in LDS: a lane's row is column l % 32 of each, its values
+// 32 dt + 8 j + 4 h + 0..3; a wave's 32 rows of kD values.
+template <typename T, int kD>
+__device__ __forceinline__ void put_rows(uint16_t* to, const f32x16 (&v)[kD / 32], float times, uint32_t lane) {
+  const uint32_t row = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x2 w = {pack2<T>(v[dt][4 * j] * times, v[dt][4 * j + 1] * times),
+                       pack2<T>(v[dt][4 * j + 2] * times, v[dt][4 * j + 3] * times)};
+      *reinterpret_cast<u32x2*>(to + place<kD>(row, 32 * dt + 8 * j + 4 * h)) = w;
+    }
+}
+
+// A wave's rows out to memory, whole, sixteen bytes a lane.
+template <int kD>
+__device__ __forceinline__ void store_rows(const uint16_t* mine, const RowTile& r, uint32_t wave, uint32_t lane,
+                                           const WindowArgs& a) {
+  between_lanes();
+#pragma unroll
+  for (int i = 0; i < kD / 16; ++i) {
+    const uint32_t at = i * 64 + lane, row = at / (kD / 8), col = at % (kD / 8) * 8;
+    uint32_t g;
+    const uint32_t t = r.token(32 * wave + row, a, &g);
+    if ((int)(32 * wave + row) < r.rows && (int)col < a.D)
+      store16(a.out + (r.base + r.t0 + t) * a.ldout + (int64_t)(r.head * a.G + g) * a.D + col,
+              load16(mine + place<kD>(row, col)));
+  }
+}
+
+template <int kD>
+__device__ __forceinline__ bool finite_rows(const f32x16 (&v)[kD / 32], float times) {
+  float s = 0.0f;
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s = fmaf(v[dt][i] * times, 0.0f, s);
+  return s == 0.0f;
+}
+
+template <typename T, int kD>
+__global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kKeys * kD];  // [turn][keys, values]
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t l = lane & 31, h = lane >> 5;
+  RowTile r;
+  if (!row_tile(a, &r)) return;
+  const int row = 32 * wave + l;
+  uint32_t g;
+  const uint32_t dt_ = r.token(row, a, &g);
+  const bool there = row < r.rows;
+  const int t = there ? r.t0 + (int)dt_ : -1;  // -1 sees nothing
+  uint32_t g_last;
+  const int first = r.t0, last = r.t0 + (int)r.token(r.rows - 1, a, &g_last);
+  const int head = r.head * a.G + (int)g;
+  u32x4 q[kD / 16];
+  load_row<kD>(q, a.q + (r.base + (there ? t : 0)) * a.ldq + (int64_t)head * a.D, there, a.D, h);
+
+  const KeyTiles keys(first, last, a.W, a.S);
+  const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
+  const auto fetch = [&](int i) {
+    const int start = keys.start(i), n = keys.end(i) - start;
+    const int64_t token = r.base + start;
+    pieces.fetch(lds[i & 1][0], a.k + token * a.ldk + (int64_t)r.head * a.D, a.D, wave,
+                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldk * 2) : kBeyond; });
+    pieces.fetch(lds[i & 1][1], a.v + token * a.ldv + (int64_t)r.head * a.D, a.D, wave,
+                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldv * 2) : kBeyond; });
+  };
+  const RowReader<kD> rows(lane);
+  const ColumnReader<kD> columns(lane);
+  const float c = a.scale * kLog2e;
+  f32x16 o[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) o[dt] = f32x16{};
+  float m = -INFINITY, sum = 0.0f;
+  fetch(0);
+  for (int i = 0; i < keys.n; ++i) {
+    meet();
+    if (i + 1 < keys.n) fetch(i + 1);
+    const uint16_t *tk = lds[i & 1][0], *tv = lds[i & 1][1];
+    f32x16 s[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+    for (int kk = 0; kk < kD / 16; ++kk)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) s[u] = product<T>(rows(tk, 32 * u, kk), q[kk], s[u]);
+    const int start = keys.start(i), end = keys.end(i);
+    // some row of the tile does not see some key
+    if (start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= a.S)) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = start + 32 * u + 8 * (e / 4) + 4 * (int)h + e % 4;
+          s[u][e] = j < end && sees(t, j, a.W, a.S) ? s[u][e] : -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+    top = fmaxf(m, column_max(top));
+    if (__any(top > m)) {
+      const float keep = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * c);
+      sum *= keep;
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt) o[dt] *= keep;
+      m = top;
+    }
+    const float less = m == -INFINITY ? 0.0f : -m * c;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[u][e] = __builtin_amdgcn_exp2f(fmaf(s[u][e], c, less));
+        sum += s[u][e];
+      }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const u32x4 p = operand<T>(s[w / 2], w % 2);
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt) o[dt] = product<T>(columns(tv, 16 * w, dt), p, o[dt]);
+    }
+  }
+  sum = column_sum(sum);
+  const float inverse = 1.0f / sum;
+  if (a.lse && there && h == 0) a.lse[(r.base + t) * (int64_t)(a.Hk * a.G) + head] = fmaf(m, c, __log2f(sum)) * kLn2;
+
+  __syncthreads();  // the tiles are read out
+  uint16_t* mine = lds[0][0] + wave * 32 * kD;
+  put_rows<T, kD>(mine, o, inverse, lane);
+  // rows that are not finite though their weights are, by the definition
+  const uint64_t redo = __ballot(there && !finite_rows<kD>(o, inverse) && fabsf(m) < INFINITY && sum < INFINITY);
+  between_lanes();
+  for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
+    const int x = __builtin_ctz(bad);
+    const int tx = __shfl(t, x), hx = __shfl(head, x);
+    const float mx = __shfl(m, x), ix = __shfl(inverse, x);
+    const uint16_t* qx = a.q + (r.base + tx) * a.ldq + (int64_t)hx * a.D;
+    float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
+    for (int i = 0; i < keys.n; ++i) {
+      const int j = keys.start(i) + (int)lane;
+      const bool seen = j < keys.end(i) && sees(tx, j, a.W, a.S);
+      const float s = seen ? dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D) : 0.0f;
+      const float p = __builtin_amdgcn_exp2f((s - mx) * c) * ix;
+      for (uint64_t left = __ballot(seen); left; left &= left - 1) {
+        const int n = __builtin_ctzll(left);
+        const uint16_t* vx = a.v + (r.base + keys.start(i) + n) * a.ldv + (int64_t)r.head * a.D;
+        const float pn = __shfl(p, n);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if ((int)lane + 64 * e < a.D) y[e] = fmaf(pn, one_value<T>(vx[lane + 64 * e]), y[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e], 0.0f);
+  }
+  store_rows<kD>(mine, r, wave, lane, a);
+}
+
+// dq of 128 rows, and delta.
+template <typename T, int kD>
+__global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kKeys * kD];  // [turn][keys, values]
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t l = lane & 31, h = lane >> 5;
+  RowTile r;
+  if (!row_tile(a, &r)) return;
+  const int row = 32 * wave + l;
+  uint32_t g, g_last;
+  const uint32_t ahead = r.token(row, a, &g);
+  const bool there = row < r.rows;
+  const int t = there ? r.t0 + (int)ahead : -1;  // -1 sees nothing
+  const int first = r.t0, last = r.t0 + (int)r.token(r.rows - 1, a, &g_last);
+  const int head = r.head * a.G + (int)g;
+  const int64_t token = r.base + (there ? t : 0), at_head = token * (a.Hk * a.G) + head;
+  u32x4 q[kD / 16], go[kD / 16];
+  load_row<kD>(q, a.q + token * a.ldq + (int64_t)head * a.D, there, a.D, h);
+  load_row<kD>(go, a.grad_o + token * a.ldgo + (int64_t)head * a.D, there, a.D, h);
+  const float lse = there ? a.lse_in[at_head] * kLog2e : 0.0f;
+  float delta = 0.0f;
+  {
+    u32x4 o[kD / 16];
+    load_row<kD>(o, a.o + token * a.ldo + (int64_t)head * a.D, there, a.D, h);
+#pragma unroll
+    for (int kk = 0; kk < kD / 16; ++kk) delta += dot8<T>(go[kk], o[kk]);
+    delta = column_sum(delta);
+    if (there && h == 0) a.delta[at_head] = delta;
+  }
+
+  const KeyTiles keys(first, last, a.W, a.S);
+  const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
+  const auto fetch = [&](int i) {
+    const int start = keys.start(i), n = keys.end(i) - start;
+    const int64_t from = r.base + start;
+    pieces.fetch(lds[i & 1][0], a.k + from * a.ldk + (int64_t)r.head * a.D, a.D, wave,
+                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldk * 2) : kBeyond; });
+    pieces.fetch(lds[i & 1][1], a.v + from * a.ldv + (int64_t)r.head * a.D, a.D, wave,
+                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldv * 2) : kBeyond; });
+  };
+  const RowReader<kD> rows(lane);
+  const ColumnReader<kD> columns(lane);
+  const float c = a.scale * kLog2e;
+  f32x16 dq[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) dq[dt] = f32x16{};
+  fetch(0);
+  for (int i = 0; i < keys.n; ++i) {
+    meet();
+    if (i + 1 < keys.n) fetch(i + 1);
+    const uint16_t *tk = lds[i & 1][0], *tv = lds[i & 1][1];
+    const int start = keys.start(i), end = keys.end(i);
+    const bool some = start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= a.S);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x16 s = f32x16{}, d = f32x16{};
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk) s = product<T>(rows(tk, 32 * u, kk), q[kk], s);
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk) d = product<T>(rows(tv, 32 * u, kk), go[kk], d);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) d[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse)) * (d[e] - delta);
+      if (some) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = start + 32 * u + 8 * (e / 4) + 4 * (int)h + e % 4;
+          d[e] = j < end && sees(t, j, a.W, a.S) ? d[e] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const u32x4 p = operand<T>(d, w);
+#pragma unroll
+        for (int dt = 0; dt < kD / 32; ++dt) dq[dt] = product<T>(columns(tk, 32 * u + 16 * w, dt), p, dq[dt]);
+      }
+    }
+  }
+
+  __syncthreads();  // the tiles are read out
+  uint16_t* mine = lds[0][0] + wave * 32 * kD;
+  put_rows<T, kD>(mine, dq, a.scale, lane);
+  const uint64_t redo = __ballot(there && !finite_rows<kD>(dq, a.scale) && fabsf(lse) < INFINITY && fabsf(delta) < INFINITY);
+  between_lanes();
+  for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
+    const int x = __builtin_ctz(bad);
+    const int tx = __shfl(t, x), hx = __shfl(head, x);
+    const float lx = __shfl(lse, x), dx = __shfl(delta, x);
+    const uint16_t* qx = a.q + (r.base + tx) * a.ldq + (int64_t)hx * a.D;
+    const uint16_t* gx = a.grad_o + (r.base + tx) * a.ldgo + (int64_t)hx * a.D;
+    float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
+    for (int i = 0; i < keys.n; ++i) {
+      const int j = keys.start(i) + (int)lane;
+      const bool seen = j < keys.end(i) && sees(tx, j, a.W, a.S);
+      float d = 0.0f;
+      if (seen) {
+        const float s = dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D);
+        const float dp = dot_row<T>(gx, a.v + (r.base + j) * a.ldv + (int64_t)r.head * a.D, a.D);
+        d = __builtin_amdgcn_exp2f(fmaf(s, c, -lx)) * (dp - dx);
+      }
+      for (uint64_t left = __ballot(seen); left; left &= left - 1) {
+        const int n = __builtin_ctzll(left);
+        const uint16_t* kx = a.k + (r.base + keys.start(i) + n) * a.ldk + (int64_t)r.head * a.D;
+        const float dn = __shfl(d, n);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if ((int)lane + 64 * e < a.D) y[e] = fmaf(dn, one_value<T>(kx[lane + 64 * e]), y[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e] * a.scale, 0.0f);
+  }
+  store_rows<kD>(mine, r, wave, lane, a);
+}
+
+// The sums of a piece of a sequence: [piece][key head][dk, dv][S][D].
+__device__ __forceinline__ float* piece_sums(const WindowArgs& a, int64_t piece, int head, int which) {
+  return a.sums + ((piece * a.Hk + head) * 2 + which) * a.S * a.D;
+}
+
+// dk and dv of 128 keys.  kSinks: the part of the sinks' (the first keys of a
+// sequence) that comes from the rows of one piece of it that see them as sinks,
+// fp32 and unscaled; otherwise the rows whose window the keys are in, and for sinks
+// the pieces' sums.
+template <typename T, int kD, bool kSinks>
+__global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kKeys * kD];  // [turn][queries, gradients of o] of 64 rows
+  __shared__ __attribute__((aligned(16))) float lses[2][kKeys], deltas[2][kKeys];
+  __shared__ __attribute__((aligned(16))) int tokens[2][kKeys];
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t l = lane & 31, h = lane >> 5;
+  const int at = neighbours(blockIdx.x, gridDim.x), id = at % a.tiles, head = at / a.tiles;
+  const Sequences seqs{a.cu, a.N, a.B};
+  int64_t tile;
+  const int b = sequence_of(seqs, id, 1, kSinks ? a.piece : kRows, &tile);
+  const int64_t base = seqs.start(b);
+  const int length = (int)(seqs.end(b) - base);
+  const int64_t unit = kSinks ? a.piece : kRows;
+  if (tile < 0 || length <= 0 || tile * unit >= length) return;
+  const int k0 = kSinks ? 0 : (int)tile * kRows;
+  // the rows' tokens
+  int from = k0, to = k0 + kRows - 1 + a.W;
+  if (kSinks) {
+    from = (int)tile * a.piece > a.W ? (int)tile * a.piece : a.W;
+    to = ((int)tile + 1) * a.piece;
+  }
+  if (to > length) to = length;
+  if (from >= to) return;  // no row of the piece sees a sink as one
+
+  const int key0 = k0 + 32 * wave, key = key0 + (int)l;
+  const int keys = kSinks ? (a.S < length ? a.S : length) : length;  // of the sequence, as far as they matter here
+  const bool active = key0 < keys, there = key < keys;
+  u32x4 k[kD / 16], v[kD / 16];
+  const int64_t key_token = base + (there ? key : 0);
+  load_row<kD>(k, a.k + key_token * a.ldk + (int64_t)head * a.D, there, a.D, h);
+  load_row<kD>(v, a.v + key_token * a.ldv + (int64_t)head * a.D, there, a.D, h);
+
+  const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
+  const int n = ((to - from) * a.G + kKeys - 1) / kKeys;  // tiles of rows
+  const int Hq = a.Hk * a.G;
+  float lse = 0.0f, delta = 0.0f;
+  int token = 0;
+  int t0 = from;      // of the next tile to fetch: its first row's token and head
+  uint32_t x0 = 0;
+  const auto fetch = [&](int i) {
+    const auto row_at = [&](uint32_t row, uint32_t* t, uint32_t* g) {
+      const uint32_t x = x0 + row;
+      *t = a.by_G(x);
+      *g = x - *t * (uint32_t)a.G;
+      return t0 + (int)*t < to;
+    };
+    const int64_t first = base + t0, heads = (int64_t)head * a.G * a.D;
+    const auto offset = [&](uint32_t row, int64_t ld) {
+      uint32_t t, g;
+      return row_at(row, &t, &g) ? t * (uint32_t)(ld * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
+    };
+    pieces.fetch(lds[i & 1][0], a.q + first * a.ldq + heads, a.D, wave, [&](uint32_t row) { return offset(row, a.ldq); });
+    pieces.fetch(lds[i & 1][1], a.grad_o + first * a.ldgo + heads, a.D, wave,
+                 [&](uint32_t row) { return offset(row, a.ldgo); });
+    if (wave == 0) {
+      uint32_t t, g;
+      const bool in = row_at(lane, &t, &g);
+      const int64_t at = (first + (in ? t : 0)) * Hq + head * a.G + (in ? g : 0);
+      // a row that is not there has weights of 0
+      lse = in ? a.lse_in[at] * kLog2e : INFINITY;
+      delta = in ? a.delta[at] : 0.0f;
+      token = t0 + (int)t;
+    }
+    x0 += kKeys;
+    t0 += (int)a.by_G(x0);
+    x0 -= a.by_G(x0) * (uint32_t)a.G;
+  };
+  const RowReader<kD> rows(lane);
+  const ColumnReader<kD> columns(lane);
+  const float c = a.scale * kLog2e;
+  f32x16 dk[kD / 32], dv[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
+  fetch(0);
+  for (int i = 0; i < n; ++i) {
+    if (wave == 0) {
+      lses[i & 1][lane] = lse;
+      deltas[i & 1][lane] = delta;
+      tokens[i & 1][lane] = token;
+    }
+    meet();
+    if (i + 1 < n) fetch(i + 1);
+    if (!active) continue;
+    const uint16_t *tq = lds[i & 1][0], *tg = lds[i & 1][1];
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      const int ta = tokens[i & 1][32 * u], tb = tokens[i & 1][32 * u + 31];  // the rows' first and last token
+      if (kSinks ? key0 > tb - a.W : key0 > tb || key0 + 31 <= ta - a.W) continue;
+      f32x16 s = f32x16{}, d = f32x16{};
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk) s = product<T>(rows(tq, 32 * u, kk), k[kk], s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk) d = product<T>(rows(tg, 32 * u, kk), v[kk], d);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&lses[i & 1][32 * u + 8 * j + 4 * h]);
+        const f32x4 de = *reinterpret_cast<const f32x4*>(&deltas[i & 1][32 * u + 8 * j + 4 * h]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], c, -ls[e]));
+          d[4 * j + e] = s[4 * j + e] * (d[4 * j + e] - de[e]);
+        }
+      }
+      if (kSinks ? key0 + 31 > ta - a.W || key0 + 31 >= keys : key0 + 31 > ta || key0 <= tb - a.W) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int t = tokens[i & 1][32 * u + 8 * (e / 4) + 4 * h + e % 4];
+          const bool seen = kSinks ? key <= t - a.W && key < keys : key <= t && key > t - a.W;
+          s[e] = seen ? s[e] : 0.0f;
+          d[e] = seen ? d[e] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const u32x4 p = operand<T>(s, w), e = operand<T>(d, w);
+#pragma unroll
+        for (int dt = 0; dt < kD / 32; ++dt) {
+          __builtin_amdgcn_sched_barrier(0);
+          dv[dt] = product<T>(columns(tg, 32 * u + 16 * w, dt), p, dv[dt]);
+          dk[dt] = product<T>(columns(tq, 32 * u + 16 * w, dt), e, dk[dt]);
+        }
+      }
+    }
+  }
+
+  if (kSinks) {
+    if (there) {
+      float *to_k = piece_sums(a, id, head, 0) + (int64_t)key * a.D, *to_v = piece_sums(a, id, head, 1) + (int64_t)key * a.D;
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int col = 32 * dt + 8 * j + 4 * (int)h;
+          if (col >= a.D) continue;
+          *reinterpret_cast<f32x4*>(to_k + col) = f32x4{dk[dt][4 * j], dk[dt][4 * j + 1], dk[dt][4 * j + 2], dk[dt][4 * j + 3]};
+          *reinterpret_cast<f32x4*>(to_v + col) = f32x4{dv[dt][4 * j], dv[dt][4 * j + 1], dv[dt][4 * j + 2], dv[dt][4 * j + 3]};
+        }
+    }
+    return;
+  }
+  if (key < a.S && there && length > a.W) {
+    const int64_t mine = first_tile(seqs, b, 1, a.piece);
+    for (int p = a.W / a.piece; p <= (length - 1) / a.piece; ++p) {
+      const float *from_k = piece_sums(a, mine + p, head, 0) + (int64_t)key * a.D;
+      const float *from_v = piece_sums(a, mine + p, head, 1) + (int64_t)key * a.D;
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int col = 32 * dt + 8 * j + 4 * (int)h;
+          if (col >= a.D) continue;
+          const f32x4 x = *reinterpret_cast<const f32x4*>(from_k + col), y = *reinterpret_cast<const f32x4*>(from_v + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dk[dt][4 * j + e] += x[e];
+            dv[dt][4 * j + e] += y[e];
+          }
+        }
+    }
+  }
+
+  __syncthreads();  // the tiles are read out
+  uint16_t* mine = lds[0][0] + wave * 32 * kD;
+  const auto finish = [&](const int which, const f32x16(&sum)[kD / 32]) {
+    const float times = which ? 1.0f : a.scale;
+    put_rows<T, kD>(mine, sum, times, lane);
+    const uint64_t redo = __ballot(there && !finite_rows<kD>(sum, times));
+    between_lanes();
+    for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
+      const int x = __builtin_ctz(bad), j = key0 + x;
+      const uint16_t* kx = a.k + (base + j) * a.ldk + (int64_t)head * a.D;
+      const uint16_t* vx = a.v + (base + j) * a.ldv + (int64_t)head * a.D;
+      const int behind = j < a.S ? length : (j + a.W < length ? j + a.W : length);
+      float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
+      for (int64_t row = (int64_t)j * a.G; row < (int64_t)behind * a.G; row += 64) {
+        const int64_t at = row + lane;
+        const bool in = at < (int64_t)behind * a.G;
+        const int64_t t = base + at / a.G;
+        const int hq = head * a.G + (int)(at % a.G);
+        float w = 0.0f;
+        if (in) {
+          const float s = dot_row<T>(a.q + t * a.ldq + (int64_t)hq * a.D, kx, a.D);
+          w = __builtin_amdgcn_exp2f(fmaf(s, c, -a.lse_in[t * Hq + hq] * kLog2e));
+          if (which == 0) w *= dot_row<T>(a.grad_o + t * a.ldgo + (int64_t)hq * a.D, vx, a.D) - a.delta[t * Hq + hq];
+        }
+        for (uint64_t left = __ballot(in); left; left &= left - 1) {
+          const int n = __builtin_ctzll(left);
+          const int64_t tn = base + (row + n) / a.G;
+          const int64_t hn = head * a.G + (row + n) % a.G;
+          const uint16_t* from_row = which ? a.grad_o + tn * a.ldgo + hn * a.D : a.q + tn * a.ldq + hn * a.D;
+          const float wn = __shfl(w, n);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if ((int)lane + 64 * e < a.D) y[e] = fmaf(wn, one_value<T>(from_row[lane + 64 * e]), y[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e] * times, 0.0f);
+    }
+    between_lanes();
+    uint16_t* out = which ? a.grad_v : a.grad_k;
+    const int64_t ld = which ? a.ldgv : a.ldgk;
+#pragma unroll
+    for (int i = 0; i < kD / 16; ++i) {
+      const uint32_t x = (i * 64 + lane) / (kD / 8), col = (i * 64 + lane) % (kD / 8) * 8;
+      if (key0 + (int)x < length && (int)col < a.D)
+        store16(out + (base + key0 + x) * ld + (int64_t)head * a.D + col, load16(mine + place<kD>(x, col)));
+    }
+    between_lanes();
+  };
+  finish(0, dk);
+  finish(1, dv);
+}
+
+struct WindowKernels {
+  const void *fwd, *dq, *dkdv, *sinks;
+};
+template <typename T, int kD>
+WindowKernels window_of() {
+  return {(const void*)&window_fwd_kernel<T, kD>, (const void*)&window_dq_kernel<T, kD>,
+          (const void*)&window_dkdv_kernel<T, kD, false>, (const void*)&window_dkdv_kernel<T, kD, true>};
+}
+WindowKernels window_kernels(int dtype, int D) {
+  if (dtype == ENGRAM_BF16) return D <= 64 ? window_of<bf16_t, 64>() : window_of<bf16_t, 128>();
+  return D <= 64 ? window_of<_Float16, 64>() : window_of<_Float16, 128>();
+}
+
+WindowArgs window_args(const WindowCall& w) {
+  WindowArgs a{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+               nullptr, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0f, Divide((uint32_t)(w.Hq / w.Hk))};
+  a.q = w.q; a.k = w.k; a.v = w.v; a.cu = w.cu;
+  a.N = w.N; a.ldq = w.ldq; a.ldk = w.ldk; a.ldv = w.ldv;
+  a.B = (int)w.B; a.Hk = (int)w.Hk; a.G = (int)(w.Hq / w.Hk); a.D = (int)w.D;
+  a.W = (int)(w.window < w.N ? w.window : w.N);
+  a.S = (int)w.sinks;
+  a.scale = w.scale;
+  return a;
+}
+hipError_t launch_heads(const void* kernel, WindowArgs a, int64_t tiles, hipStream_t stream) {
+  a.tiles = (int)tiles;
+  void* args[] = {&a};
+  return hipLaunchKernel(kernel, dim3((unsigned)(tiles * a.Hk)), dim3(kThreads), args, 0, stream);
+}
+
+// Tokens of a piece: some thousand workgroups in all, but pieces worth a launch.
+int64_t piece_of(int64_t N, int64_t Hk) {
+  const int64_t pieces = 1024 / Hk > 1 ? 1024 / Hk : 1, piece = (N + pieces - 1) / pieces;
+  return piece < 256 ? 256 : piece;
+}
+int64_t delta_values(int64_t N, int64_t Hq) { return (N * Hq + 3) / 4 * 4; }
+
+}  // namespace
+
+size_t window_bwd_workspace(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks) {
+  int64_t values = delta_values(N, Hq);
+  if (sinks > 0 && window < N) values += (N / piece_of(N, Hk) + B) * Hk * 2 * sinks * D;
+  return (size_t)values * sizeof(float);
+}
+
+hipError_t launch_window_fwd(const WindowCall& w, hipStream_t stream) {
+  WindowArgs a = window_args(w);
+  a.out = w.o; a.ldout = w.ldo; a.lse = w.lse;
+  return launch_heads(window_kernels(w.dtype, a.D).fwd, a, a.N * a.G / kRows + a.B, stream);
+}
+
+hipError_t launch_window_bwd(const WindowCall& w, hipStream_t stream) {
+  WindowArgs a = window_args(w);
+  const WindowKernels k = window_kernels(w.dtype, a.D);
+  a.o = w.o_in; a.ldo = w.ldo; a.grad_o = w.grad_o; a.ldgo = w.ldgo; a.lse_in = w.lse_in;
+  a.out = w.grad_q; a.ldout = w.ldgq; a.grad_k = w.grad_k; a.ldgk = w.ldgk; a.grad_v = w.grad_v; a.ldgv = w.ldgv;
+  a.delta = static_cast<float*>(w.workspace);
+  a.sums = a.delta + delta_values(w.N, w.Hq);
+  a.piece = (int)piece_of(w.N, w.Hk);
+  hipError_t e = launch_heads(k.dq, a, a.N * a.G / kRows + a.B, stream);
+  if (e == hipSuccess && a.S > 0 && a.W < a.N) e = launch_heads(k.sinks, a, a.N / a.piece + a.B, stream);
+  return e == hipSuccess ? launch_heads(k.dkdv, a, a.N / kRows + a.B, stream) : e;
+}
+
+}  // namespace engram

@@ -544,6 +544,50 @@ size_t engram_window_attn_bwd_workspace_bytes(int64_t N, int64_t B, int64_t Hq, 
                                               int64_t sinks);
 
 /*
+ * One token for each row of a decode batch, over a pool of caches that hold
+ * just what can still be seen: a cache has `capacity` lines, the token at
+ * position j (behind j others of its sequence) in line j if j < sinks, else in
+ * line sinks + (j - sinks) % (capacity - sinks).  Writes each row's k and v into
+ * its line and attends over what the token sees, itself among them.
+ *   q, o [B][Hq][D], k, v [B][Hk][D]  as above with rows of the batch for tokens
+ *   cache_k, cache_v [slots_total][Hk][capacity][D]  in and out, of q's type
+ *   slots [B]      int64, in, device memory: each row's cache.  A row whose slot
+ *                  is outside 0..slots_total-1, or whose position is negative
+ *                  (padding), is skipped and its o left as it is.
+ *   positions [B]  int64, in, device memory: each row's position.  The tokens
+ *                  before it that it sees lie in the cache.  Neighbouring rows
+ *                  of the same slot with positions p, p + 1, ... are tokens of
+ *                  one sequence, in order, each seeing those before it: n of them
+ *                  need capacity >= sinks + window + n - 1, and n <= 64.
+ *   workspace      engram_window_attn_step_workspace_bytes(B, Hq, Hk, D, capacity)
+ *                  bytes, or NULL where that is 0
+ *   B 1..ENGRAM_WINDOW_STEP_ROWS_MAX; Hq, Hk, D, sinks, scale, dtype as above;
+ *   window 1..capacity - sinks; capacity 1..ENGRAM_WINDOW_CAPACITY_MAX;
+ *   slots_total 1..
+ */
+#define ENGRAM_WINDOW_STEP_ROWS_MAX 4096
+#define ENGRAM_WINDOW_CAPACITY_MAX 1048576
+engram_status engram_window_attn_step(const void *q, const void *k, const void *v, void *cache_k, void *cache_v,
+                                      const int64_t *slots, const int64_t *positions, void *o, void *workspace,
+                                      int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t slots_total,
+                                      int64_t capacity, int64_t window, int64_t sinks, int64_t ldq, int64_t ldk,
+                                      int64_t ldv, int64_t ldo, float scale, int dtype, void *stream);
+size_t engram_window_attn_step_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t capacity);
+
+/*
+ * Fill caches from prompts, for the steps that follow: sequence b of
+ * cu_seqlens, at positions from 0 on, goes into slot slots[b] (outside the pool:
+ * skipped; of sequences with the same slot the last counts).  Lines to which no
+ * token of the sequence belongs are left as they are.
+ *   k, v [N][Hk][D] in, leading dimensions ldk, ldv; cu_seqlens [B+1] as above
+ *   B 1..ENGRAM_WINDOW_STEP_ROWS_MAX; sinks < capacity; the rest as above
+ */
+engram_status engram_window_cache_fill(const void *k, const void *v, const int64_t *cu_seqlens, const int64_t *slots,
+                                       void *cache_k, void *cache_v, int64_t N, int64_t B, int64_t Hk, int64_t D,
+                                       int64_t slots_total, int64_t capacity, int64_t sinks, int64_t ldk, int64_t ldv,
+                                       int dtype, void *stream);
+
+/*
  * Gated recurrence of each channel.  For every sequence, with
  * f_t = sigmoid(gate_t):
  *   h_t = f_t h_{t-1} + (1 - f_t) u_t

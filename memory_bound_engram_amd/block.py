@@ -19,6 +19,7 @@ _P, _I64, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_flo
 NORM_ROWS_MAX, NORM_D_MAX = 2097152, 16384
 WINDOW_ROWS_MAX, WINDOW_HEADS_MAX, WINDOW_HEAD_ROWS_MAX = 4194304, 1024, 536870912
 WINDOW_SEQ_HEADS_MAX, WINDOW_D_MAX, WINDOW_SINKS_MAX = 4194304, 128, 128
+WINDOW_STEP_ROWS_MAX, WINDOW_CAPACITY_MAX = 4096, 1048576
 SCAN_ROWS_MAX, SCAN_STATES_MAX, SCAN_D_MAX, SCAN_VALUES_MAX = 16777216, 4194304, 65536, 34359738368
 SCAN_STEP_ROWS_MAX = 4096
 
@@ -29,6 +30,8 @@ def _declare(lib):
         "engram_layer_norm_bwd": [_P] * 9 + [_I64] * 6 + [_INT, _P],
         "engram_window_attn_fwd": [_P] * 6 + [_I64] * 11 + [_F, _INT, _P],
         "engram_window_attn_bwd": [_P] * 11 + [_I64] * 15 + [_F, _INT, _P],
+        "engram_window_attn_step": [_P] * 9 + [_I64] * 12 + [_F, _INT, _P],
+        "engram_window_cache_fill": [_P] * 6 + [_I64] * 9 + [_INT, _P],
         "engram_gated_scan_fwd": [_P] * 7 + [_I64] * 6 + [_INT, _P],
         "engram_gated_scan_bwd": [_P] * 11 + [_I64] * 9 + [_INT, _P],
         "engram_gated_scan_step": [_P] * 5 + [_I64] * 6 + [_INT, _P],
@@ -36,6 +39,7 @@ def _declare(lib):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = _INT
     for name, n in {"engram_layer_norm_bwd_workspace_bytes": 2, "engram_window_attn_bwd_workspace_bytes": 7,
+                    "engram_window_attn_step_workspace_bytes": 5,
                     "engram_gated_scan_fwd_workspace_bytes": 3, "engram_gated_scan_bwd_workspace_bytes": 3}.items():
         getattr(lib, name).argtypes = [_I64] * n
         getattr(lib, name).restype = ctypes.c_size_t
@@ -136,6 +140,51 @@ def engram_window_attn_bwd(grad_o, q, k, v, o, lse, cu_seqlens, grad_q, grad_k, 
            ldgo, *lds, ldo, ldgq, ldgk, ldgv, scale, _CODE[q.dtype]), stream)
 
 
+def engram_window_attn_step_workspace_bytes(B: int, Hq: int, Hk: int, D: int, capacity: int) -> int:
+    """Scratch bytes of the window attention's step (0: no workspace is needed)."""
+    return int(_eg.lib.engram_window_attn_step_workspace_bytes(B, Hq, Hk, D, capacity))
+
+
+def engram_window_attn_step(q, k, v, cache_k, cache_v, slots, positions, o, workspace, window, sinks=0, scale=1.0,
+                            stream=None) -> None:
+    """Enqueue one token for each row of a decode batch: q, o [B,Hq,D], k, v
+    [B,Hk,D] bf16 or fp16, rows may be apart; cache_k, cache_v
+    [slots,Hk,capacity,D], a pool of caches that take k and v, capacity at least
+    sinks + window; slots, positions [B] int64 (on the GPU), each row's cache
+    (outside the pool: the row is skipped) and its token's place in the sequence
+    (negative: skipped).  Neighbouring rows of one slot at positions one behind
+    the other are one sequence's tokens in order."""
+    a = _Args()
+    (B, Hq, Hk, D), dt, ptrs, lds = _window_inputs(a, q, k, v)
+    total, _, capacity, _ = _shape("cache_k", cache_k, 4)
+    pck = a.dense("cache_k", cache_k, dt, (total, Hk, capacity, D))
+    pcv = a.dense("cache_v", cache_v, dt, (total, Hk, capacity, D))
+    pslots, pp = a.dense("slots", slots, _INTS, (B,)), a.dense("positions", positions, _INTS, (B,))
+    po, ldo = a.rows("o", o, dt, (B, Hq, D), Hq * D)
+    ws = a.workspace(workspace, _eg.lib.engram_window_attn_step_workspace_bytes(B, Hq, Hk, D, capacity))
+    a.call(_eg.lib.engram_window_attn_step, (*ptrs, pck, pcv, pslots, pp, po, ws, B, Hq, Hk, D, total, capacity, window,
+           sinks, *lds, ldo, scale, _CODE[q.dtype]), stream)
+
+
+def engram_window_cache_fill(k, v, cu_seqlens, slots, cache_k, cache_v, sinks=0, stream=None) -> None:
+    """Enqueue the filling of caches for the steps behind a prompt: sequence b of
+    k, v [N,Hk,D] (tokens may be apart), cut by cu_seqlens [B+1] int64, goes into
+    cache slots[b] of cache_k, cache_v [slots,Hk,capacity,D] at positions from 0
+    on, as far as its tokens can still be seen."""
+    a = _Args()
+    N, Hk, D = _shape("k", k, 3)
+    dt = (k.dtype,)
+    pk, ldk = a.rows("k", k, _HALVES, (N, Hk, D), Hk * D)
+    pv, ldv = a.rows("v", v, dt, (N, Hk, D), Hk * D)
+    B = _shape("cu_seqlens", cu_seqlens, 1)[0] - 1
+    pcu, pslots = a.dense("cu_seqlens", cu_seqlens, _INTS, (B + 1,)), a.dense("slots", slots, _INTS, (B,))
+    total, _, capacity, _ = _shape("cache_k", cache_k, 4)
+    pck = a.dense("cache_k", cache_k, dt, (total, Hk, capacity, D))
+    pcv = a.dense("cache_v", cache_v, dt, (total, Hk, capacity, D))
+    a.call(_eg.lib.engram_window_cache_fill, (pk, pv, pcu, pslots, pck, pcv, N, B, Hk, D, total, capacity, sinks, ldk, ldv,
+           _CODE[k.dtype]), stream)
+
+
 def engram_gated_scan_fwd_workspace_bytes(N: int, B: int, D: int) -> int:
     """Scratch bytes of the gated recurrence's forward."""
     return int(_eg.lib.engram_gated_scan_fwd_workspace_bytes(N, B, D))
@@ -205,5 +254,6 @@ def engram_gated_scan_step(gate, u, state, slots, h, stream=None) -> None:
 
 __all__ = ["engram_layer_norm_fwd", "engram_layer_norm_bwd", "engram_layer_norm_bwd_workspace_bytes",
            "engram_window_attn_fwd", "engram_window_attn_bwd", "engram_window_attn_bwd_workspace_bytes",
+           "engram_window_attn_step", "engram_window_attn_step_workspace_bytes", "engram_window_cache_fill",
            "engram_gated_scan_fwd", "engram_gated_scan_bwd", "engram_gated_scan_step",
            "engram_gated_scan_fwd_workspace_bytes", "engram_gated_scan_bwd_workspace_bytes"]

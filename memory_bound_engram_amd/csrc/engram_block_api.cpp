@@ -38,6 +38,10 @@ bool window_sizes_ok(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, in
          N <= ENGRAM_WINDOW_HEAD_ROWS_MAX / Hq && in(B, 1, ENGRAM_WINDOW_SEQ_HEADS_MAX / Hk) &&
          in(D, 8, ENGRAM_WINDOW_D_MAX) && window >= 1 && in(sinks, 0, ENGRAM_WINDOW_SINKS_MAX);
 }
+bool step_sizes_ok(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t capacity) {
+  return window_sizes_ok(1, 1, Hq, Hk, D, 1, 0) && in(B, 1, ENGRAM_WINDOW_STEP_ROWS_MAX) &&
+         in(capacity, 1, ENGRAM_WINDOW_CAPACITY_MAX);
+}
 bool scale_ok(float scale) { return scale > 0.0f && isfinite(scale); }
 
 Rows heads(const void* p, int64_t rows, int64_t ld, int64_t H, int64_t D) { return Rows{p, rows, ld * 2, H * D * 2}; }
@@ -169,6 +173,68 @@ engram_status engram_window_attn_bwd(const void* grad_o, const void* q, const vo
   w.ldgo = ldgo; w.ldq = ldq; w.ldk = ldk; w.ldv = ldv; w.ldo = ldo; w.ldgq = ldgq; w.ldgk = ldgk; w.ldgv = ldgv;
   w.scale = scale; w.dtype = dtype;
   return launched(engram::launch_window_bwd(w, (hipStream_t)stream));
+}
+
+size_t engram_window_attn_step_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t capacity) {
+  if (!step_sizes_ok(B, Hq, Hk, D, capacity) || D % 8) return 0;
+  return engram::window_step_workspace(B, Hq, Hk, D, capacity);
+}
+
+engram_status engram_window_attn_step(const void* q, const void* k, const void* v, void* cache_k, void* cache_v,
+                                      const int64_t* slots, const int64_t* positions, void* o, void* workspace, int64_t B,
+                                      int64_t Hq, int64_t Hk, int64_t D, int64_t slots_total, int64_t capacity,
+                                      int64_t window, int64_t sinks, int64_t ldq, int64_t ldk, int64_t ldv, int64_t ldo,
+                                      float scale, int dtype, void* stream) {
+  if (!q || !k || !v || !cache_k || !cache_v || !slots || !positions || !o) return ENGRAM_ERR_NULL;
+  if (!half_kind_ok(dtype)) return ENGRAM_ERR_KIND;
+  if (!step_sizes_ok(B, Hq, Hk, D, capacity) || !in(sinks, 0, ENGRAM_WINDOW_SINKS_MAX) || !in(window, 1, capacity - sinks) ||
+      !in(slots_total, 1, INT64_MAX / (Hk * capacity * D * 2)) || !ld_in_range(ldq, Hq * D) || !ld_in_range(ldk, Hk * D) ||
+      !ld_in_range(ldv, Hk * D) || !ld_in_range(ldo, Hq * D) || !scale_ok(scale))
+    return ENGRAM_ERR_N_RANGE;
+  if ((D | ldq | ldk | ldv | ldo) % 8 || !aligned8(slots) || !aligned8(positions)) return ENGRAM_ERR_ALIGN;
+  const size_t ws = engram::window_step_workspace(B, Hq, Hk, D, capacity);
+  if (ws && !workspace) return ENGRAM_ERR_NULL;
+  const void* ptrs[] = {q, k, v, cache_k, cache_v, o, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ENGRAM_ERR_ALIGN;
+  const int64_t pool = slots_total * Hk * capacity * D * 2;
+  const Rows ins[] = {heads(q, B, ldq, Hq, D), heads(k, B, ldk, Hk, D), heads(v, B, ldv, Hk, D), flat(slots, B * 8),
+                      flat(positions, B * 8)};
+  const Rows outs[] = {flat(cache_k, pool), flat(cache_v, pool), heads(o, B, ldo, Hq, D), flat(workspace, (int64_t)ws)};
+  if (any_overlap(ins, 5, outs, 4)) return ENGRAM_ERR_OVERLAP;
+  engram::WindowStepCall w{};
+  w.q = static_cast<const uint16_t*>(q); w.k = static_cast<const uint16_t*>(k); w.v = static_cast<const uint16_t*>(v);
+  w.cache_k = static_cast<uint16_t*>(cache_k); w.cache_v = static_cast<uint16_t*>(cache_v);
+  w.slots = slots; w.positions = positions; w.o = static_cast<uint16_t*>(o); w.workspace = workspace;
+  w.B = B; w.Hq = Hq; w.Hk = Hk; w.D = D; w.n_slots = slots_total; w.capacity = capacity; w.window = window; w.sinks = sinks;
+  w.ldq = ldq; w.ldk = ldk; w.ldv = ldv; w.ldo = ldo; w.scale = scale; w.dtype = dtype;
+  return launched(engram::launch_window_step(w, (hipStream_t)stream));
+}
+
+engram_status engram_window_cache_fill(const void* k, const void* v, const int64_t* cu_seqlens, const int64_t* slots,
+                                       void* cache_k, void* cache_v, int64_t N, int64_t B, int64_t Hk, int64_t D,
+                                       int64_t slots_total, int64_t capacity, int64_t sinks, int64_t ldk, int64_t ldv,
+                                       int dtype, void* stream) {
+  if (!k || !v || !cu_seqlens || !slots || !cache_k || !cache_v) return ENGRAM_ERR_NULL;
+  if (!half_kind_ok(dtype)) return ENGRAM_ERR_KIND;
+  if (!in(N, 1, ENGRAM_WINDOW_ROWS_MAX) || !step_sizes_ok(B, Hk, Hk, D, capacity) || !in(sinks, 0, ENGRAM_WINDOW_SINKS_MAX) ||
+      sinks >= capacity || !in(slots_total, 1, INT64_MAX / (Hk * capacity * D * 2)) || !ld_in_range(ldk, Hk * D) ||
+      !ld_in_range(ldv, Hk * D))
+    return ENGRAM_ERR_N_RANGE;
+  if ((D | ldk | ldv) % 8 || !aligned8(cu_seqlens) || !aligned8(slots)) return ENGRAM_ERR_ALIGN;
+  const void* ptrs[] = {k, v, cache_k, cache_v};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return ENGRAM_ERR_ALIGN;
+  const int64_t pool = slots_total * Hk * capacity * D * 2;
+  const Rows ins[] = {heads(k, N, ldk, Hk, D), heads(v, N, ldv, Hk, D), flat(cu_seqlens, (B + 1) * 8), flat(slots, B * 8)};
+  const Rows outs[] = {flat(cache_k, pool), flat(cache_v, pool)};
+  if (any_overlap(ins, 4, outs, 2)) return ENGRAM_ERR_OVERLAP;
+  engram::WindowStepCall w{};
+  w.k = static_cast<const uint16_t*>(k); w.v = static_cast<const uint16_t*>(v); w.cu = cu_seqlens; w.slots = slots;
+  w.cache_k = static_cast<uint16_t*>(cache_k); w.cache_v = static_cast<uint16_t*>(cache_v);
+  w.N = N; w.B = B; w.Hk = Hk; w.D = D; w.n_slots = slots_total; w.capacity = capacity; w.sinks = sinks;
+  w.ldk = ldk; w.ldv = ldv; w.dtype = dtype;
+  return launched(engram::launch_window_fill(w, (hipStream_t)stream));
 }
 
 size_t engram_gated_scan_fwd_workspace_bytes(int64_t N, int64_t B, int64_t D) { return scan_workspace_bytes(N, B, D); }

@@ -153,6 +153,21 @@ size_t window_bwd_workspace(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_
 hipError_t launch_window_fwd(const WindowCall& w, hipStream_t stream);
 hipError_t launch_window_bwd(const WindowCall& w, hipStream_t stream);
 
+// Window attention of single tokens over a pool of caches, and their filling.
+struct WindowStepCall {
+  const uint16_t *q, *k, *v;
+  uint16_t *cache_k, *cache_v, *o;
+  const int64_t *slots, *positions, *cu;
+  void* workspace;
+  int64_t N, B, Hq, Hk, D, n_slots, capacity, window, sinks;
+  int64_t ldq, ldk, ldv, ldo;
+  float scale;
+  int dtype;
+};
+size_t window_step_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t capacity);
+hipError_t launch_window_step(const WindowStepCall& w, hipStream_t stream);
+hipError_t launch_window_fill(const WindowStepCall& w, hipStream_t stream);
+
 // Gated scan: one call's arguments.
 struct ScanCall {
   const void *gate, *u, *h_in, *grad_h;

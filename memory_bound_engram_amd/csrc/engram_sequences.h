@@ -22,6 +22,36 @@ struct Sequences {
   }
   __device__ __forceinline__ int64_t start(int i) const { return bound(i); }
   __device__ __forceinline__ int64_t end(int i) const { return bound(i + 1); }
+  // The last sequence whose key(its start, its number) is at most `most`, for keys
+  // that rise with the number (0 if none is), and its bounds: sixty-four starts at
+  // a time, one load for up to 63 sequences.
+  template <typename F>
+  __device__ __forceinline__ int last_at_most(int64_t most, F key, int64_t* start, int64_t* end) const {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = B;
+    for (;;) {
+      const int step = (n + 63) / 64, i = lo + lane * step;
+      const int64_t raw = cu[i <= B ? i : B], at = raw < 0 ? 0 : (raw > N ? N : raw);
+      const uint64_t in = __ballot(lane * step < n && key(at, i) <= most);
+      const int last = in ? 63 - __builtin_clzll(in) : 0;
+      if (step == 1) {
+        if (n < 64) {
+          *start = from_lane(at, last);
+          *end = from_lane(at, last + 1);
+        } else {
+          *start = bound(lo + last);
+          *end = bound(lo + last + 1);
+        }
+        return lo + last;
+      }
+      n = n - last * step < step ? n - last * step : step;
+      lo += last * step;
+    }
+  }
+  static __device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+  }
   // the first sequence that ends behind a token (B if none does)
   __device__ int first_behind(int64_t token) const {
     int lo = 0, hi = B;

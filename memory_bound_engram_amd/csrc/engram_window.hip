@@ -38,6 +38,8 @@
 #include "engram_sequences.h"
 #include "engram_window_tiles.h"
 
+#include <type_traits>
+
 namespace engram {
 namespace {
 
@@ -69,23 +71,48 @@ __device__ __forceinline__ int neighbours(int block, int blocks) {
 }
 
 // Which sequence a workgroup is in, and which tile of it: sequence b has the
-// numbers from first_tile(b) on, as many as its tiles of `unit` rows at least
-// (`per` rows a token).
-__device__ __forceinline__ int64_t first_tile(const Sequences& seqs, int b, int64_t per, int64_t unit) {
-  return seqs.start(b) * per / unit + b;
+// numbers from first_tile(start, b) on, as many as its tiles of `unit` rows at
+// least (`per` rows a token).
+__device__ __forceinline__ int64_t first_tile(int64_t start, int b, uint32_t per, uint32_t unit) {
+  return start * per / unit + b;
 }
-__device__ __forceinline__ int sequence_of(const Sequences& seqs, int64_t id, int64_t per, int64_t unit, int64_t* tile) {
-  int lo = 0, hi = seqs.B - 1;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (first_tile(seqs, mid, per, unit) <= id) lo = mid;
-    else hi = mid - 1;
+struct Sequence {
+  int b;
+  int64_t start, length, tile;  // tile: negative before the first sequence
+  __device__ __forceinline__ Sequence(const WindowArgs& a, int64_t id, uint32_t per, uint32_t unit) {
+    const Sequences seqs{a.cu, a.N, a.B};
+    int64_t end;
+    b = seqs.last_at_most(id, [&](int64_t at, int i) { return first_tile(at, i, per, unit); }, &start, &end);
+    length = end - start;
+    tile = id - first_tile(start, b, per, unit);
   }
-  *tile = id - first_tile(seqs, lo, per, unit);  // negative before the first sequence
-  return lo;
-}
+};
 
 __device__ __forceinline__ bool sees(int t, int j, int W, int S) { return j <= t && (j > t - W || j < S); }
+
+// Of sixteen scores of a row at t, for keys start + 8 (e / 4) + e % 4 below end,
+// those of keys that it does not see become `other`.
+__device__ __forceinline__ void keep_seen(f32x16& s, int t, int start, int end, int W, int S, float other) {
+  asm volatile("" : "+v"(start));  // or what follows moves in front of the branch around it
+  const int from = t - W + 1 - start, below = (t < end ? t + 1 : end) - start;
+  if (__any(start < S)) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int j = 8 * (e / 4) + e % 4;
+      s[e] = j < below && (j >= from || j < S - start) ? s[e] : other;
+    }
+  } else {
+    const uint32_t span = below > from ? (uint32_t)(below - from) : 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = (uint32_t)(8 * (e / 4) + e % 4 - from) < span ? s[e] : other;
+  }
+}
+// The softmax's terms may exceed 1: the sum and the outputs are scaled anew only
+// where the maximum grows by more than 2^kSlack, which after the first keys hardly
+// happens (where it grows at all, they would be in most of the halves of a tile, as one
+// of a wave's 32 rows always finds a larger score).  Terms keep their digits, and
+// in fp16 are far from its largest value.
+constexpr float kSlack = 8.0f;
 
 // The keys of a run of tokens, as tiles of kKeys: the sinks before the window, then the window.
 struct KeyTiles {
@@ -118,17 +145,16 @@ struct RowTile {
 
 __device__ __forceinline__ bool row_tile(const WindowArgs& a, RowTile* r) {
   const int at = neighbours(blockIdx.x, gridDim.x);
-  const Sequences seqs{a.cu, a.N, a.B};
-  int64_t tile;
-  const int b = sequence_of(seqs, at % a.tiles, a.G, kRows, &tile);
   r->head = at / a.tiles;
-  r->base = seqs.start(b);
-  const int64_t length = seqs.end(b) - r->base, first = tile * kRows, all = length * a.G;
-  if (tile < 0 || length <= 0 || first >= all) return false;
-  r->length = (int)length;
-  r->t0 = (int)(first / a.G);
-  r->x0 = (uint32_t)(first % a.G);
-  r->rows = (int)(all - first < kRows ? all - first : kRows);
+  const Sequence s(a, at % a.tiles, a.G, kRows);
+  const int64_t all = s.length * a.G;
+  if (s.tile < 0 || s.length <= 0 || s.tile * kRows >= all) return false;
+  const uint32_t first = (uint32_t)s.tile * kRows;  // N * Hq is below 2^30
+  r->base = s.start;
+  r->length = (int)s.length;
+  r->t0 = (int)(first / (uint32_t)a.G);
+  r->x0 = first - (uint32_t)r->t0 * (uint32_t)a.G;
+  r->rows = all - first < kRows ? (int)(all - first) : kRows;
   return true;
 }
 
@@ -202,19 +228,21 @@ __device__ __forceinline__ void store_rows(const uint16_t* mine, const RowTile& 
   }
 }
 
+// Whether they are all finite (a sum that is not finite has a term that is not).
 template <int kD>
-__device__ __forceinline__ bool finite_rows(const f32x16 (&v)[kD / 32], float times) {
+__device__ __forceinline__ bool finite_rows(const f32x16 (&v)[kD / 32]) {
   float s = 0.0f;
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s = fmaf(v[dt][i] * times, 0.0f, s);
-  return s == 0.0f;
+    for (int i = 0; i < 16; ++i) s += v[dt][i] * 0x1p-8f;
+  return fabsf(s) < INFINITY;
 }
 
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kKeys * kD];  // [turn][keys, values]
+  // keys of two tiles; values of three, since a tile's are read out half a tile after its keys
+  __shared__ __attribute__((aligned(16))) uint16_t lds[5][kKeys * kD];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5;
   RowTile r;
@@ -228,18 +256,9 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   const int first = r.t0, last = r.t0 + (int)r.token(r.rows - 1, a, &g_last);
   const int head = r.head * a.G + (int)g;
   u32x4 q[kD / 16];
-  load_row<kD>(q, a.q + (r.base + (there ? t : 0)) * a.ldq + (int64_t)head * a.D, there, a.D, h);
-
   const KeyTiles keys(first, last, a.W, a.S);
   const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
-  const auto fetch = [&](int i) {
-    const int start = keys.start(i), n = keys.end(i) - start;
-    const int64_t token = r.base + start;
-    pieces.fetch(lds[i & 1][0], a.k + token * a.ldk + (int64_t)r.head * a.D, a.D, wave,
-                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldk * 2) : kBeyond; });
-    pieces.fetch(lds[i & 1][1], a.v + token * a.ldv + (int64_t)r.head * a.D, a.D, wave,
-                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldv * 2) : kBeyond; });
-  };
+  const uint32_t k_at = pieces.offset(a.ldk, a.D), v_at = pieces.offset(a.ldv, a.D);
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
   const float c = a.scale * kLog2e;
@@ -247,64 +266,110 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) o[dt] = f32x16{};
   float m = -INFINITY, sum = 0.0f;
-  fetch(0);
-  for (int i = 0; i < keys.n; ++i) {
-    meet();
-    if (i + 1 < keys.n) fetch(i + 1);
-    const uint16_t *tk = lds[i & 1][0], *tv = lds[i & 1][1];
-    f32x16 s[2] = {f32x16{}, f32x16{}};
+  // (behind the last tile: zeros)
+  const auto fetch_tile = [&](int i) {
+    const int start = keys.start(i), n = keys.end(i) - start;
+    const int64_t token = r.base + start, col = (int64_t)r.head * a.D;
+    pieces.fetch(lds[i & 1], a.k + token * a.ldk + col, a.ldk, n, a.D, k_at, wave);
+    pieces.fetch(lds[2 + i % 3], a.v + token * a.ldv + col, a.ldv, n, a.D, v_at, wave);
+  };
+  // Operands on their way from LDS: of the next half's scores, and of this half's values.
+  constexpr int kX = kD / 16;  // products of a half's scores, and of its values
+  u32x4 kf[kX], vf[kX];
+  const auto read_keys = [&](lds_bytes tk, int u, int x) { kf[x] = rows(tk, 32 * u, x); };
+  const auto largest = [&](const f32x16& s) {
+    float top = s[0];
 #pragma unroll
-    for (int kk = 0; kk < kD / 16; ++kk)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) s[u] = product<T>(rows(tk, 32 * u, kk), q[kk], s[u]);
-    const int start = keys.start(i), end = keys.end(i);
-    // some row of the tile does not see some key
-    if (start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= a.S)) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = start + 32 * u + 8 * (e / 4) + 4 * (int)h + e % 4;
-          s[u][e] = j < end && sees(t, j, a.W, a.S) ? s[u][e] : -INFINITY;
-        }
+    for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+    return top;
+  };
+  // what rows do not see goes; the maximum, and what there is in its terms
+  const auto settle = [&](f32x16& s, float top, int i, int u) {
+    const int start = keys.start(i) + 32 * u, end = keys.end(i);
+    if (start + 32 > end || start + 31 > first || !(start > last - a.W || start + 32 <= a.S)) {
+      keep_seen(s, t, start + 4 * (int)h, end, a.W, a.S, -INFINITY);
+      top = largest(s);
     }
-    float top = s[0][0];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
-    top = fmaxf(m, column_max(top));
-    if (__any(top > m)) {
+    if (__any((top - m) * c > kSlack)) {
+      top = fmaxf(m, column_max(top));
       const float keep = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * c);
       sum *= keep;
 #pragma unroll
       for (int dt = 0; dt < kD / 32; ++dt) o[dt] *= keep;
       m = top;
     }
+  };
+  // Half u of tile i, whose scores are in s: first the scores of the next half (if
+  // there is one), beside which the weights are made, then the weights times the
+  // values, beside which the next scores' maximum is found.  Each product is sent
+  // with what goes on beside it, in this order: left to itself the compiler reads
+  // each operand just before its product and makes the weights in one go.
+  const auto step = [&](f32x16& s, f32x16& next, int i, auto half, auto more) {
+    constexpr int u = decltype(half)::value, kEach = 16 / kX;
+    constexpr bool kNext = decltype(more)::value;
+    const lds_bytes tv = opaque(lds_of(lds[2 + i % 3])), tk = opaque(lds_of(lds[(i + 1) & 1]));
     const float less = m == -INFINITY ? 0.0f : -m * c;
+    u32x4 p[2];
+    next = f32x16{};
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int x = 0; x < kX; ++x) {
+      if constexpr (kNext) next = product<T>(kf[x], q[x], next);
+      vf[x] = columns(tv, 32 * u + 16 * (x / (kD / 32)), x % (kD / 32));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[u][e] = __builtin_amdgcn_exp2f(fmaf(s[u][e], c, less));
-        sum += s[u][e];
+      for (int e = x * kEach; e < (x + 1) * kEach; ++e) {
+        s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, less));
+        sum += s[e];
       }
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const u32x4 p = operand<T>(s[w / 2], w % 2);
-#pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt) o[dt] = product<T>(columns(tv, 16 * w, dt), p, o[dt]);
+      if ((x + 1) * kEach % 8 == 0) p[(x + 1) * kEach / 8 - 1] = operand<T>(s, (x + 1) * kEach / 8 - 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (u == 0) {
+      meet();  // the next tile is there, and this one's keys are read out, the last one's values too
+      fetch_tile(i + 2);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      __builtin_amdgcn_sched_barrier(0);
+      o[x % (kD / 32)] = product<T>(vf[x], p[x / (kD / 32)], o[x % (kD / 32)]);
+      // (behind the last tile this reads what lies there, for no one)
+      if constexpr (kNext) read_keys(tk, u, x);
+      if constexpr (kNext)
+        if (x >= 2)
+#pragma unroll
+          for (int e = (x - 2) * 16 / (kX - 2); e < (x - 1) * 16 / (kX - 2); ++e) top = fmaxf(top, next[e]);
+    }
+    asm volatile("" : "+v"(sum), "+v"(top));  // or they move behind the branches, away from the products
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kNext) settle(next, top, i + u, 1 - u);
+  };
+  constexpr auto first_half = std::integral_constant<int, 0>{};
+  constexpr auto second_half = std::integral_constant<int, 1>{};
+  load_row<kD>(q, a.q + (r.base + (there ? t : 0)) * a.ldq + (int64_t)head * a.D, there, a.D, h);
+  fetch_tile(0);
+  fetch_tile(1);
+  meet();
+  f32x16 s0 = f32x16{}, s1;
+#pragma unroll
+  for (int x = 0; x < kX; ++x) s0 = product<T>(rows(lds_of(lds[0]), 0, x), q[x], s0);
+#pragma unroll
+  for (int x = 0; x < kX; ++x) read_keys(lds_of(lds[0]), 1, x);
+  settle(s0, largest(s0), 0, 0);
+  for (int i = 0; i < keys.n; ++i) {
+    step(s0, s1, i, first_half, std::true_type{});
+    if (i + 1 < keys.n) step(s1, s0, i, second_half, std::true_type{});
   }
+  step(s1, s0, keys.n - 1, second_half, std::false_type{});
   sum = column_sum(sum);
   const float inverse = 1.0f / sum;
   if (a.lse && there && h == 0) a.lse[(r.base + t) * (int64_t)(a.Hk * a.G) + head] = fmaf(m, c, __log2f(sum)) * kLn2;
 
   __syncthreads();  // the tiles are read out
-  uint16_t* mine = lds[0][0] + wave * 32 * kD;
+  uint16_t* mine = lds[0] + wave * 32 * kD;
   put_rows<T, kD>(mine, o, inverse, lane);
   // rows that are not finite though their weights are, by the definition
-  const uint64_t redo = __ballot(there && !finite_rows<kD>(o, inverse) && fabsf(m) < INFINITY && sum < INFINITY);
+  const uint64_t redo = __ballot(there && !finite_rows<kD>(o) && fabsf(m) < INFINITY && sum < INFINITY);
   between_lanes();
   for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
     const int x = __builtin_ctz(bad);
@@ -365,13 +430,12 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
 
   const KeyTiles keys(first, last, a.W, a.S);
   const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
+  const uint32_t k_at = pieces.offset(a.ldk, a.D), v_at = pieces.offset(a.ldv, a.D);
   const auto fetch = [&](int i) {
     const int start = keys.start(i), n = keys.end(i) - start;
-    const int64_t from = r.base + start;
-    pieces.fetch(lds[i & 1][0], a.k + from * a.ldk + (int64_t)r.head * a.D, a.D, wave,
-                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldk * 2) : kBeyond; });
-    pieces.fetch(lds[i & 1][1], a.v + from * a.ldv + (int64_t)r.head * a.D, a.D, wave,
-                 [&](uint32_t row) { return (int)row < n ? row * (uint32_t)(a.ldv * 2) : kBeyond; });
+    const int64_t token = r.base + start, col = (int64_t)r.head * a.D;
+    pieces.fetch(lds[i & 1][0], a.k + token * a.ldk + col, a.ldk, n, a.D, k_at, wave);
+    pieces.fetch(lds[i & 1][1], a.v + token * a.ldv + col, a.ldv, n, a.D, v_at, wave);
   };
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
@@ -383,7 +447,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   for (int i = 0; i < keys.n; ++i) {
     meet();
     if (i + 1 < keys.n) fetch(i + 1);
-    const uint16_t *tk = lds[i & 1][0], *tv = lds[i & 1][1];
+    const lds_bytes tk = lds_of(lds[i & 1][0]), tv = lds_of(lds[i & 1][1]);
     const int start = keys.start(i), end = keys.end(i);
     const bool some = start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= a.S);
 #pragma unroll
@@ -395,13 +459,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
       for (int kk = 0; kk < kD / 16; ++kk) d = product<T>(rows(tv, 32 * u, kk), go[kk], d);
 #pragma unroll
       for (int e = 0; e < 16; ++e) d[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse)) * (d[e] - delta);
-      if (some) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = start + 32 * u + 8 * (e / 4) + 4 * (int)h + e % 4;
-          d[e] = j < end && sees(t, j, a.W, a.S) ? d[e] : 0.0f;
-        }
-      }
+      if (some) keep_seen(d, t, start + 32 * u + 4 * (int)h, end, a.W, a.S, 0.0f);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const u32x4 p = operand<T>(d, w);
@@ -414,7 +472,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   __syncthreads();  // the tiles are read out
   uint16_t* mine = lds[0][0] + wave * 32 * kD;
   put_rows<T, kD>(mine, dq, a.scale, lane);
-  const uint64_t redo = __ballot(there && !finite_rows<kD>(dq, a.scale) && fabsf(lse) < INFINITY && fabsf(delta) < INFINITY);
+  const uint64_t redo = __ballot(there && !finite_rows<kD>(dq) && fabsf(lse) < INFINITY && fabsf(delta) < INFINITY);
   between_lanes();
   for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
     const int x = __builtin_ctz(bad);
@@ -465,12 +523,10 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5;
   const int at = neighbours(blockIdx.x, gridDim.x), id = at % a.tiles, head = at / a.tiles;
-  const Sequences seqs{a.cu, a.N, a.B};
-  int64_t tile;
-  const int b = sequence_of(seqs, id, 1, kSinks ? a.piece : kRows, &tile);
-  const int64_t base = seqs.start(b);
-  const int length = (int)(seqs.end(b) - base);
-  const int64_t unit = kSinks ? a.piece : kRows;
+  const uint32_t unit = kSinks ? (uint32_t)a.piece : (uint32_t)kRows;
+  const Sequence seq(a, id, 1, unit);
+  const int64_t base = seq.start, tile = seq.tile;
+  const int length = (int)seq.length;
   if (tile < 0 || length <= 0 || tile * unit >= length) return;
   const int k0 = kSinks ? 0 : (int)tile * kRows;
   // the rows' tokens
@@ -509,8 +565,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
       uint32_t t, g;
       return row_at(row, &t, &g) ? t * (uint32_t)(ld * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
     };
-    pieces.fetch(lds[i & 1][0], a.q + first * a.ldq + heads, a.D, wave, [&](uint32_t row) { return offset(row, a.ldq); });
-    pieces.fetch(lds[i & 1][1], a.grad_o + first * a.ldgo + heads, a.D, wave,
+    pieces.gather(lds[i & 1][0], a.q + first * a.ldq + heads, a.D, wave, [&](uint32_t row) { return offset(row, a.ldq); });
+    pieces.gather(lds[i & 1][1], a.grad_o + first * a.ldgo + heads, a.D, wave,
                  [&](uint32_t row) { return offset(row, a.ldgo); });
     if (wave == 0) {
       uint32_t t, g;
@@ -541,7 +597,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
     meet();
     if (i + 1 < n) fetch(i + 1);
     if (!active) continue;
-    const uint16_t *tq = lds[i & 1][0], *tg = lds[i & 1][1];
+    const lds_bytes tq = lds_of(lds[i & 1][0]), tg = lds_of(lds[i & 1][1]);
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
       const int ta = tokens[i & 1][32 * u], tb = tokens[i & 1][32 * u + 31];  // the rows' first and last token
@@ -601,7 +657,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
     return;
   }
   if (key < a.S && there && length > a.W) {
-    const int64_t mine = first_tile(seqs, b, 1, a.piece);
+    const int64_t mine = first_tile(base, seq.b, 1, (uint32_t)a.piece);
     for (int p = a.W / a.piece; p <= (length - 1) / a.piece; ++p) {
       const float *from_k = piece_sums(a, mine + p, head, 0) + (int64_t)key * a.D;
       const float *from_v = piece_sums(a, mine + p, head, 1) + (int64_t)key * a.D;
@@ -626,7 +682,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
   const auto finish = [&](const int which, const f32x16(&sum)[kD / 32]) {
     const float times = which ? 1.0f : a.scale;
     put_rows<T, kD>(mine, sum, times, lane);
-    const uint64_t redo = __ballot(there && !finite_rows<kD>(sum, times));
+    const uint64_t redo = __ballot(there && !finite_rows<kD>(sum));
     between_lanes();
     for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
       const int x = __builtin_ctz(bad), j = key0 + x;

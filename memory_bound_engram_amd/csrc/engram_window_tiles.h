@@ -73,16 +73,27 @@ __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t col) {
   return row * kD + ((col >> 3) ^ turn<kD>(row)) * 8 + (col & 7);
 }
 
+// A tile's place as LDS sees it.
+typedef __attribute__((address_space(3))) const char* lds_bytes;
+__device__ __forceinline__ lds_bytes lds_of(const uint16_t* tile) { return (lds_bytes)(lds_ptr)tile; }
+// The same in a scalar register, as a value the compiler knows nothing of: or it
+// keeps every address that depends on it as a variable of the loop.
+__device__ __forceinline__ lds_bytes opaque(lds_bytes tile) {
+  uint32_t at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)tile);
+  asm volatile("" : "+s"(at));
+  return (lds_bytes)(uintptr_t)at;
+}
+
 // An operand whose rows are rows of the tile, row0 + l % 32 (row0 a multiple of
 // 32), values 16 kk + 8 h on.
 template <int kD>
 struct RowReader {
-  uint32_t at;   // of row l % 32
-  uint32_t swap;
+  uint32_t at, swap;  // of row l % 32, in bytes
   __device__ __forceinline__ explicit RowReader(uint32_t lane)
-      : at((lane & 31) * kD), swap(turn<kD>(lane & 31) ^ (lane >> 5)) {}
-  __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int row0, int kk) const {
-    return load16(tile + row0 * kD + at + ((2 * kk) ^ swap) * 8);
+      : at((lane & 31) * kD * 2), swap((turn<kD>(lane & 31) ^ (lane >> 5)) * 16) {}
+  __device__ __forceinline__ u32x4 operator()(lds_bytes tile, int row0, int kk) const {
+    typedef __attribute__((address_space(3))) const u32x4* p;
+    return *(p)(tile + (at + ((32 * kk) ^ swap)) + row0 * kD * 2);
   }
 };
 
@@ -92,17 +103,17 @@ struct RowReader {
 // group name four rows of sixteen values and get a column of four each.
 template <int kD>
 struct ColumnReader {
-  uint32_t at[2][kD / 32];  // of the rows' first eight and the second
+  uint32_t at[2][kD / 32];  // of the rows' first eight and the second, in bytes
   __device__ __forceinline__ explicit ColumnReader(uint32_t lane) {
     const uint32_t l = lane % 16, row = 4 * (lane >> 5) + l / 4, col = 16 * (lane >> 4 & 1) + 4 * (l % 4);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt) at[i][dt] = place<kD>(row + 8 * i, col + 32 * dt);
+      for (int dt = 0; dt < kD / 32; ++dt) at[i][dt] = place<kD>(row + 8 * i, col + 32 * dt) * 2;
   }
-  __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int row0, int dt) const {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + row0 * kD + at[0][dt]));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + row0 * kD + at[1][dt]));
+  __device__ __forceinline__ u32x4 operator()(lds_bytes tile, int row0, int dt) const {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at[0][dt] + row0 * kD * 2));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at[1][dt] + row0 * kD * 2));
     const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
     return u32x4{a[0], a[1], b[0], b[1]};
   }
@@ -118,16 +129,35 @@ struct Pieces {
   uint32_t row, col;  // of the first; the others' column is the same
   __device__ __forceinline__ explicit Pieces(uint32_t thread)
       : row(thread / (kD / 8)), col(((thread % (kD / 8)) ^ turn<kD>(thread / (kD / 8))) * 8) {}
-  // `at(row)`: bytes from src to a row's values, or kBeyond; the wave's place in the tile
-  // comes from its number.
+  // The place of the first piece, in bytes from a tile's first row, where rows are
+  // ld values apart.
+  __device__ __forceinline__ uint32_t offset(int64_t ld, int D) const {
+    return col < (uint32_t)D ? row * (uint32_t)(ld * 2) + col * 2 : kBeyond;
+  }
+  // n rows (or fewer: zeros; the memory's bound sees to it) from src on, ld apart;
+  // `at`: the above.  No vector instruction but the loads.
+  __device__ __forceinline__ void fetch(const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,
+                                        uint32_t wave) const {
+    u32x4 words = buffer_words(src);
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024, line = (uint32_t)(ld * 2);
+#pragma unroll
+    for (int q = 0; q < kMoves; ++q) {
+      const u32x4 w = buffer_words(src + (int64_t)(q * kStep) * ld);
+      words[0] = w[0];
+      words[1] = w[1];
+      words[2] = n > q * kStep ? (uint32_t)(n - q * kStep - 1) * line + (uint32_t)(D * 2) : 0;
+      load_to_lds(to + q * kThreads * 16, words, at);
+    }
+  }
+  // Rows wherever they are: `where(row)` in bytes from src, or kBeyond.
   template <typename F>
-  __device__ __forceinline__ void fetch(const uint16_t* tile, const void* src, int D, uint32_t wave, F at) const {
+  __device__ __forceinline__ void gather(const uint16_t* tile, const void* src, int D, uint32_t wave, F where) const {
     const u32x4 words = buffer_words(src);
     const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024;
     const bool in = col < (uint32_t)D;
 #pragma unroll
     for (int q = 0; q < kMoves; ++q) {
-      const uint32_t from = at(row + q * kStep);
+      const uint32_t from = where(row + q * kStep);
       load_to_lds(to + q * kThreads * 16, words, in && from != kBeyond ? from + col * 2 : kBeyond);
     }
   }

@@ -517,7 +517,7 @@ size_t engram_layer_norm_bwd_workspace_bytes(int64_t N, int64_t D);
 #define ENGRAM_WINDOW_ROWS_MAX 4194304
 #define ENGRAM_WINDOW_HEADS_MAX 1024
 #define ENGRAM_WINDOW_HEAD_ROWS_MAX 536870912 /* N * Hq */
-#define ENGRAM_WINDOW_SEQ_HEADS_MAX 4194304   /* B * Hk */
+#define ENGRAM_WINDOW_SEQ_HEADS_MAX 1048576   /* B * Hk */
 #define ENGRAM_WINDOW_D_MAX 128
 #define ENGRAM_WINDOW_SINKS_MAX 128
 engram_status engram_window_attn_fwd(const void *q, const void *k, const void *v, const int64_t *cu_seqlens, void *o,

@@ -18,7 +18,7 @@ _P, _I64, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_flo
 
 NORM_ROWS_MAX, NORM_D_MAX = 2097152, 16384
 WINDOW_ROWS_MAX, WINDOW_HEADS_MAX, WINDOW_HEAD_ROWS_MAX = 4194304, 1024, 536870912
-WINDOW_SEQ_HEADS_MAX, WINDOW_D_MAX, WINDOW_SINKS_MAX = 4194304, 128, 128
+WINDOW_SEQ_HEADS_MAX, WINDOW_D_MAX, WINDOW_SINKS_MAX = 1048576, 128, 128
 WINDOW_STEP_ROWS_MAX, WINDOW_CAPACITY_MAX = 4096, 1048576
 SCAN_ROWS_MAX, SCAN_STATES_MAX, SCAN_D_MAX, SCAN_VALUES_MAX = 16777216, 4194304, 65536, 34359738368
 SCAN_STEP_ROWS_MAX = 4096

@@ -58,7 +58,7 @@ struct WindowArgs {
   int64_t N, ldq, ldk, ldv, ldo, ldgo, ldout, ldgk, ldgv;
   int B, Hk, G, D, W, S;
   int tiles;                        // workgroups of a key head
-  int piece;                        // backward: tokens of a piece (sinks)
+  int piece, pieces, sink_blocks;   // backward: tokens of a piece, pieces there may be, their workgroups (0: no sinks)
   float scale;
   Divide by_G;
 };
@@ -266,12 +266,13 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) o[dt] = f32x16{};
   float m = -INFINITY, sum = 0.0f;
-  // (behind the last tile: zeros)
-  const auto fetch_tile = [&](int i) {
+  // the x-th of a tile's loads, keys and values in turn (behind the last tile: zeros)
+  constexpr int kLoads = 2 * pieces.kMoves;
+  const auto fetch = [&](int x, int i) {
     const int start = keys.start(i), n = keys.end(i) - start;
     const int64_t token = r.base + start, col = (int64_t)r.head * a.D;
-    pieces.fetch(lds[i & 1], a.k + token * a.ldk + col, a.ldk, n, a.D, k_at, wave);
-    pieces.fetch(lds[2 + i % 3], a.v + token * a.ldv + col, a.ldv, n, a.D, v_at, wave);
+    if (x % 2 == 0) pieces.move(x / 2, lds[i & 1], a.k + token * a.ldk + col, a.ldk, n, a.D, k_at, wave);
+    else pieces.move(x / 2, lds[2 + i % 3], a.v + token * a.ldv + col, a.ldv, n, a.D, v_at, wave);
   };
   // Operands on their way from LDS: of the next half's scores, and of this half's values.
   constexpr int kX = kD / 16;  // products of a half's scores, and of its values
@@ -307,38 +308,42 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   const auto step = [&](f32x16& s, f32x16& next, int i, auto half, auto more) {
     constexpr int u = decltype(half)::value, kEach = 16 / kX;
     constexpr bool kNext = decltype(more)::value;
+    static_assert(kLoads == kX, "a load beside each product");
     const lds_bytes tv = opaque(lds_of(lds[2 + i % 3])), tk = opaque(lds_of(lds[(i + 1) & 1]));
     const float less = m == -INFINITY ? 0.0f : -m * c;
     u32x4 p[2];
     next = f32x16{};
     __builtin_amdgcn_sched_barrier(0);
+    const auto weigh = [&](int from, int n) {
+#pragma unroll
+      for (int e = from; e < from + n; ++e) {
+        s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, less));
+        sum += s[e];
+      }
+      if ((from + n) % 8 == 0) p[(from + n) / 8 - 1] = operand<T>(s, (from + n) / 8 - 1);
+    };
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       if constexpr (kNext) next = product<T>(kf[x], q[x], next);
       vf[x] = columns(tv, 32 * u + 16 * (x / (kD / 32)), x % (kD / 32));
-#pragma unroll
-      for (int e = x * kEach; e < (x + 1) * kEach; ++e) {
-        s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, less));
-        sum += s[e];
-      }
-      if ((x + 1) * kEach % 8 == 0) p[(x + 1) * kEach / 8 - 1] = operand<T>(s, (x + 1) * kEach / 8 - 1);
+      weigh(x * kEach / 2, kEach / 2);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (u == 0) {
-      meet();  // the next tile is there, and this one's keys are read out, the last one's values too
-      fetch_tile(i + 2);
-    }
+    if constexpr (u == 0) meet();  // the next tile is there, and this one's keys are read out, the last one's values too
     float top = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       __builtin_amdgcn_sched_barrier(0);
       o[x % (kD / 32)] = product<T>(vf[x], p[x / (kD / 32)], o[x % (kD / 32)]);
-      // (behind the last tile this reads what lies there, for no one)
+      // (behind the last tile these read what lies there, for no one)
       if constexpr (kNext) read_keys(tk, u, x);
-      if constexpr (kNext)
-        if (x >= 2)
+      if constexpr (u == 0) fetch(x, i + 2);
+      if (x < kX / 2) {
+        weigh(8 + x * kEach, kEach);
+      } else if constexpr (kNext) {
 #pragma unroll
-          for (int e = (x - 2) * 16 / (kX - 2); e < (x - 1) * 16 / (kX - 2); ++e) top = fmaxf(top, next[e]);
+        for (int e = (x - kX / 2) * 2 * kEach; e < (x - kX / 2 + 1) * 2 * kEach; ++e) top = fmaxf(top, next[e]);
+      }
     }
     asm volatile("" : "+v"(sum), "+v"(top));  // or they move behind the branches, away from the products
     __builtin_amdgcn_sched_barrier(0);
@@ -346,10 +351,26 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   };
   constexpr auto first_half = std::integral_constant<int, 0>{};
   constexpr auto second_half = std::integral_constant<int, 1>{};
-  load_row<kD>(q, a.q + (r.base + (there ? t : 0)) * a.ldq + (int64_t)head * a.D, there, a.D, h);
-  fetch_tile(0);
-  fetch_tile(1);
-  meet();
+  // the queries through LDS, whole rows: a wave's own, where the second tile's values come later
+  {
+    const uint16_t* mine = lds[3] + wave * 32 * kD;
+    const Pieces<kD, 32, 64> whole(lane);
+    whole.gather(mine, a.q + (r.base + r.t0) * a.ldq + (int64_t)r.head * a.G * a.D, a.D, 0, [&](uint32_t row) {
+      uint32_t g;
+      const uint32_t t = r.token(32 * wave + row, a, &g);
+      return (int)(32 * wave + row) < r.rows ? t * (uint32_t)(a.ldq * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
+    });
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) fetch(x, 0);
+#pragma unroll
+    for (int x = 0; x < kLoads; x += 2) fetch(x, 1);
+    meet();
+#pragma unroll
+    for (int x = 0; x < kX; ++x) q[x] = rows(lds_of(mine), 0, x);
+    meet();
+#pragma unroll
+    for (int x = 1; x < kLoads; x += 2) fetch(x, 1);
+  }
   f32x16 s0 = f32x16{}, s1;
 #pragma unroll
   for (int x = 0; x < kX; ++x) s0 = product<T>(rows(lds_of(lds[0]), 0, x), q[x], s0);
@@ -506,68 +527,117 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   store_rows<kD>(mine, r, wave, lane, a);
 }
 
-// The sums of a piece of a sequence: [piece][key head][dk, dv][S][D].
+// The sinks' sums, fp32 and unscaled: [piece][key head][dk, dv][S][D], a piece for
+// each of the rows that see them as sinks, and then one a sequence for the rows whose
+// window they are in.
 __device__ __forceinline__ float* piece_sums(const WindowArgs& a, int64_t piece, int head, int which) {
   return a.sums + ((piece * a.Hk + head) * 2 + which) * a.S * a.D;
 }
 
-// dk and dv of 128 keys.  kSinks: the part of the sinks' (the first keys of a
-// sequence) that comes from the rows of one piece of it that see them as sinks,
-// fp32 and unscaled; otherwise the rows whose window the keys are in, and for sinks
-// the pieces' sums.
-template <typename T, int kD, bool kSinks>
-__global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kKeys * kD];  // [turn][queries, gradients of o] of 64 rows
+// dk (which: 0) or dv (1) of token j by the definition, by one wave: a lane's values
+// lane and lane + 64.
+template <typename T>
+__device__ __forceinline__ void define_key(float (&y)[2], const WindowArgs& a, int64_t base, int length, int head, int j,
+                                           int which) {
+  const int lane = threadIdx.x & 63, Hq = a.Hk * a.G;
+  const float c = a.scale * kLog2e;
+  const uint16_t* kj = a.k + (base + j) * a.ldk + (int64_t)head * a.D;
+  const uint16_t* vj = a.v + (base + j) * a.ldv + (int64_t)head * a.D;
+  const int behind = j < a.S ? length : (j + a.W < length ? j + a.W : length);
+  y[0] = y[1] = 0.0f;
+  for (int64_t row = (int64_t)j * a.G; row < (int64_t)behind * a.G; row += 64) {
+    const int64_t at = row + lane;
+    const bool in = at < (int64_t)behind * a.G;
+    float w = 0.0f;
+    if (in) {
+      const int64_t t = base + at / a.G;
+      const int hq = head * a.G + (int)(at % a.G);
+      const float s = dot_row<T>(a.q + t * a.ldq + (int64_t)hq * a.D, kj, a.D);
+      w = __builtin_amdgcn_exp2f(fmaf(s, c, -a.lse_in[t * Hq + hq] * kLog2e));
+      if (which == 0) w *= dot_row<T>(a.grad_o + t * a.ldgo + (int64_t)hq * a.D, vj, a.D) - a.delta[t * Hq + hq];
+    }
+    for (uint64_t left = __ballot(in); left; left &= left - 1) {
+      const int n = __builtin_ctzll(left);
+      const int64_t t = base + (row + n) / a.G, hq = head * a.G + (row + n) % a.G;
+      const uint16_t* from = which ? a.grad_o + t * a.ldgo + hq * a.D : a.q + t * a.ldq + hq * a.D;
+      const float wn = __shfl(w, n);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (lane + 64 * e < a.D) y[e] = fmaf(wn, one_value<T>(from[lane + 64 * e]), y[e]);
+    }
+  }
+}
+
+// dk and dv of 128 keys.  The first a.sink_blocks workgroups make the part of the
+// sinks (the first keys of a sequence) that comes from the rows of one piece of it
+// that see them as sinks; the others take the rows whose window the keys are in.  Four
+// waves have 32 keys each for the first half of a tile of rows, four the same keys for
+// the second; at the end they exchange what they have, and the first four leave
+// dk, the others dv.  (Keys in registers, values in LDS: with both in registers
+// there would be none left for operands on their way, and the waits for what is spilled
+// wait for the next tile too.)
+constexpr int kKeyWaves = 8, kKeyThreads = kKeyWaves * 64;
+template <typename T, int kD>
+__global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs a) {
+  constexpr int kX = kD / 16;
+  // the values; then [turn][queries, gradients of o] of 64 rows; at the end all of it for the exchange
+  constexpr int kValues = kRows * kD, kTile = kKeys * kD, kExchange = 4 * 64 * kD / 2 * 2;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[kValues + 4 * kTile > kExchange ? kValues + 4 * kTile : kExchange];
   __shared__ __attribute__((aligned(16))) float lses[2][kKeys], deltas[2][kKeys];
-  __shared__ __attribute__((aligned(16))) int tokens[2][kKeys];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t l = lane & 31, h = lane >> 5;
-  const int at = neighbours(blockIdx.x, gridDim.x), id = at % a.tiles, head = at / a.tiles;
-  const uint32_t unit = kSinks ? (uint32_t)a.piece : (uint32_t)kRows;
+  const uint32_t l = lane & 31, h = lane >> 5, quarter = wave & 3, half = wave >> 2;
+  const bool sinks = (int)blockIdx.x < a.sink_blocks;
+  const int at = sinks ? blockIdx.x : neighbours(blockIdx.x - a.sink_blocks, gridDim.x - a.sink_blocks);
+  const int per_head = sinks ? a.sink_blocks / a.Hk : a.tiles, id = at % per_head, head = at / per_head;
+  const uint32_t unit = sinks ? (uint32_t)a.piece : (uint32_t)kRows;
   const Sequence seq(a, id, 1, unit);
   const int64_t base = seq.start, tile = seq.tile;
   const int length = (int)seq.length;
   if (tile < 0 || length <= 0 || tile * unit >= length) return;
-  const int k0 = kSinks ? 0 : (int)tile * kRows;
-  // the rows' tokens
+  const int k0 = sinks ? 0 : (int)tile * kRows;
+  // the rows' tokens, and how far behind a key those lie that see it: `near` on, fewer than `span` further
   int from = k0, to = k0 + kRows - 1 + a.W;
-  if (kSinks) {
+  const int near = sinks ? a.W : 0;
+  if (sinks) {
     from = (int)tile * a.piece > a.W ? (int)tile * a.piece : a.W;
     to = ((int)tile + 1) * a.piece;
   }
   if (to > length) to = length;
   if (from >= to) return;  // no row of the piece sees a sink as one
-
-  const int key0 = k0 + 32 * wave, key = key0 + (int)l;
-  const int keys = kSinks ? (a.S < length ? a.S : length) : length;  // of the sequence, as far as they matter here
+  const int key0 = k0 + 32 * (int)quarter, key = key0 + (int)l;
+  const int keys = sinks ? (a.S < length ? a.S : length) : length;  // of the sequence, as far as they matter here
   const bool active = key0 < keys, there = key < keys;
-  u32x4 k[kD / 16], v[kD / 16];
-  const int64_t key_token = base + (there ? key : 0);
-  load_row<kD>(k, a.k + key_token * a.ldk + (int64_t)head * a.D, there, a.D, h);
-  load_row<kD>(v, a.v + key_token * a.ldv + (int64_t)head * a.D, there, a.D, h);
+  const int span = !there ? 0 : sinks ? length : a.W;
 
-  const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
+  u32x4 k[kX];
+  load_row<kD>(k, a.k + (base + (there ? key : 0)) * a.ldk + (int64_t)head * a.D, there, a.D, h);
+  const Pieces<kD, kRows, kKeyThreads> wide(threadIdx.x);
+  wide.fetch(lds, a.v + (base + k0) * a.ldv + (int64_t)head * a.D, a.ldv, keys - k0 < kRows ? keys - k0 : kRows, a.D,
+             wide.offset(a.ldv, a.D), wave);
+  uint16_t* const tiles = lds + kValues;
+
+  const Pieces<kD, kKeys, kKeyThreads> pieces(threadIdx.x);
   const int n = ((to - from) * a.G + kKeys - 1) / kKeys;  // tiles of rows
   const int Hq = a.Hk * a.G;
   float lse = 0.0f, delta = 0.0f;
-  int token = 0;
   int t0 = from;      // of the next tile to fetch: its first row's token and head
   uint32_t x0 = 0;
   const auto fetch = [&](int i) {
+    const int64_t first = base + t0, heads = (int64_t)head * a.G * a.D;
     const auto row_at = [&](uint32_t row, uint32_t* t, uint32_t* g) {
       const uint32_t x = x0 + row;
       *t = a.by_G(x);
       *g = x - *t * (uint32_t)a.G;
       return t0 + (int)*t < to;
     };
-    const int64_t first = base + t0, heads = (int64_t)head * a.G * a.D;
     const auto offset = [&](uint32_t row, int64_t ld) {
       uint32_t t, g;
       return row_at(row, &t, &g) ? t * (uint32_t)(ld * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
     };
-    pieces.gather(lds[i & 1][0], a.q + first * a.ldq + heads, a.D, wave, [&](uint32_t row) { return offset(row, a.ldq); });
-    pieces.gather(lds[i & 1][1], a.grad_o + first * a.ldgo + heads, a.D, wave,
-                 [&](uint32_t row) { return offset(row, a.ldgo); });
+    uint16_t* const to_q = tiles + (i & 1) * 2 * kTile;
+    pieces.gather(to_q, a.q + first * a.ldq + heads, a.D, wave, [&](uint32_t row) { return offset(row, a.ldq); });
+    pieces.gather(to_q + kTile, a.grad_o + first * a.ldgo + heads, a.D, wave,
+                  [&](uint32_t row) { return offset(row, a.ldgo); });
     if (wave == 0) {
       uint32_t t, g;
       const bool in = row_at(lane, &t, &g);
@@ -575,7 +645,6 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
       // a row that is not there has weights of 0
       lse = in ? a.lse_in[at] * kLog2e : INFINITY;
       delta = in ? a.delta[at] : 0.0f;
-      token = t0 + (int)t;
     }
     x0 += kKeys;
     t0 += (int)a.by_G(x0);
@@ -587,148 +656,180 @@ __global__ __launch_bounds__(kThreads, 2) void window_dkdv_kernel(WindowArgs a) 
   f32x16 dk[kD / 32], dv[kD / 32];
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
+  int t_first = from;       // of this tile: as t0 and x0
+  uint32_t x_first = 0;
   fetch(0);
   for (int i = 0; i < n; ++i) {
     if (wave == 0) {
       lses[i & 1][lane] = lse;
       deltas[i & 1][lane] = delta;
-      tokens[i & 1][lane] = token;
     }
     meet();
     if (i + 1 < n) fetch(i + 1);
-    if (!active) continue;
-    const lds_bytes tq = lds_of(lds[i & 1][0]), tg = lds_of(lds[i & 1][1]);
-#pragma unroll 1
-    for (int u = 0; u < 2; ++u) {
-      const int ta = tokens[i & 1][32 * u], tb = tokens[i & 1][32 * u + 31];  // the rows' first and last token
-      if (kSinks ? key0 > tb - a.W : key0 > tb || key0 + 31 <= ta - a.W) continue;
-      f32x16 s = f32x16{}, d = f32x16{};
+    const uint32_t x = x_first + 32 * half;  // this wave's rows: heads x to x + 31 from token t_first's first on
+    const int ta = t_first + (int)a.by_G(x), tb = t_first + (int)a.by_G(x + 31);
+    const int t_here = t_first;
+    const uint32_t x_here = x;
+    x_first += kKeys;
+    t_first += (int)a.by_G(x_first);
+    x_first -= a.by_G(x_first) * (uint32_t)a.G;
+    // rows lie between ta - key0 - 31 and tb - key0 tokens behind the keys
+    const int least = ta - key0 - 31, most = tb - key0;
+    if (!active || most < near || (!sinks && least >= a.W)) continue;
+    const lds_bytes tq = opaque(lds_of(tiles + (i & 1) * 2 * kTile)), tg = tq + 2 * kTile, tv = lds_of(lds);
+    const int r0 = 32 * (int)half;
+    u32x4 fa[kX];
+    f32x16 s = f32x16{}, d = f32x16{};
 #pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) s = product<T>(rows(tq, 32 * u, kk), k[kk], s);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int kk = 0; kk < kX; ++kk) fa[kk] = rows(tq + r0 * kD * 2, 0, kk);
 #pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) d = product<T>(rows(tg, 32 * u, kk), v[kk], d);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int kk = 0; kk < kX; ++kk) s = product<T>(fa[kk], k[kk], s);
+#pragma unroll
+    for (int kk = 0; kk < kX; ++kk)
+      d = product<T>(rows(tg + r0 * kD * 2, 0, kk), rows(tv + quarter * 32 * kD * 2, 0, kk), d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4 ls = *reinterpret_cast<const f32x4*>(&lses[i & 1][r0 + 8 * j + 4 * h]);
+      const f32x4 de = *reinterpret_cast<const f32x4*>(&deltas[i & 1][r0 + 8 * j + 4 * h]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], c, -ls[e]));
+        d[4 * j + e] = s[4 * j + e] * (d[4 * j + e] - de[e]);
+      }
+    }
+    if (least < near || (!sinks && most >= a.W) || key0 + 31 >= keys) {
+      uint32_t xe = x_here + 4 * h;
+      asm volatile("" : "+v"(xe));  // or what follows moves in front of the branch
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int behind = t_here + (int)a.by_G(xe + 8 * (e / 4) + e % 4) - key - near;
+        const bool seen = (uint32_t)behind < (uint32_t)span;
+        s[e] = seen ? s[e] : 0.0f;
+        d[e] = seen ? d[e] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const u32x4 p = operand<T>(s, w);
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt) dv[dt] = product<T>(columns(tg + (r0 + 16 * w) * kD * 2, 0, dt), p, dv[dt]);
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const u32x4 p = operand<T>(d, w);
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = product<T>(columns(tq + (r0 + 16 * w) * kD * 2, 0, dt), p, dk[dt]);
+    }
+  }
+
+  // The exchange: the first four waves' dv, then the others' dk, in the order they
+  // are there for each lane.
+  f32x4* const given = reinterpret_cast<f32x4*>(lds) + quarter * (kD / 8) * 64 + lane;
+  __syncthreads();  // the tiles are read out
+#pragma unroll
+  for (int turn = 0; turn < 2; ++turn) {
+    if (half == (uint32_t)turn) {
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x16& x = turn ? dk[dt] : dv[dt];
+          given[(dt * 4 + j) * 64] = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+        }
+    }
+    __syncthreads();
+    if (half != (uint32_t)turn) {
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 x = given[(dt * 4 + j) * 64];
+          f32x16& to = turn ? dk[dt] : dv[dt];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[4 * j + e] += x[e];
+        }
+    }
+    __syncthreads();
+  }
+  const int which = (int)half;
+  f32x16 sum[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) sum[dt] = half ? dv[dt] : dk[dt];
+
+  // Sinks that rows behind their window see too: fp32, joined by the next launch.
+  const bool part = sinks || (key < a.S && length > a.W);
+  if (part && there) {
+    float* out = piece_sums(a, sinks ? id : a.pieces + seq.b, head, which) + (int64_t)key * a.D;
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(&lses[i & 1][32 * u + 8 * j + 4 * h]);
-        const f32x4 de = *reinterpret_cast<const f32x4*>(&deltas[i & 1][32 * u + 8 * j + 4 * h]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], c, -ls[e]));
-          d[4 * j + e] = s[4 * j + e] * (d[4 * j + e] - de[e]);
-        }
+        const int col = 32 * dt + 8 * j + 4 * (int)h;
+        if (col < a.D)
+          *reinterpret_cast<f32x4*>(out + col) = f32x4{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
       }
-      if (kSinks ? key0 + 31 > ta - a.W || key0 + 31 >= keys : key0 + 31 > ta || key0 <= tb - a.W) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = tokens[i & 1][32 * u + 8 * (e / 4) + 4 * h + e % 4];
-          const bool seen = kSinks ? key <= t - a.W && key < keys : key <= t && key > t - a.W;
-          s[e] = seen ? s[e] : 0.0f;
-          d[e] = seen ? d[e] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const u32x4 p = operand<T>(s, w), e = operand<T>(d, w);
-#pragma unroll
-        for (int dt = 0; dt < kD / 32; ++dt) {
-          __builtin_amdgcn_sched_barrier(0);
-          dv[dt] = product<T>(columns(tg, 32 * u + 16 * w, dt), p, dv[dt]);
-          dk[dt] = product<T>(columns(tq, 32 * u + 16 * w, dt), e, dk[dt]);
-        }
-      }
-    }
   }
+  if (sinks) return;
+  uint16_t* const mine = lds + wave * 32 * kD;
+  const float times = which ? 1.0f : a.scale;
+  put_rows<T, kD>(mine, sum, times, lane);
+  const uint64_t redo = __ballot(there && !part && !finite_rows<kD>(sum));
+  between_lanes();
+  for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
+    const int x = __builtin_ctz(bad);
+    float y[2];
+    define_key<T>(y, a, base, length, head, key0 + x, which);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e] * times, 0.0f);
+  }
+  between_lanes();
+  uint16_t* out = which ? a.grad_v : a.grad_k;
+  const int64_t ld = which ? a.ldgv : a.ldgk;
+  const int done = length > a.W ? a.S : 0;  // keys before this one are the next launch's
+#pragma unroll
+  for (int i = 0; i < kD / 16; ++i) {
+    const uint32_t x = (i * 64 + lane) / (kD / 8), col = (i * 64 + lane) % (kD / 8) * 8;
+    const int j = key0 + (int)x;
+    if (j >= done && j < length && (int)col < a.D)
+      store16(out + (base + j) * ld + (int64_t)head * a.D + col, load16(mine + place<kD>(x, col)));
+  }
+}
 
-  if (kSinks) {
-    if (there) {
-      float *to_k = piece_sums(a, id, head, 0) + (int64_t)key * a.D, *to_v = piece_sums(a, id, head, 1) + (int64_t)key * a.D;
-#pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = 32 * dt + 8 * j + 4 * (int)h;
-          if (col >= a.D) continue;
-          *reinterpret_cast<f32x4*>(to_k + col) = f32x4{dk[dt][4 * j], dk[dt][4 * j + 1], dk[dt][4 * j + 2], dk[dt][4 * j + 3]};
-          *reinterpret_cast<f32x4*>(to_v + col) = f32x4{dv[dt][4 * j], dv[dt][4 * j + 1], dv[dt][4 * j + 2], dv[dt][4 * j + 3]};
-        }
-    }
-    return;
-  }
-  if (key < a.S && there && length > a.W) {
-    const int64_t mine = first_tile(base, seq.b, 1, (uint32_t)a.piece);
-    for (int p = a.W / a.piece; p <= (length - 1) / a.piece; ++p) {
-      const float *from_k = piece_sums(a, mine + p, head, 0) + (int64_t)key * a.D;
-      const float *from_v = piece_sums(a, mine + p, head, 1) + (int64_t)key * a.D;
-#pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = 32 * dt + 8 * j + 4 * (int)h;
-          if (col >= a.D) continue;
-          const f32x4 x = *reinterpret_cast<const f32x4*>(from_k + col), y = *reinterpret_cast<const f32x4*>(from_v + col);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dk[dt][4 * j + e] += x[e];
-            dv[dt][4 * j + e] += y[e];
-          }
-        }
-    }
-  }
-
-  __syncthreads();  // the tiles are read out
-  uint16_t* mine = lds[0][0] + wave * 32 * kD;
-  const auto finish = [&](const int which, const f32x16(&sum)[kD / 32]) {
-    const float times = which ? 1.0f : a.scale;
-    put_rows<T, kD>(mine, sum, times, lane);
-    const uint64_t redo = __ballot(there && !finite_rows<kD>(sum));
-    between_lanes();
-    for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
-      const int x = __builtin_ctz(bad), j = key0 + x;
-      const uint16_t* kx = a.k + (base + j) * a.ldk + (int64_t)head * a.D;
-      const uint16_t* vx = a.v + (base + j) * a.ldv + (int64_t)head * a.D;
-      const int behind = j < a.S ? length : (j + a.W < length ? j + a.W : length);
-      float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
-      for (int64_t row = (int64_t)j * a.G; row < (int64_t)behind * a.G; row += 64) {
-        const int64_t at = row + lane;
-        const bool in = at < (int64_t)behind * a.G;
-        const int64_t t = base + at / a.G;
-        const int hq = head * a.G + (int)(at % a.G);
-        float w = 0.0f;
-        if (in) {
-          const float s = dot_row<T>(a.q + t * a.ldq + (int64_t)hq * a.D, kx, a.D);
-          w = __builtin_amdgcn_exp2f(fmaf(s, c, -a.lse_in[t * Hq + hq] * kLog2e));
-          if (which == 0) w *= dot_row<T>(a.grad_o + t * a.ldgo + (int64_t)hq * a.D, vx, a.D) - a.delta[t * Hq + hq];
-        }
-        for (uint64_t left = __ballot(in); left; left &= left - 1) {
-          const int n = __builtin_ctzll(left);
-          const int64_t tn = base + (row + n) / a.G;
-          const int64_t hn = head * a.G + (row + n) % a.G;
-          const uint16_t* from_row = which ? a.grad_o + tn * a.ldgo + hn * a.D : a.q + tn * a.ldq + hn * a.D;
-          const float wn = __shfl(w, n);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if ((int)lane + 64 * e < a.D) y[e] = fmaf(wn, one_value<T>(from_row[lane + 64 * e]), y[e]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e] * times, 0.0f);
-    }
-    between_lanes();
-    uint16_t* out = which ? a.grad_v : a.grad_k;
-    const int64_t ld = which ? a.ldgv : a.ldgk;
-#pragma unroll
-    for (int i = 0; i < kD / 16; ++i) {
-      const uint32_t x = (i * 64 + lane) / (kD / 8), col = (i * 64 + lane) % (kD / 8) * 8;
-      if (key0 + (int)x < length && (int)col < a.D)
-        store16(out + (base + key0 + x) * ld + (int64_t)head * a.D + col, load16(mine + place<kD>(x, col)));
-    }
-    between_lanes();
+// dk and dv of the sinks of sequences longer than the window: a wave for each
+// sequence, key head, sink and gradient, a lane's values 2 lane and 2 lane + 1.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void window_sinks_kernel(WindowArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int which = blockIdx.y & 1, j = (int)blockIdx.y >> 1;
+  const int at = blockIdx.x * (kJoinThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int head = at % a.Hk, b = at / a.Hk;
+  if (b >= a.B) return;
+  const Sequences seqs{a.cu, a.N, a.B};
+  const int64_t base = seqs.start(b), all = seqs.end(b) - base;
+  if (all <= a.W || j >= all) return;
+  const int length = (int)all, d = 2 * lane;
+  const bool mine = d < a.D;
+  const auto add = [&](float (&y)[2], int64_t piece) {
+    const f32x2 x = mine ? *reinterpret_cast<const f32x2*>(piece_sums(a, piece, head, which) + (int64_t)j * a.D + d) : f32x2{0, 0};
+    y[0] += x[0];
+    y[1] += x[1];
   };
-  finish(0, dk);
-  finish(1, dv);
+  float y[2] = {0.0f, 0.0f};
+  add(y, a.pieces + b);
+  const int64_t first = first_tile(base, b, 1, (uint32_t)a.piece);
+  for (int p = a.W / a.piece; p <= (length - 1) / a.piece; ++p) add(y, first + p);
+  const float times = which ? 1.0f : a.scale;
+  uint16_t* out = (which ? a.grad_v + (base + j) * a.ldgv : a.grad_k + (base + j) * a.ldgk) + (int64_t)head * a.D;
+  if (__any(mine && !(fabsf(y[0]) < INFINITY && fabsf(y[1]) < INFINITY))) {
+    define_key<T>(y, a, base, length, head, j, which);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 64 * e < a.D) out[lane + 64 * e] = (uint16_t)pack2<T>(y[e] * times, 0.0f);
+  } else if (mine) {
+    *reinterpret_cast<uint32_t*>(out + d) = pack2<T>(y[0] * times, y[1] * times);
+  }
 }
 
 struct WindowKernels {
@@ -737,7 +838,7 @@ struct WindowKernels {
 template <typename T, int kD>
 WindowKernels window_of() {
   return {(const void*)&window_fwd_kernel<T, kD>, (const void*)&window_dq_kernel<T, kD>,
-          (const void*)&window_dkdv_kernel<T, kD, false>, (const void*)&window_dkdv_kernel<T, kD, true>};
+          (const void*)&window_dkdv_kernel<T, kD>, (const void*)&window_sinks_kernel<T>};
 }
 WindowKernels window_kernels(int dtype, int D) {
   if (dtype == ENGRAM_BF16) return D <= 64 ? window_of<bf16_t, 64>() : window_of<bf16_t, 128>();
@@ -746,7 +847,7 @@ WindowKernels window_kernels(int dtype, int D) {
 
 WindowArgs window_args(const WindowCall& w) {
   WindowArgs a{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
-               nullptr, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0f, Divide((uint32_t)(w.Hq / w.Hk))};
+               nullptr, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0f, Divide((uint32_t)(w.Hq / w.Hk))};
   a.q = w.q; a.k = w.k; a.v = w.v; a.cu = w.cu;
   a.N = w.N; a.ldq = w.ldq; a.ldk = w.ldk; a.ldv = w.ldv;
   a.B = (int)w.B; a.Hk = (int)w.Hk; a.G = (int)(w.Hq / w.Hk); a.D = (int)w.D;
@@ -755,10 +856,10 @@ WindowArgs window_args(const WindowCall& w) {
   a.scale = w.scale;
   return a;
 }
-hipError_t launch_heads(const void* kernel, WindowArgs a, int64_t tiles, hipStream_t stream) {
+hipError_t launch_heads(const void* kernel, WindowArgs a, int64_t tiles, int threads, hipStream_t stream) {
   a.tiles = (int)tiles;
   void* args[] = {&a};
-  return hipLaunchKernel(kernel, dim3((unsigned)(tiles * a.Hk)), dim3(kThreads), args, 0, stream);
+  return hipLaunchKernel(kernel, dim3((unsigned)(tiles * a.Hk + a.sink_blocks)), dim3((unsigned)threads), args, 0, stream);
 }
 
 // Tokens of a piece: some thousand workgroups in all, but pieces worth a launch.
@@ -772,14 +873,14 @@ int64_t delta_values(int64_t N, int64_t Hq) { return (N * Hq + 3) / 4 * 4; }
 
 size_t window_bwd_workspace(int64_t N, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks) {
   int64_t values = delta_values(N, Hq);
-  if (sinks > 0 && window < N) values += (N / piece_of(N, Hk) + B) * Hk * 2 * sinks * D;
+  if (sinks > 0 && window < N) values += (N / piece_of(N, Hk) + 2 * B) * Hk * 2 * sinks * D;
   return (size_t)values * sizeof(float);
 }
 
 hipError_t launch_window_fwd(const WindowCall& w, hipStream_t stream) {
   WindowArgs a = window_args(w);
   a.out = w.o; a.ldout = w.ldo; a.lse = w.lse;
-  return launch_heads(window_kernels(w.dtype, a.D).fwd, a, a.N * a.G / kRows + a.B, stream);
+  return launch_heads(window_kernels(w.dtype, a.D).fwd, a, a.N * a.G / kRows + a.B, kThreads, stream);
 }
 
 hipError_t launch_window_bwd(const WindowCall& w, hipStream_t stream) {
@@ -790,9 +891,16 @@ hipError_t launch_window_bwd(const WindowCall& w, hipStream_t stream) {
   a.delta = static_cast<float*>(w.workspace);
   a.sums = a.delta + delta_values(w.N, w.Hq);
   a.piece = (int)piece_of(w.N, w.Hk);
-  hipError_t e = launch_heads(k.dq, a, a.N * a.G / kRows + a.B, stream);
-  if (e == hipSuccess && a.S > 0 && a.W < a.N) e = launch_heads(k.sinks, a, a.N / a.piece + a.B, stream);
-  return e == hipSuccess ? launch_heads(k.dkdv, a, a.N / kRows + a.B, stream) : e;
+  hipError_t e = launch_heads(k.dq, a, a.N * a.G / kRows + a.B, kThreads, stream);
+  if (e != hipSuccess) return e;
+  const bool sinks = a.S > 0 && a.W < a.N;
+  a.pieces = (int)(a.N / a.piece) + a.B;
+  if (sinks) a.sink_blocks = a.pieces * a.Hk;
+  e = launch_heads(k.dkdv, a, a.N / kRows + a.B, kKeyThreads, stream);
+  if (e != hipSuccess || !sinks) return e;
+  void* args[] = {&a};
+  return hipLaunchKernel(k.sinks, dim3((unsigned)((a.B * a.Hk * 64 + kJoinThreads - 1) / kJoinThreads), (unsigned)(2 * a.S)),
+                         dim3(kJoinThreads), args, 0, stream);
 }
 
 }  // namespace engram

@@ -125,40 +125,41 @@ template <int kD, int kRows, int kThreads>
 struct Pieces {
   static constexpr int kMoves = kRows * kD / 8 / kThreads;
   static constexpr int kStep = kThreads * 8 / kD;  // rows between a lane's pieces
-  static_assert(kMoves * kThreads * 8 == kRows * kD && kStep % 16 == 0, "the order of the pieces repeats every 16 rows");
-  uint32_t row, col;  // of the first; the others' column is the same
+  static_assert(kMoves * kThreads * 8 == kRows * kD, "");
+  // the order of the pieces repeats every 16 rows: else a lane's column is another for each
+  static constexpr bool kSame = kStep % 16 == 0;
+  uint32_t row, col;  // of the first
   __device__ __forceinline__ explicit Pieces(uint32_t thread)
       : row(thread / (kD / 8)), col(((thread % (kD / 8)) ^ turn<kD>(thread / (kD / 8))) * 8) {}
   // The place of the first piece, in bytes from a tile's first row, where rows are
   // ld values apart.
   __device__ __forceinline__ uint32_t offset(int64_t ld, int D) const {
+    static_assert(kSame, "one offset serves all of a lane's pieces");
     return col < (uint32_t)D ? row * (uint32_t)(ld * 2) + col * 2 : kBeyond;
   }
-  // n rows (or fewer: zeros; the memory's bound sees to it) from src on, ld apart;
-  // `at`: the above.  No vector instruction but the loads.
+  // Of n rows (or fewer: zeros; the memory's bound sees to it) from src on, ld apart,
+  // the q-th pieces; `at`: the above.  No vector instruction but the load.
+  __device__ __forceinline__ void move(int q, const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,
+                                       uint32_t wave) const {
+    u32x4 words = buffer_words(src + (int64_t)(q * kStep) * ld);
+    words[2] = n > q * kStep ? (uint32_t)(n - q * kStep - 1) * (uint32_t)(ld * 2) + (uint32_t)(D * 2) : 0;
+    load_to_lds((uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024 + q * kThreads * 16, words, at);
+  }
   __device__ __forceinline__ void fetch(const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,
                                         uint32_t wave) const {
-    u32x4 words = buffer_words(src);
-    const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024, line = (uint32_t)(ld * 2);
 #pragma unroll
-    for (int q = 0; q < kMoves; ++q) {
-      const u32x4 w = buffer_words(src + (int64_t)(q * kStep) * ld);
-      words[0] = w[0];
-      words[1] = w[1];
-      words[2] = n > q * kStep ? (uint32_t)(n - q * kStep - 1) * line + (uint32_t)(D * 2) : 0;
-      load_to_lds(to + q * kThreads * 16, words, at);
-    }
+    for (int q = 0; q < kMoves; ++q) move(q, tile, src, ld, n, D, at, wave);
   }
   // Rows wherever they are: `where(row)` in bytes from src, or kBeyond.
   template <typename F>
   __device__ __forceinline__ void gather(const uint16_t* tile, const void* src, int D, uint32_t wave, F where) const {
     const u32x4 words = buffer_words(src);
     const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024;
-    const bool in = col < (uint32_t)D;
 #pragma unroll
     for (int q = 0; q < kMoves; ++q) {
       const uint32_t from = where(row + q * kStep);
-      load_to_lds(to + q * kThreads * 16, words, in && from != kBeyond ? from + col * 2 : kBeyond);
+      const uint32_t c = kSame ? col : col ^ (turn<kD>(row) ^ turn<kD>(row + q * kStep)) * 8;
+      load_to_lds(to + q * kThreads * 16, words, c < (uint32_t)D && from != kBeyond ? from + c * 2 : kBeyond);
     }
   }
 };

@@ -573,16 +573,16 @@ __device__ __forceinline__ void define_key(float (&y)[2], const WindowArgs& a, i
 // that see them as sinks; the others take the rows whose window the keys are in.  Four
 // waves have 32 keys each for the first half of a tile of rows, four the same keys for
 // the second; at the end they exchange what they have, and the first four leave
-// dk, the others dv.  (Keys in registers, values in LDS: with both in registers
-// there would be none left for operands on their way, and the waits for what is spilled
-// wait for the next tile too.)
+// dk, the others dv.  Keys and values stay in LDS: in registers they would leave
+// none for operands on their way, and the waits for what is spilled wait for
+// the next tile too.
 constexpr int kKeyWaves = 8, kKeyThreads = kKeyWaves * 64;
 template <typename T, int kD>
 __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs a) {
   constexpr int kX = kD / 16;
-  // the values; then [turn][queries, gradients of o] of 64 rows; at the end all of it for the exchange
-  constexpr int kValues = kRows * kD, kTile = kKeys * kD, kExchange = 4 * 64 * kD / 2 * 2;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[kValues + 4 * kTile > kExchange ? kValues + 4 * kTile : kExchange];
+  // the values and keys; then [turn][queries, gradients of o] of 64 rows; at the end half of it for the exchange
+  constexpr int kTile = kKeys * kD;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * kRows * kD + 4 * kTile];
   __shared__ __attribute__((aligned(16))) float lses[2][kKeys], deltas[2][kKeys];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5, quarter = wave & 3, half = wave >> 2;
@@ -609,12 +609,12 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   const bool active = key0 < keys, there = key < keys;
   const int span = !there ? 0 : sinks ? length : a.W;
 
-  u32x4 k[kX];
-  load_row<kD>(k, a.k + (base + (there ? key : 0)) * a.ldk + (int64_t)head * a.D, there, a.D, h);
   const Pieces<kD, kRows, kKeyThreads> wide(threadIdx.x);
-  wide.fetch(lds, a.v + (base + k0) * a.ldv + (int64_t)head * a.D, a.ldv, keys - k0 < kRows ? keys - k0 : kRows, a.D,
-             wide.offset(a.ldv, a.D), wave);
-  uint16_t* const tiles = lds + kValues;
+  const int n_keys = keys - k0 < kRows ? keys - k0 : kRows;
+  wide.fetch(lds, a.v + (base + k0) * a.ldv + (int64_t)head * a.D, a.ldv, n_keys, a.D, wide.offset(a.ldv, a.D), wave);
+  wide.fetch(lds + kRows * kD, a.k + (base + k0) * a.ldk + (int64_t)head * a.D, a.ldk, n_keys, a.D,
+             wide.offset(a.ldk, a.D), wave);
+  uint16_t* const tiles = lds + 2 * kRows * kD;
 
   const Pieces<kD, kKeys, kKeyThreads> pieces(threadIdx.x);
   const int n = ((to - from) * a.G + kKeys - 1) / kKeys;  // tiles of rows
@@ -678,48 +678,79 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     if (!active || most < near || (!sinks && least >= a.W)) continue;
     const lds_bytes tq = opaque(lds_of(tiles + (i & 1) * 2 * kTile)), tg = tq + 2 * kTile, tv = lds_of(lds);
     const int r0 = 32 * (int)half;
-    u32x4 fa[kX];
+    // The operands from the tiles of rows, in the order of their products: queries and
+    // gradients of o by rows, then gradients and queries by columns; four on their way.
+    constexpr int kRing = 4;
+    u32x4 f[kRing], kv[2], p[2], e[2];
+    const lds_bytes tk = tv + kRows * kD * 2 + quarter * 32 * kD * 2, tw = tv + quarter * 32 * kD * 2;
+    const auto read = [&](int n) {
+      const int x = n % kX, side = n / kX;
+      if (side >= 4) return;
+      const lds_bytes t = (side == 0 || side == 3 ? tq : tg) + r0 * kD * 2;
+      f[n % kRing] = side < 2 ? rows(t, 0, x) : columns(t + 16 * (x / (kD / 32)) * kD * 2, 0, x % (kD / 32));
+    };
+    const auto read_key = [&](int n) {
+      if (n < 2 * kX) kv[n & 1] = n < kX ? rows(tk, 0, n) : rows(tw, 0, n - kX);
+    };
     f32x16 s = f32x16{}, d = f32x16{};
+    f32x4 row[2];
+    const auto read_lse = [&](int j) { row[j & 1] = *reinterpret_cast<const f32x4*>(&lses[i & 1][r0 + 8 * j + 4 * h]); };
+    const auto read_delta = [&](int j) { row[j & 1] = *reinterpret_cast<const f32x4*>(&deltas[i & 1][r0 + 8 * j + 4 * h]); };
+    constexpr int kEach = 16 / kX;
 #pragma unroll
-    for (int kk = 0; kk < kX; ++kk) fa[kk] = rows(tq + r0 * kD * 2, 0, kk);
+    for (int n = 0; n < kRing; ++n) read(n);
+    read_key(0);
+    read_key(1);
 #pragma unroll
-    for (int kk = 0; kk < kX; ++kk) s = product<T>(fa[kk], k[kk], s);
-#pragma unroll
-    for (int kk = 0; kk < kX; ++kk)
-      d = product<T>(rows(tg + r0 * kD * 2, 0, kk), rows(tv + quarter * 32 * kD * 2, 0, kk), d);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const f32x4 ls = *reinterpret_cast<const f32x4*>(&lses[i & 1][r0 + 8 * j + 4 * h]);
-      const f32x4 de = *reinterpret_cast<const f32x4*>(&deltas[i & 1][r0 + 8 * j + 4 * h]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], c, -ls[e]));
-        d[4 * j + e] = s[4 * j + e] * (d[4 * j + e] - de[e]);
-      }
+    for (int x = 0; x < kX; ++x) {
+      __builtin_amdgcn_sched_barrier(0);
+      s = product<T>(f[x % kRing], kv[x & 1], s);
+      read(x + kRing);
+      read_key(x + 2);
     }
+    read_lse(0);
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      __builtin_amdgcn_sched_barrier(0);
+      d = product<T>(f[x % kRing], kv[x & 1], d);
+      read(kX + x + kRing);
+      read_key(kX + x + 2);
+      if (x * kEach % 4 == 0 && x * kEach < 12) read_lse(x * kEach / 4 + 1);
+#pragma unroll
+      for (int m = x * kEach; m < (x + 1) * kEach; ++m)
+        s[m] = __builtin_amdgcn_exp2f(fmaf(s[m], c, -row[m / 4 & 1][m % 4]));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    read_delta(0);
     if (least < near || (!sinks && most >= a.W) || key0 + 31 >= keys) {
       uint32_t xe = x_here + 4 * h;
       asm volatile("" : "+v"(xe));  // or what follows moves in front of the branch
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int behind = t_here + (int)a.by_G(xe + 8 * (e / 4) + e % 4) - key - near;
-        const bool seen = (uint32_t)behind < (uint32_t)span;
-        s[e] = seen ? s[e] : 0.0f;
-        d[e] = seen ? d[e] : 0.0f;
+      for (int m = 0; m < 16; ++m) {
+        const int behind = t_here + (int)a.by_G(xe + 8 * (m / 4) + m % 4) - key - near;
+        s[m] = (uint32_t)behind < (uint32_t)span ? s[m] : 0.0f;
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const u32x4 p = operand<T>(s, w);
+    for (int w = 0; w < 2; ++w) p[w] = operand<T>(s, w);
 #pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt) dv[dt] = product<T>(columns(tg + (r0 + 16 * w) * kD * 2, 0, dt), p, dv[dt]);
+    for (int x = 0; x < kX; ++x) {
+      __builtin_amdgcn_sched_barrier(0);
+      dv[x % (kD / 32)] = product<T>(f[x % kRing], p[x / (kD / 32)], dv[x % (kD / 32)]);
+      read(2 * kX + x + kRing);
+      if (x * kEach % 4 == 0 && x * kEach < 12) read_delta(x * kEach / 4 + 1);
+#pragma unroll
+      for (int m = x * kEach; m < (x + 1) * kEach; ++m) d[m] = s[m] * (d[m] - row[m / 4 & 1][m % 4]);
+      if ((x + 1) * kEach % 8 == 0) e[(x + 1) * kEach / 8 - 1] = operand<T>(d, (x + 1) * kEach / 8 - 1);
     }
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const u32x4 p = operand<T>(d, w);
-#pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = product<T>(columns(tq + (r0 + 16 * w) * kD * 2, 0, dt), p, dk[dt]);
+    for (int x = 0; x < kX; ++x) {
+      __builtin_amdgcn_sched_barrier(0);
+      dk[x % (kD / 32)] = product<T>(f[x % kRing], e[x / (kD / 32)], dk[x % (kD / 32)]);
+      read(3 * kX + x + kRing);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // The exchange: the first four waves' dv, then the others' dk, in the order they

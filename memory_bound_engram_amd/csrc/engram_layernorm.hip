@@ -24,7 +24,7 @@
 namespace engram {
 namespace {
 
-constexpr int kThreads = 256;  // of a workgroup that takes whole rows a wave or less
+constexpr int kRowThreads = 256;  // of a workgroup whose rows are a wave or less
 constexpr int kMostWaves = 16;
 
 // The sum over kLanes lanes, in each of them.
@@ -77,64 +77,76 @@ struct Place {
   int row, rows, lane, lanes;
   __device__ __forceinline__ Place()
       : row(kGroup ? threadIdx.x / (kGroup ? kGroup : 1) : 0),
-        rows(kGroup ? kThreads / (kGroup ? kGroup : 1) : 1),
+        rows(kGroup ? kRowThreads / (kGroup ? kGroup : 1) : 1),
         lane(kGroup ? threadIdx.x % (kGroup ? kGroup : 1) : threadIdx.x),
         lanes(kGroup ? kGroup : blockDim.x) {}
 };
 
-template <typename T, int kGroup, int kVecs>
-__global__ __launch_bounds__(kGroup ? kThreads : kMostWaves * 64) void layer_norm_fwd_kernel(NormArgs a) {
+template <typename T, int kGroup, int kVecs, int kThreads>
+__global__ __launch_bounds__(kThreads) void layer_norm_fwd_kernel(NormArgs a) {
   __shared__ float sums[2][1][kMostWaves];
   const Place<kGroup> at;
-  const int64_t n = (int64_t)blockIdx.x * at.rows + at.row;
-  const bool in = n < a.N;
-  if (kGroup == 0 && !in) return;
-  const T* x = static_cast<const T*>(a.x) + (in ? n : 0) * a.ldx;
   const int nv = a.D / 8;
   const float inv = 1.0f / (float)a.D;
-  float v[kVecs][8], sum[1] = {0.0f};
+  float w[kVecs][8], b[kVecs][8];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = at.lane + i * at.lanes;
-    const bool mine = in && c < nv;
-    const Raw<T> raw = mine ? load_raw(x + 8 * c) : zero_raw<T>();
-    unpack8(raw, v[i]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum[0] += v[i][k];
+    unpack8(c < nv ? load_raw(a.w + 8 * c) : zero_raw<float>(), w[i]);
+    unpack8(c < nv && a.b ? load_raw(a.b + 8 * c) : zero_raw<float>(), b[i]);
   }
-  row_sums<kGroup>(sum, sums[0]);
-  const float mean = sum[0] * inv;
-  sum[0] = 0.0f;
+  Raw<T> raw[kVecs];
+  const auto fetch = [&](int64_t n) {
+    const bool in = n < a.N;
+    const T* x = static_cast<const T*>(a.x) + (in ? n : 0) * a.ldx;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const bool mine = at.lane + i * at.lanes < nv;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[i][k] -= mean;
-      if (mine) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = at.lane + i * at.lanes;
+      raw[i] = in && c < nv ? load_raw(x + 8 * c) : zero_raw<T>();
     }
-  }
-  row_sums<kGroup>(sum, sums[1]);
-  const float rstd = 1.0f / sqrtf(sum[0] * inv + a.eps);
-  if (!in) return;
-  if (a.saved && at.lane == 0) *reinterpret_cast<f32x2*>(a.saved + 2 * n) = f32x2{mean, rstd};
-  T* y = static_cast<T*>(a.out) + n * a.ldout;
+  };
+  const int64_t step = (int64_t)gridDim.x * at.rows;
+  int64_t n = (int64_t)blockIdx.x * at.rows + at.row;
+  fetch(n);
+  for (int64_t first = (int64_t)blockIdx.x * at.rows; first < a.N; first += step, n += step) {
+    float v[kVecs][8], sum[1] = {0.0f};
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int c = at.lane + i * at.lanes;
-    if (c >= nv) continue;
-    float w[8], b[8];
-    unpack8(load_raw(a.w + 8 * c), w);
-    if (a.b) unpack8(load_raw(a.b + 8 * c), b);
-    else unpack8(zero_raw<float>(), b);
+    for (int i = 0; i < kVecs; ++i) {
+      unpack8(raw[i], v[i]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[i][k] = fmaf(v[i][k] * rstd, w[k], b[k]);
-    store8<true>(y + 8 * c, v[i]);
+      for (int k = 0; k < 8; ++k) sum[0] += v[i][k];
+    }
+    if (first + step < a.N) fetch(n + step);
+    row_sums<kGroup>(sum, sums[0]);
+    const float mean = sum[0] * inv;
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const bool mine = at.lane + i * at.lanes < nv;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[i][k] -= mean;
+        if (mine) sum[0] = fmaf(v[i][k], v[i][k], sum[0]);
+      }
+    }
+    row_sums<kGroup>(sum, sums[1]);
+    const float rstd = 1.0f / sqrtf(sum[0] * inv + a.eps);
+    if (n >= a.N) continue;
+    if (a.saved && at.lane == 0) *reinterpret_cast<f32x2*>(a.saved + 2 * n) = f32x2{mean, rstd};
+    T* y = static_cast<T*>(a.out) + n * a.ldout;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = at.lane + i * at.lanes;
+      if (c >= nv) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = fmaf(v[i][k] * rstd, w[i][k], b[i][k]);
+      store8<true>(y + 8 * c, v[i]);
+    }
   }
 }
 
-template <typename T, int kGroup, int kVecs>
-__global__ __launch_bounds__(kGroup ? kThreads : kMostWaves * 64) void layer_norm_bwd_kernel(NormArgs a) {
+template <typename T, int kGroup, int kVecs, int kThreads>
+__global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(NormArgs a) {
   __shared__ float sums[2][2][kMostWaves];
   const Place<kGroup> at;
   const int nv = a.D / 8;
@@ -159,7 +171,8 @@ __global__ __launch_bounds__(kGroup ? kThreads : kMostWaves * 64) void layer_nor
   };
   const int64_t step = (int64_t)gridDim.x * at.rows;
   int64_t n = (int64_t)blockIdx.x * at.rows + at.row;
-  // the next row's loads on their way, where there are registers for them
+  // The next row's loads on their way, but for two vectors a lane, where the second
+  // row is another workgroup's (8192 x 5120: 79 us, 92 with them).
   constexpr bool kAhead = kGroup != 0 || kVecs == 1;
   if (kAhead) fetch(n);
   int turn = 0;
@@ -193,7 +206,7 @@ __global__ __launch_bounds__(kGroup ? kThreads : kMostWaves * 64) void layer_nor
       const int c = at.lane + i * at.lanes;
       rr[i] = in && c < nv ? load_raw(static_cast<const T*>(a.grad_residual) + n * a.ldgr + 8 * c) : zero_raw<T>();
     };
-    if (kAhead && a.grad_residual)
+    if (a.grad_residual)
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) fetch_residual(i);
     row_sums<kGroup>(sum, sums[turn]);
@@ -208,7 +221,6 @@ __global__ __launch_bounds__(kGroup ? kThreads : kMostWaves * 64) void layer_nor
       for (int k = 0; k < 8; ++k) y[k] = rstd * (gw[i][k] - m0 - u[i][k] * m1);
       if (a.grad_residual) {
         float r[8];
-        if (!kAhead) fetch_residual(i);
         unpack8(rr[i], r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] += r[k];
@@ -262,15 +274,22 @@ __global__ __launch_bounds__(kGroup ? kThreads : kMostWaves * 64) void layer_nor
 }
 
 // The columns of the workgroups' rows: kRedSlices threads a column, each every
-// kRedSlices-th row, then their sums in halves.
-constexpr int kRedCols = 32, kRedSlices = 16;
+// kRedSlices-th row, eight of them on their way at once, then their sums in halves.
+constexpr int kRedCols = 32, kRedSlices = 32, kRedAhead = 8;
 __global__ __launch_bounds__(kRedCols * kRedSlices) void layer_norm_reduce_kernel(const float* partial, float* dw, float* db,
                                                                                   int rows, int D) {
   __shared__ float part[kRedSlices][kRedCols];
   const int at = threadIdx.x % kRedCols, slice = threadIdx.x / kRedCols, col = blockIdx.x * kRedCols + at;
   float s = 0.0f;
   if (col < 2 * D)
-    for (int r = slice; r < rows; r += kRedSlices) s += partial[(int64_t)r * 2 * D + col];
+    for (int r = slice; r < rows; r += kRedSlices * kRedAhead) {
+      float v[kRedAhead];
+#pragma unroll
+      for (int i = 0; i < kRedAhead; ++i)
+        v[i] = r + i * kRedSlices < rows ? partial[(int64_t)(r + i * kRedSlices) * 2 * D + col] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kRedAhead; ++i) s += v[i];
+    }
   part[slice][at] = s;
   __syncthreads();
   for (int half = kRedSlices / 2; half >= 1; half /= 2) {
@@ -288,24 +307,26 @@ struct NormKernels {
   int threads, rows;  // of a workgroup
 };
 
-template <typename T, int kGroup, int kVecs>
-NormKernels norm_of(int threads, int rows) {
-  return {(const void*)&layer_norm_fwd_kernel<T, kGroup, kVecs>, (const void*)&layer_norm_bwd_kernel<T, kGroup, kVecs>, threads,
-          rows};
+template <typename T, int kGroup, int kVecs, int kMost>
+NormKernels norm_of(int threads) {
+  return {(const void*)&layer_norm_fwd_kernel<T, kGroup, kVecs, kMost>,
+          (const void*)&layer_norm_bwd_kernel<T, kGroup, kVecs, kMost>, threads, kGroup ? threads / (kGroup ? kGroup : 1) : 1};
 }
 
-// The narrowest group of lanes that a row fits, a vector a lane (two where a
-// wave, or the largest workgroup, does not reach).
+// The narrowest group of lanes that a row fits, a vector a lane; two vectors where
+// that is a workgroup of up to eight waves.  (8192 x 5120, 640 threads of one vector:
+// forward 33.6 us and backward 83.4 against 29.8 and 79.0 with 320 of two.)
 template <typename T>
 NormKernels norm_kernels_of(int D) {
   const int nv = D / 8;
-  if (nv <= 8) return norm_of<T, 8, 1>(kThreads, kThreads / 8);
-  if (nv <= 16) return norm_of<T, 16, 1>(kThreads, kThreads / 16);
-  if (nv <= 32) return norm_of<T, 32, 1>(kThreads, kThreads / 32);
-  if (nv <= 64) return norm_of<T, 64, 1>(kThreads, kThreads / 64);
-  if (nv <= 128) return norm_of<T, 64, 2>(kThreads, kThreads / 64);
-  const int vecs = nv <= kMostWaves * 64 ? 1 : 2, threads = ((nv + vecs - 1) / vecs + 63) / 64 * 64;
-  return vecs == 1 ? norm_of<T, 0, 1>(threads, 1) : norm_of<T, 0, 2>(threads, 1);
+  if (nv <= 8) return norm_of<T, 8, 1, kRowThreads>(kRowThreads);
+  if (nv <= 16) return norm_of<T, 16, 1, kRowThreads>(kRowThreads);
+  if (nv <= 32) return norm_of<T, 32, 1, kRowThreads>(kRowThreads);
+  if (nv <= 64) return norm_of<T, 64, 1, kRowThreads>(kRowThreads);
+  if (nv <= 128) return norm_of<T, 64, 2, kRowThreads>(kRowThreads);
+  if (nv <= 256) return norm_of<T, 0, 1, 256>((nv + 63) / 64 * 64);
+  const int threads = ((nv + 1) / 2 + 63) / 64 * 64;
+  return norm_of<T, 0, 2, kMostWaves * 64>(threads);
 }
 
 NormKernels norm_kernels(int dtype, int D) {
@@ -314,7 +335,12 @@ NormKernels norm_kernels(int dtype, int D) {
   return norm_kernels_of<float>(D);
 }
 
-// Workgroups of the backward: each leaves a row of dw and db.
+// Workgroups.  Forward: as many as fit the chip, four a CU with 320 threads (8192 x
+// 5120: 27.7 us, 6.1 TB/s; 29.8 with 1536).  Backward: each leaves a row of dw and
+// db; two a CU, which all run at once in even shares (8192 x 5120 with residual: 79 us,
+// 4.2 TB/s; 84.5 with 448, 93 with 384, and 96 to 110 with 576 to 768, whose last ones
+// come after the others).
+constexpr int64_t kFwdBlocks = 1024;
 constexpr int64_t kBwdBlocks = 512;
 int64_t bwd_blocks(int64_t N, int rows) {
   const int64_t all = (N + rows - 1) / rows;
@@ -333,7 +359,9 @@ hipError_t launch_layer_norm_fwd(const NormCall& c, hipStream_t stream) {
   a.N = c.N; a.ldx = c.ldx; a.ldout = c.ldy; a.D = (int)c.D; a.eps = c.eps;
   const NormKernels k = norm_kernels(c.dtype, a.D);
   void* args[] = {&a};
-  return hipLaunchKernel(k.fwd, dim3((unsigned)((c.N + k.rows - 1) / k.rows)), dim3((unsigned)k.threads), args, 0, stream);
+  const int64_t blocks = (c.N + k.rows - 1) / k.rows;
+  return hipLaunchKernel(k.fwd, dim3((unsigned)(blocks < kFwdBlocks ? blocks : kFwdBlocks)), dim3((unsigned)k.threads), args, 0,
+                         stream);
 }
 
 hipError_t launch_layer_norm_bwd(const NormCall& c, hipStream_t stream) {

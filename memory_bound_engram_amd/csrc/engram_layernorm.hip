@@ -172,7 +172,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(NormArgs a) {
   const int64_t step = (int64_t)gridDim.x * at.rows;
   int64_t n = (int64_t)blockIdx.x * at.rows + at.row;
   // The next row's loads on their way, but for two vectors a lane, where the second
-  // row is another workgroup's (8192 x 5120: 79 us, 92 with them).
+  // row is another workgroup's (8192 x 5120: 79 us, 92 with them, both before the
+  // residual's loads were sent early).
   constexpr bool kAhead = kGroup != 0 || kVecs == 1;
   if (kAhead) fetch(n);
   int turn = 0;
@@ -206,7 +207,8 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(NormArgs a) {
       const int c = at.lane + i * at.lanes;
       rr[i] = in && c < nv ? load_raw(static_cast<const T*>(a.grad_residual) + n * a.ldgr + 8 * c) : zero_raw<T>();
     };
-    if (a.grad_residual)
+    constexpr bool kLate = kVecs == 2 && sizeof(T) == 4;  // no registers to have these on their way
+    if (!kLate && a.grad_residual)
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) fetch_residual(i);
     row_sums<kGroup>(sum, sums[turn]);
@@ -221,6 +223,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(NormArgs a) {
       for (int k = 0; k < 8; ++k) y[k] = rstd * (gw[i][k] - m0 - u[i][k] * m1);
       if (a.grad_residual) {
         float r[8];
+        if (kLate) fetch_residual(i);
         unpack8(rr[i], r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] += r[k];
@@ -314,7 +317,7 @@ NormKernels norm_of(int threads) {
 }
 
 // The narrowest group of lanes that a row fits, a vector a lane; two vectors where
-// that is a workgroup of up to eight waves.  (8192 x 5120, 640 threads of one vector:
+// that is a workgroup of more than four waves.  (8192 x 5120, 640 threads of one vector:
 // forward 33.6 us and backward 83.4 against 29.8 and 79.0 with 320 of two.)
 template <typename T>
 NormKernels norm_kernels_of(int D) {
@@ -337,9 +340,9 @@ NormKernels norm_kernels(int dtype, int D) {
 
 // Workgroups.  Forward: as many as fit the chip, four a CU with 320 threads (8192 x
 // 5120: 27.7 us, 6.1 TB/s; 29.8 with 1536).  Backward: each leaves a row of dw and
-// db; two a CU, which all run at once in even shares (8192 x 5120 with residual: 79 us,
-// 4.2 TB/s; 84.5 with 448, 93 with 384, and 96 to 110 with 576 to 768, whose last ones
-// come after the others).
+// db; two a CU, which all run at once in even shares (8192 x 5120 with residual: 70 us,
+// 4.8 TB/s; before the residual's loads were sent ahead of the sums 79, with 448
+// workgroups 84.5, 384: 93, and 576 to 768, whose last ones come after the others, 96 to 110).
 constexpr int64_t kFwdBlocks = 1024;
 constexpr int64_t kBwdBlocks = 512;
 int64_t bwd_blocks(int64_t N, int rows) {

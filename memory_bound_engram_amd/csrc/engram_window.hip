@@ -12,8 +12,9 @@
 // Mapping.  The rows of a sequence and key head are its (token, query head) pairs,
 // token after token, so that a narrow window, a short sequence or a few heads
 // still make whole tiles.  A workgroup of four waves takes 128 rows, a wave 32;
-// the keys that any of them sees, first the sinks that lie before the window,
-// come through LDS in tiles of 64, straight from memory, one tile ahead.  Scores
+// the keys that any of them sees, first the sinks that lie before the window
+// and then, without a gap, the window, come through LDS in tiles of 64, straight from
+// memory, one tile ahead.  Scores
 // are computed transposed, so a lane has one row, and rows and columns of the
 // softmax stay where the products leave them: its maximum and sum are a lane's own,
 // and the weights, rounded, are the next product's operand without going through
@@ -114,19 +115,31 @@ __device__ __forceinline__ void keep_seen(f32x16& s, int t, int start, int end, 
 // in fp16 are far from its largest value.
 constexpr float kSlack = 8.0f;
 
-// The keys of a run of tokens, as tiles of kKeys: the sinks before the window, then the window.
+// The keys of a run of tokens, as tiles of kKeys: first the sinks before the window,
+// then the window, without a gap.  So the last sinks may lie in the window's first
+// tile: as its first `mixed` rows, which stand for tokens just before the window.
 struct KeyTiles {
-  int sinks, from, to, n_sinks, n;  // the window is from .. to
+  int sinks, from, to, full, mixed, n;  // the window is from .. to; `full` tiles hold sinks alone
   __device__ __forceinline__ KeyTiles(int first, int last, int W, int S) {
     from = first - W + 1 > 0 ? first - W + 1 : 0;
     to = last + 1;
     sinks = S < from ? S : from;
     if (sinks == from) sinks = from = 0;  // they meet
-    n_sinks = (sinks + kKeys - 1) / kKeys;
-    n = n_sinks + (to - from + kKeys - 1) / kKeys;
+    full = sinks / kKeys;
+    mixed = sinks % kKeys;
+    n = (sinks + to - from + kKeys - 1) / kKeys;
   }
-  __device__ __forceinline__ int start(int i) const { return i < n_sinks ? i * kKeys : from + (i - n_sinks) * kKeys; }
-  __device__ __forceinline__ int end(int i) const { return i < n_sinks ? sinks : to; }  // of the run the tile is in
+  // The token that a tile's first row is or stands for, and the end of the run that it is in.
+  __device__ __forceinline__ int start(int i) const { return i < full ? i * kKeys : from - mixed + (i - full) * kKeys; }
+  __device__ __forceinline__ int end(int i) const { return i < full ? sinks : to; }
+  __device__ __forceinline__ bool mix(int i) const { return i == full && mixed; }
+  // What stands in a tile for tokens before this is seen by all rows.
+  __device__ __forceinline__ int below(int i, int S) const { return mix(i) ? from : S; }
+  // The token of a tile's row, or -1.
+  __device__ __forceinline__ int token(int i, int row) const {
+    const int j = start(i) + row;
+    return mix(i) && row < mixed ? i * kKeys + row : j < end(i) ? j : -1;
+  }
 };
 
 // A workgroup's rows of a sequence and key head.
@@ -228,6 +241,21 @@ __device__ __forceinline__ void store_rows(const uint16_t* mine, const RowTile& 
   }
 }
 
+// The q-th pieces of tile i of the keys (or values) from `src` on, the sequence's
+// first; kMix: where sinks and window may meet in it.
+template <bool kMix, typename P>
+__device__ __forceinline__ void fetch_keys(const P& pieces, int q, const uint16_t* tile, const uint16_t* src, int64_t ld,
+                                           const KeyTiles& keys, int i, int D, uint32_t at, uint32_t wave) {
+  const int start = keys.start(i), n = keys.end(i) - start;
+  if (kMix && keys.mix(i)) {
+    const uint64_t some = __ballot((int)pieces.row + q * pieces.kStep < keys.mixed);
+    pieces.move_some(q, tile, src + i * kKeys * ld, ld, keys.mixed, D, at, wave, some);
+    pieces.move_some(q, tile, src + start * ld, ld, n, D, at, wave, ~some);
+  } else {
+    pieces.move(q, tile, src + start * ld, ld, n, D, at, wave);
+  }
+}
+
 // Whether they are all finite (a sum that is not finite has a term that is not).
 template <int kD>
 __device__ __forceinline__ bool finite_rows(const f32x16 (&v)[kD / 32]) {
@@ -268,16 +296,46 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   float m = -INFINITY, sum = 0.0f;
   // the x-th of a tile's loads, keys and values in turn (behind the last tile: zeros)
   constexpr int kLoads = 2 * pieces.kMoves;
-  const auto fetch = [&](int x, int i) {
-    const int start = keys.start(i), n = keys.end(i) - start;
-    const int64_t token = r.base + start, col = (int64_t)r.head * a.D;
-    if (x % 2 == 0) pieces.move(x / 2, lds[i & 1], a.k + token * a.ldk + col, a.ldk, n, a.D, k_at, wave);
-    else pieces.move(x / 2, lds[2 + i % 3], a.v + token * a.ldv + col, a.ldv, n, a.D, v_at, wave);
+  // (sinks and window meet in one of the first two, if at all)
+  static_assert(ENGRAM_WINDOW_SINKS_MAX <= 2 * kKeys, "");
+  const uint16_t* const k0 = a.k + r.base * a.ldk + (int64_t)r.head * a.D;
+  const uint16_t* const v0 = a.v + r.base * a.ldv + (int64_t)r.head * a.D;
+  const auto fetch = [&](int x, int i, int slot, auto early) {
+    constexpr bool kMix = decltype(early)::value;
+    if (x % 2 == 0) fetch_keys<kMix>(pieces, x / 2, lds[slot % 2], k0, a.ldk, keys, i, a.D, k_at, wave);
+    else fetch_keys<kMix>(pieces, x / 2, lds[2 + slot % 3], v0, a.ldv, keys, i, a.D, v_at, wave);
   };
   // Operands on their way from LDS: of the next half's scores, and of this half's values.
   constexpr int kX = kD / 16;  // products of a half's scores, and of its values
   u32x4 kf[kX], vf[kX];
-  const auto read_keys = [&](lds_bytes tk, int u, int x) { kf[x] = rows(tk, 32 * u, x); };
+  // Tile i's keys lie in place i % 2, its values in place i % 3; the loop goes round
+  // both in six steps, so that an operand's place is a constant behind an address
+  // that stays in a register.
+  constexpr int kRound = 6, kTile = kKeys * kD * 2;
+  typedef __attribute__((address_space(3))) const u32x4* lds_words;
+  uint32_t k_from[kX], v_from[2][kD / 32];
+#pragma unroll
+  for (int x = 0; x < kX; ++x) {
+    k_from[x] = (uint32_t)(uintptr_t)lds_of(lds[0]) + rows.at + ((32 * x) ^ rows.swap);
+    asm volatile("" : "+v"(k_from[x]));  // or it takes a register for each sum with a constant
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt) {
+      v_from[n][dt] = (uint32_t)(uintptr_t)lds_of(lds[2]) + columns.at[n][dt];
+      asm volatile("" : "+v"(v_from[n][dt]));
+    }
+  const auto read_keys = [&](int slot, int u, int x) {
+    kf[x] = *(lds_words)(lds_bytes)(uintptr_t)(k_from[x] + slot % 2 * kTile + u * kTile / 2);
+  };
+  const auto read_values = [&](int slot, int u, int x) {
+    const uint32_t at = slot % 3 * kTile + (u * 2 + x / (kD / 32)) * kTile / 4;
+    const lds_bytes lo = (lds_bytes)(uintptr_t)(v_from[0][x % (kD / 32)] + at), hi = (lds_bytes)(uintptr_t)(v_from[1][x % (kD / 32)] + at);
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)lo));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)hi));
+    vf[x] = u32x4{a[0], a[1], b[0], b[1]};
+  };
   const auto largest = [&](const f32x16& s) {
     float top = s[0];
 #pragma unroll
@@ -286,9 +344,9 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   };
   // what rows do not see goes; the maximum, and what there is in its terms
   const auto settle = [&](f32x16& s, float top, int i, int u) {
-    const int start = keys.start(i) + 32 * u, end = keys.end(i);
-    if (start + 32 > end || start + 31 > first || !(start > last - a.W || start + 32 <= a.S)) {
-      keep_seen(s, t, start + 4 * (int)h, end, a.W, a.S, -INFINITY);
+    const int start = keys.start(i) + 32 * u, end = keys.end(i), below = keys.below(i, a.S);
+    if (start + 32 > end || start + 31 > first || !(start > last - a.W || start + 32 <= below)) {
+      keep_seen(s, t, start + 4 * (int)h, end, a.W, below, -INFINITY);
       top = largest(s);
     }
     if (__any((top - m) * c > kSlack)) {
@@ -305,11 +363,10 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   // values, beside which the next scores' maximum is found.  Each product is sent
   // with what goes on beside it, in this order: left to itself the compiler reads
   // each operand just before its product and makes the weights in one go.
-  const auto step = [&](f32x16& s, f32x16& next, int i, auto half, auto more) {
+  const auto step = [&](f32x16& s, f32x16& next, int i, int slot, auto half, auto more) __attribute__((always_inline)) {
     constexpr int u = decltype(half)::value, kEach = 16 / kX;
     constexpr bool kNext = decltype(more)::value;
     static_assert(kLoads == kX, "a load beside each product");
-    const lds_bytes tv = opaque(lds_of(lds[2 + i % 3])), tk = opaque(lds_of(lds[(i + 1) & 1]));
     const float less = m == -INFINITY ? 0.0f : -m * c;
     u32x4 p[2];
     next = f32x16{};
@@ -325,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       if constexpr (kNext) next = product<T>(kf[x], q[x], next);
-      vf[x] = columns(tv, 32 * u + 16 * (x / (kD / 32)), x % (kD / 32));
+      read_values(slot, u, x);
       weigh(x * kEach / 2, kEach / 2);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -336,8 +393,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       __builtin_amdgcn_sched_barrier(0);
       o[x % (kD / 32)] = product<T>(vf[x], p[x / (kD / 32)], o[x % (kD / 32)]);
       // (behind the last tile these read what lies there, for no one)
-      if constexpr (kNext) read_keys(tk, u, x);
-      if constexpr (u == 0) fetch(x, i + 2);
+      if constexpr (kNext) read_keys(slot + 1, u, x);
+      if constexpr (u == 0) fetch(x, i + 2, slot + 2, std::false_type{});
       if (x < kX / 2) {
         weigh(8 + x * kEach, kEach);
       } else if constexpr (kNext) {
@@ -361,27 +418,31 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       return (int)(32 * wave + row) < r.rows ? t * (uint32_t)(a.ldq * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
     });
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) fetch(x, 0);
+    for (int x = 0; x < kLoads; ++x) fetch(x, 0, 0, std::true_type{});
 #pragma unroll
-    for (int x = 0; x < kLoads; x += 2) fetch(x, 1);
+    for (int x = 0; x < kLoads; x += 2) fetch(x, 1, 1, std::true_type{});
     meet();
 #pragma unroll
     for (int x = 0; x < kX; ++x) q[x] = rows(lds_of(mine), 0, x);
     meet();
 #pragma unroll
-    for (int x = 1; x < kLoads; x += 2) fetch(x, 1);
+    for (int x = 1; x < kLoads; x += 2) fetch(x, 1, 1, std::true_type{});
   }
   f32x16 s0 = f32x16{}, s1;
 #pragma unroll
   for (int x = 0; x < kX; ++x) s0 = product<T>(rows(lds_of(lds[0]), 0, x), q[x], s0);
 #pragma unroll
-  for (int x = 0; x < kX; ++x) read_keys(lds_of(lds[0]), 1, x);
+  for (int x = 0; x < kX; ++x) read_keys(0, 1, x);
   settle(s0, largest(s0), 0, 0);
-  for (int i = 0; i < keys.n; ++i) {
-    step(s0, s1, i, first_half, std::true_type{});
-    if (i + 1 < keys.n) step(s1, s0, i, second_half, std::true_type{});
+  for (int i = 0; i < keys.n;) {
+#pragma unroll
+    for (int slot = 0; slot < kRound; ++slot) {
+      step(s0, s1, i, slot, first_half, std::true_type{});
+      if (++i >= keys.n) break;
+      step(s1, s0, i - 1, slot, second_half, std::true_type{});
+    }
   }
-  step(s1, s0, keys.n - 1, second_half, std::false_type{});
+  step(s1, s0, keys.n - 1, (keys.n - 1) % kRound, second_half, std::false_type{});
   sum = column_sum(sum);
   const float inverse = 1.0f / sum;
   if (a.lse && there && h == 0) a.lse[(r.base + t) * (int64_t)(a.Hk * a.G) + head] = fmaf(m, c, __log2f(sum)) * kLn2;
@@ -399,13 +460,13 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
     const uint16_t* qx = a.q + (r.base + tx) * a.ldq + (int64_t)hx * a.D;
     float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
     for (int i = 0; i < keys.n; ++i) {
-      const int j = keys.start(i) + (int)lane;
-      const bool seen = j < keys.end(i) && sees(tx, j, a.W, a.S);
+      const int j = keys.token(i, (int)lane);
+      const bool seen = j >= 0 && sees(tx, j, a.W, a.S);
       const float s = seen ? dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D) : 0.0f;
       const float p = __builtin_amdgcn_exp2f((s - mx) * c) * ix;
       for (uint64_t left = __ballot(seen); left; left &= left - 1) {
         const int n = __builtin_ctzll(left);
-        const uint16_t* vx = a.v + (r.base + keys.start(i) + n) * a.ldv + (int64_t)r.head * a.D;
+        const uint16_t* vx = a.v + (r.base + __shfl(j, n)) * a.ldv + (int64_t)r.head * a.D;
         const float pn = __shfl(p, n);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -452,11 +513,14 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   const KeyTiles keys(first, last, a.W, a.S);
   const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
   const uint32_t k_at = pieces.offset(a.ldk, a.D), v_at = pieces.offset(a.ldv, a.D);
+  const uint16_t* const k0 = a.k + r.base * a.ldk + (int64_t)r.head * a.D;
+  const uint16_t* const v0 = a.v + r.base * a.ldv + (int64_t)r.head * a.D;
   const auto fetch = [&](int i) {
-    const int start = keys.start(i), n = keys.end(i) - start;
-    const int64_t token = r.base + start, col = (int64_t)r.head * a.D;
-    pieces.fetch(lds[i & 1][0], a.k + token * a.ldk + col, a.ldk, n, a.D, k_at, wave);
-    pieces.fetch(lds[i & 1][1], a.v + token * a.ldv + col, a.ldv, n, a.D, v_at, wave);
+#pragma unroll
+    for (int q = 0; q < pieces.kMoves; ++q) {
+      fetch_keys<true>(pieces, q, lds[i & 1][0], k0, a.ldk, keys, i, a.D, k_at, wave);
+      fetch_keys<true>(pieces, q, lds[i & 1][1], v0, a.ldv, keys, i, a.D, v_at, wave);
+    }
   };
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
@@ -469,8 +533,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
     meet();
     if (i + 1 < keys.n) fetch(i + 1);
     const lds_bytes tk = lds_of(lds[i & 1][0]), tv = lds_of(lds[i & 1][1]);
-    const int start = keys.start(i), end = keys.end(i);
-    const bool some = start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= a.S);
+    const int start = keys.start(i), end = keys.end(i), below = keys.below(i, a.S);
+    const bool some = start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= below);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x16 s = f32x16{}, d = f32x16{};
@@ -480,7 +544,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
       for (int kk = 0; kk < kD / 16; ++kk) d = product<T>(rows(tv, 32 * u, kk), go[kk], d);
 #pragma unroll
       for (int e = 0; e < 16; ++e) d[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse)) * (d[e] - delta);
-      if (some) keep_seen(d, t, start + 32 * u + 4 * (int)h, end, a.W, a.S, 0.0f);
+      if (some) keep_seen(d, t, start + 32 * u + 4 * (int)h, end, a.W, below, 0.0f);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const u32x4 p = operand<T>(d, w);
@@ -503,8 +567,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
     const uint16_t* gx = a.grad_o + (r.base + tx) * a.ldgo + (int64_t)hx * a.D;
     float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
     for (int i = 0; i < keys.n; ++i) {
-      const int j = keys.start(i) + (int)lane;
-      const bool seen = j < keys.end(i) && sees(tx, j, a.W, a.S);
+      const int j = keys.token(i, (int)lane);
+      const bool seen = j >= 0 && sees(tx, j, a.W, a.S);
       float d = 0.0f;
       if (seen) {
         const float s = dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D);
@@ -513,7 +577,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
       }
       for (uint64_t left = __ballot(seen); left; left &= left - 1) {
         const int n = __builtin_ctzll(left);
-        const uint16_t* kx = a.k + (r.base + keys.start(i) + n) * a.ldk + (int64_t)r.head * a.D;
+        const uint16_t* kx = a.k + (r.base + __shfl(j, n)) * a.ldk + (int64_t)r.head * a.D;
         const float dn = __shfl(d, n);
 #pragma unroll
         for (int e = 0; e < 2; ++e)

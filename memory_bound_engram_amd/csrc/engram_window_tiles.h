@@ -119,6 +119,16 @@ struct ColumnReader {
   }
 };
 
+// load_to_lds by some of the lanes (all are at work here); the others' places stay as they are.
+__device__ __forceinline__ void load_some_to_lds(uint32_t to, u32x4 src, uint32_t off, uint64_t lanes) {
+  uint64_t all;
+  asm volatile("s_mov_b64 %0, exec\n\ts_mov_b32 m0, %1\n\ts_mov_b64 exec, %4\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+               "s_mov_b64 exec, %0"
+               : "=&s"(all)
+               : "s"(to), "v"(off), "s"(src), "s"(lanes)
+               : "memory");
+}
+
 // The pieces of a tile that a lane of kThreads moves: the q-th lies at
 // (q kThreads + thread) 16 bytes of the tile.
 template <int kD, int kRows, int kThreads>
@@ -141,9 +151,20 @@ struct Pieces {
   // the q-th pieces; `at`: the above.  No vector instruction but the load.
   __device__ __forceinline__ void move(int q, const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,
                                        uint32_t wave) const {
+    load_to_lds(lds_place(q, tile, wave), words_of(q, src, ld, n, D), at);
+  }
+  // Those of the lanes in `some`.
+  __device__ __forceinline__ void move_some(int q, const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D,
+                                            uint32_t at, uint32_t wave, uint64_t some) const {
+    load_some_to_lds(lds_place(q, tile, wave), words_of(q, src, ld, n, D), at, some);
+  }
+  static __device__ __forceinline__ uint32_t lds_place(int q, const uint16_t* tile, uint32_t wave) {
+    return (uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024 + q * kThreads * 16;
+  }
+  static __device__ __forceinline__ u32x4 words_of(int q, const uint16_t* src, int64_t ld, int n, int D) {
     u32x4 words = buffer_words(src + (int64_t)(q * kStep) * ld);
     words[2] = n > q * kStep ? (uint32_t)(n - q * kStep - 1) * (uint32_t)(ld * 2) + (uint32_t)(D * 2) : 0;
-    load_to_lds((uint32_t)(uintptr_t)(lds_ptr)tile + wave * 1024 + q * kThreads * 16, words, at);
+    return words;
   }
   __device__ __forceinline__ void fetch(const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,
                                         uint32_t wave) const {

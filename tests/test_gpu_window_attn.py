@@ -182,6 +182,11 @@ def test_long(gpu, window, sinks):
     check_all(case([2500, 700], 4, 2, 128, BF, gpu, window, sinks, seed=4), gpu)
 
 
+@pytest.mark.parametrize("sinks", [1, 63, 64, 65, 127, 128])
+def test_sinks_and_window_in_one_tile(gpu, sinks):
+    check_all(case([400, 190], 4, 2, 72, BF, gpu, 30, sinks, seed=7), gpu)
+
+
 def test_peaked_and_even_weights(gpu):
     for std in (0.0, 40.0):
         check_all(case([200], 2, 1, 64, BF, gpu, 64, 2, std=std, seed=5), gpu)

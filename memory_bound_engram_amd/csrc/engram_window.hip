@@ -447,7 +447,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   const float inverse = 1.0f / sum;
   if (a.lse && there && h == 0) a.lse[(r.base + t) * (int64_t)(a.Hk * a.G) + head] = fmaf(m, c, __log2f(sum)) * kLn2;
 
-  __syncthreads();  // the tiles are read out
+  meet();  // the tiles are read out, and what was fetched behind the last one is there
   uint16_t* mine = lds[0] + wave * 32 * kD;
   put_rows<T, kD>(mine, o, inverse, lane);
   // rows that are not finite though their weights are, by the definition

@@ -480,7 +480,9 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   store_rows<kD>(mine, r, wave, lane, a);
 }
 
-// dq of 128 rows, and delta.
+// dq of 128 rows, and delta.  Half a tile at a time: its scores, its values times the
+// rows of grad_o, beside which the weights are made, and d times its keys.  Each
+// operand is read four products ahead.
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kKeys * kD];  // [turn][keys, values]
@@ -515,11 +517,11 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   const uint32_t k_at = pieces.offset(a.ldk, a.D), v_at = pieces.offset(a.ldv, a.D);
   const uint16_t* const k0 = a.k + r.base * a.ldk + (int64_t)r.head * a.D;
   const uint16_t* const v0 = a.v + r.base * a.ldv + (int64_t)r.head * a.D;
-  const auto fetch = [&](int i) {
+  const auto fetch = [&](int i, int slot) {
 #pragma unroll
     for (int q = 0; q < pieces.kMoves; ++q) {
-      fetch_keys<true>(pieces, q, lds[i & 1][0], k0, a.ldk, keys, i, a.D, k_at, wave);
-      fetch_keys<true>(pieces, q, lds[i & 1][1], v0, a.ldv, keys, i, a.D, v_at, wave);
+      fetch_keys<true>(pieces, q, lds[slot][0], k0, a.ldk, keys, i, a.D, k_at, wave);
+      fetch_keys<true>(pieces, q, lds[slot][1], v0, a.ldv, keys, i, a.D, v_at, wave);
     }
   };
   const RowReader<kD> rows(lane);
@@ -528,29 +530,89 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   f32x16 dq[kD / 32];
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) dq[dt] = f32x16{};
-  fetch(0);
+  // Places as constants behind addresses that stay in registers, as in the forward; they go
+  // to and fro between the two tiles' places.
+  constexpr int kX = kD / 16, kEach = 16 / kX, kRing = 4, kTile = kKeys * kD * 2;
+  typedef __attribute__((address_space(3))) const u32x4* lds_words;
+  uint32_t by_row[kX], by_column[2][kD / 32];
+#pragma unroll
+  for (int x = 0; x < kX; ++x) {
+    by_row[x] = (uint32_t)(uintptr_t)lds_of(lds[0][0]) + rows.at + ((32 * x) ^ rows.swap);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt) {
+      by_column[n][dt] = (uint32_t)(uintptr_t)lds_of(lds[0][0]) + columns.at[n][dt];
+    }
+  fetch(0, 0);
   for (int i = 0; i < keys.n; ++i) {
     meet();
-    if (i + 1 < keys.n) fetch(i + 1);
-    const lds_bytes tk = lds_of(lds[i & 1][0]), tv = lds_of(lds[i & 1][1]);
-    const int start = keys.start(i), end = keys.end(i), below = keys.below(i, a.S);
-    const bool some = start + kKeys > end || start + kKeys - 1 > first || !(start > last - a.W || start + kKeys <= below);
+    if (i + 1 < keys.n) fetch(i + 1, (i + 1) & 1);
+#pragma unroll
+    for (int x = 0; x < kX; ++x) asm volatile("" : "+v"(by_row[x]), "+v"(by_column[x / (kD / 32)][x % (kD / 32)]));
+    u32x4 f[kRing];
+    // the n-th operand of the tile
+    const auto read = [&](int n) {
+      if (n >= 6 * kX) return;
+      const int u = n / (3 * kX), side = n / kX % 3, x = n % kX;
+      if (side < 2) {
+        f[n % kRing] = *(lds_words)(lds_bytes)(uintptr_t)(by_row[x] + side * kTile + u * kTile / 2);
+      } else {
+        const uint32_t at = (u * 2 + x / (kD / 32)) * kTile / 4;
+        const lds_bytes lo = (lds_bytes)(uintptr_t)(by_column[0][x % (kD / 32)] + at);
+        const lds_bytes hi = (lds_bytes)(uintptr_t)(by_column[1][x % (kD / 32)] + at);
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)lo));
+        const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)hi));
+        f[n % kRing] = u32x4{y[0], y[1], z[0], z[1]};
+      }
+    };
+#pragma unroll
+    for (int n = 0; n < kRing; ++n) read(n);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      const int at = u * 3 * kX;
       f32x16 s = f32x16{}, d = f32x16{};
 #pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) s = product<T>(rows(tk, 32 * u, kk), q[kk], s);
-#pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) d = product<T>(rows(tv, 32 * u, kk), go[kk], d);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) d[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse)) * (d[e] - delta);
-      if (some) keep_seen(d, t, start + 32 * u + 4 * (int)h, end, a.W, below, 0.0f);
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const u32x4 p = operand<T>(d, w);
-#pragma unroll
-        for (int dt = 0; dt < kD / 32; ++dt) dq[dt] = product<T>(columns(tk, 32 * u + 16 * w, dt), p, dq[dt]);
+      for (int x = 0; x < kX; ++x) {
+        __builtin_amdgcn_sched_barrier(0);
+        s = product<T>(f[x % kRing], q[x], s);
+        read(at + x + kRing);
       }
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        __builtin_amdgcn_sched_barrier(0);
+        d = product<T>(f[x % kRing], go[x], d);
+        read(at + kX + x + kRing);
+#pragma unroll
+        for (int m = x * kEach; m < (x + 1) * kEach; ++m) s[m] = __builtin_amdgcn_exp2f(fmaf(s[m], c, -lse));
+      }
+      asm volatile("" : "+v"(s));  // or it moves behind the branch, away from the products
+      __builtin_amdgcn_sched_barrier(0);
+      const int start = keys.start(i) + 32 * u, end = keys.end(i), below = keys.below(i, a.S);
+      const bool some = start + 32 > end || start + 31 > first || !(start > last - a.W || start + 32 <= below);
+      if (some) keep_seen(s, t, start + 4 * (int)h, end, a.W, below, 0.0f);
+      u32x4 e[2];
+      const auto differ = [&](int from, int n) {
+#pragma unroll
+        for (int m = from; m < from + n; ++m) d[m] = s[m] * (d[m] - delta);
+        if ((from + n) % 8 == 0) e[(from + n) / 8 - 1] = operand<T>(d, (from + n) / 8 - 1);
+      };
+      differ(0, 8);
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        __builtin_amdgcn_sched_barrier(0);
+        dq[x % (kD / 32)] = product<T>(f[x % kRing], e[x / (kD / 32)], dq[x % (kD / 32)]);
+        read(at + 2 * kX + x + kRing);
+        if (x < kX / 2) differ(8 + x * kEach, kEach);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t turn = i & 1 ? -2 * kTile : 2 * kTile;
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      by_row[x] += turn;
+      by_column[x / (kD / 32)][x % (kD / 32)] += turn;
     }
   }
 
@@ -632,9 +694,10 @@ __device__ __forceinline__ void define_key(float (&y)[2], const WindowArgs& a, i
   }
 }
 
-// dk and dv of 128 keys.  The first a.sink_blocks workgroups make the part of the
-// sinks (the first keys of a sequence) that comes from the rows of one piece of it
-// that see them as sinks; the others take the rows whose window the keys are in.  Four
+// dk and dv of 128 keys, of the rows whose window they are in.  The last
+// a.sink_blocks workgroups make the part of the sinks (the first keys of a sequence)
+// that comes from the rows of one piece of it that see them as sinks: they are
+// short, and so fill the CUs that the last of the others leave free.  Four
 // waves have 32 keys each for the first half of a tile of rows, four the same keys for
 // the second; at the end they exchange what they have, and the first four leave
 // dk, the others dv.  Keys and values stay in LDS: in registers they would leave
@@ -650,8 +713,9 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   __shared__ __attribute__((aligned(16))) float lses[2][kKeys], deltas[2][kKeys];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5, quarter = wave & 3, half = wave >> 2;
-  const bool sinks = (int)blockIdx.x < a.sink_blocks;
-  const int at = sinks ? blockIdx.x : neighbours(blockIdx.x - a.sink_blocks, gridDim.x - a.sink_blocks);
+  const int wide_blocks = (int)gridDim.x - a.sink_blocks;
+  const bool sinks = (int)blockIdx.x >= wide_blocks;
+  const int at = sinks ? (int)blockIdx.x - wide_blocks : neighbours(blockIdx.x, wide_blocks);
   const int per_head = sinks ? a.sink_blocks / a.Hk : a.tiles, id = at % per_head, head = at / per_head;
   const uint32_t unit = sinks ? (uint32_t)a.piece : (uint32_t)kRows;
   const Sequence seq(a, id, 1, unit);
@@ -681,31 +745,41 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   uint16_t* const tiles = lds + 2 * kRows * kD;
 
   const Pieces<kD, kKeys, kKeyThreads> pieces(threadIdx.x);
-  const int n = ((to - from) * a.G + kKeys - 1) / kKeys;  // tiles of rows
+  // Tiles of rows: from the first token that is a multiple of their number on, then what
+  // is before it.  Workgroups that run side by side, each 128 keys further, so meet at
+  // the same rows at a time, which the XCD's L2 then fetches once for all nine that a window of 1024 reaches.
+  const int runs = to - from, ahead = sinks ? 0 : (runs - from % runs) % runs, middle = from + ahead;
+  const int n1 = ((to - middle) * a.G + kKeys - 1) / kKeys, n = n1 + (ahead * a.G + kKeys - 1) / kKeys;
   const int Hq = a.Hk * a.G;
   float lse = 0.0f, delta = 0.0f;
-  int t0 = from;      // of the next tile to fetch: its first row's token and head
+  int t0 = middle, behind = to;  // of the next tile to fetch: its first row's token and head, the end of its run
   uint32_t x0 = 0;
-  const auto fetch = [&](int i) {
-    const int64_t first = base + t0, heads = (int64_t)head * a.G * a.D;
-    const auto row_at = [&](uint32_t row, uint32_t* t, uint32_t* g) {
-      const uint32_t x = x0 + row;
-      *t = a.by_G(x);
-      *g = x - *t * (uint32_t)a.G;
-      return t0 + (int)*t < to;
-    };
-    const auto offset = [&](uint32_t row, int64_t ld) {
-      uint32_t t, g;
-      return row_at(row, &t, &g) ? t * (uint32_t)(ld * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
-    };
+  const int64_t of_head = (int64_t)head * a.G * a.D;
+  const auto row_at = [&](uint32_t row, uint32_t* t, uint32_t* g) {
+    const uint32_t x = x0 + row;
+    *t = a.by_G(x);
+    *g = x - *t * (uint32_t)a.G;
+    return t0 + (int)*t < behind;
+  };
+  // The j-th pieces of tile i's rows (none behind the last tile: zeros).
+  const auto fetch = [&](int i, int j) {
+    const int64_t first = base + t0;
+    uint32_t t, g;
+    const bool in = row_at(pieces.row + j * pieces.kStep, &t, &g) && i < n;
     uint16_t* const to_q = tiles + (i & 1) * 2 * kTile;
-    pieces.gather(to_q, a.q + first * a.ldq + heads, a.D, wave, [&](uint32_t row) { return offset(row, a.ldq); });
-    pieces.gather(to_q + kTile, a.grad_o + first * a.ldgo + heads, a.D, wave,
-                  [&](uint32_t row) { return offset(row, a.ldgo); });
+    const uint32_t at = in && pieces.col < (uint32_t)a.D ? g * (uint32_t)(a.D * 2) + pieces.col * 2 : kBeyond;
+    const uint32_t far = at == kBeyond ? 0 : t;
+    static_assert(pieces.kSame, "");
+    load_to_lds(pieces.lds_place(j, to_q, wave), buffer_words(a.q + first * a.ldq + of_head), at + far * (uint32_t)(a.ldq * 2));
+    load_to_lds(pieces.lds_place(j, to_q + kTile, wave), buffer_words(a.grad_o + first * a.ldgo + of_head),
+                at + far * (uint32_t)(a.ldgo * 2));
+  };
+  // What the first wave keeps of tile i's rows, and on to the next tile.
+  const auto fetch_sums = [&](int i) {
     if (wave == 0) {
       uint32_t t, g;
-      const bool in = row_at(lane, &t, &g);
-      const int64_t at = (first + (in ? t : 0)) * Hq + head * a.G + (in ? g : 0);
+      const bool in = row_at(lane, &t, &g) && i < n;
+      const int64_t at = (base + t0 + (in ? t : 0)) * Hq + head * a.G + (in ? g : 0);
       // a row that is not there has weights of 0
       lse = in ? a.lse_in[at] * kLog2e : INFINITY;
       delta = in ? a.delta[at] : 0.0f;
@@ -713,6 +787,16 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     x0 += kKeys;
     t0 += (int)a.by_G(x0);
     x0 -= a.by_G(x0) * (uint32_t)a.G;
+    if (i + 1 == n1) {
+      t0 = from;
+      x0 = 0;
+      behind = middle;
+    }
+  };
+  const auto fetch_all = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < pieces.kMoves; ++j) fetch(i, j);
+    fetch_sums(i);
   };
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
@@ -720,16 +804,38 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   f32x16 dk[kD / 32], dv[kD / 32];
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
-  int t_first = from;       // of this tile: as t0 and x0
+  int t_first = middle;     // of this tile: as t0 and x0
   uint32_t x_first = 0;
-  fetch(0);
+  // Places as constants behind addresses that stay in registers and go to and fro
+  // between the two tiles' places; those of keys and values in an instruction each.
+  constexpr int kBytes = kTile * 2;
+  typedef __attribute__((address_space(3))) const u32x4* lds_words;
+  uint32_t by_row[kX], by_column[2][kD / 32];
+  const uint32_t of_half = (uint32_t)(uintptr_t)lds_of(tiles) + half * kBytes / 2;
+  const uint32_t of_key = (uint32_t)(uintptr_t)lds_of(lds) + rows.at + quarter * kBytes / 2;
+#pragma unroll
+  for (int x = 0; x < kX; ++x) by_row[x] = of_half + rows.at + ((32 * x) ^ rows.swap);
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt) by_column[n][dt] = of_half + columns.at[n][dt];
+  fetch_all(0);
   for (int i = 0; i < n; ++i) {
+    const uint32_t turn = i == 0 ? 0 : i & 1 ? 2 * kBytes : -2 * kBytes;
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      by_row[x] += turn;
+      by_column[x / (kD / 32)][x % (kD / 32)] += turn;
+    }
     if (wave == 0) {
       lses[i & 1][lane] = lse;
       deltas[i & 1][lane] = delta;
     }
     meet();
-    if (i + 1 < n) fetch(i + 1);
+    if (i == n1) {
+      t_first = from;
+      x_first = 0;
+    }
     const uint32_t x = x_first + 32 * half;  // this wave's rows: heads x to x + 31 from token t_first's first on
     const int ta = t_first + (int)a.by_G(x), tb = t_first + (int)a.by_G(x + 31);
     const int t_here = t_first;
@@ -739,22 +845,35 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     x_first -= a.by_G(x_first) * (uint32_t)a.G;
     // rows lie between ta - key0 - 31 and tb - key0 tokens behind the keys
     const int least = ta - key0 - 31, most = tb - key0;
-    if (!active || most < near || (!sinks && least >= a.W)) continue;
-    const lds_bytes tq = opaque(lds_of(tiles + (i & 1) * 2 * kTile)), tg = tq + 2 * kTile, tv = lds_of(lds);
+    if (!active || most < near || (!sinks && least >= a.W)) {
+      fetch_all(i + 1);
+      continue;
+    }
     const int r0 = 32 * (int)half;
     // The operands from the tiles of rows, in the order of their products: queries and
     // gradients of o by rows, then gradients and queries by columns; four on their way.
     constexpr int kRing = 4;
-    u32x4 f[kRing], kv[2], p[2], e[2];
-    const lds_bytes tk = tv + kRows * kD * 2 + quarter * 32 * kD * 2, tw = tv + quarter * 32 * kD * 2;
+    u32x4 f[kRing], kv[kRing], p[2], e[2];
     const auto read = [&](int n) {
       const int x = n % kX, side = n / kX;
       if (side >= 4) return;
-      const lds_bytes t = (side == 0 || side == 3 ? tq : tg) + r0 * kD * 2;
-      f[n % kRing] = side < 2 ? rows(t, 0, x) : columns(t + 16 * (x / (kD / 32)) * kD * 2, 0, x % (kD / 32));
+      const int tile = side == 0 || side == 3 ? 0 : kBytes;  // queries, gradients
+      if (side < 2) {
+        f[n % kRing] = *(lds_words)(lds_bytes)(uintptr_t)(by_row[x] + tile);
+      } else {
+        const uint32_t at = tile + x / (kD / 32) * kBytes / 4;
+        const lds_bytes lo = (lds_bytes)(uintptr_t)(by_column[0][x % (kD / 32)] + at);
+        const lds_bytes hi = (lds_bytes)(uintptr_t)(by_column[1][x % (kD / 32)] + at);
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)lo));
+        const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)hi));
+        f[n % kRing] = u32x4{y[0], y[1], z[0], z[1]};
+      }
     };
+    uint32_t swap = rows.swap;
+    asm volatile("" : "+v"(swap));  // or it keeps the addresses for the next tile
     const auto read_key = [&](int n) {
-      if (n < 2 * kX) kv[n & 1] = n < kX ? rows(tk, 0, n) : rows(tw, 0, n - kX);
+      if (n >= 2 * kX) return;
+      kv[n % kRing] = *(lds_words)(lds_bytes)(uintptr_t)(of_key + ((32 * (n % kX)) ^ swap) + (n < kX ? kRows * kD * 2 : 0));
     };
     f32x16 s = f32x16{}, d = f32x16{};
     f32x4 row[2];
@@ -763,27 +882,31 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     constexpr int kEach = 16 / kX;
 #pragma unroll
     for (int n = 0; n < kRing; ++n) read(n);
-    read_key(0);
-    read_key(1);
+#pragma unroll
+    for (int n = 0; n < kRing; ++n) read_key(n);
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       __builtin_amdgcn_sched_barrier(0);
-      s = product<T>(f[x % kRing], kv[x & 1], s);
+      s = product<T>(f[x % kRing], kv[x % kRing], s);
       read(x + kRing);
-      read_key(x + 2);
+      read_key(x + kRing);
+      if (x % 2 == 1 && x / 2 < pieces.kMoves) fetch(i + 1, x / 2);
     }
+    fetch_sums(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
     read_lse(0);
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       __builtin_amdgcn_sched_barrier(0);
-      d = product<T>(f[x % kRing], kv[x & 1], d);
+      d = product<T>(f[x % kRing], kv[x % kRing], d);
       read(kX + x + kRing);
-      read_key(kX + x + 2);
+      read_key(kX + x + kRing);
       if (x * kEach % 4 == 0 && x * kEach < 12) read_lse(x * kEach / 4 + 1);
 #pragma unroll
       for (int m = x * kEach; m < (x + 1) * kEach; ++m)
         s[m] = __builtin_amdgcn_exp2f(fmaf(s[m], c, -row[m / 4 & 1][m % 4]));
     }
+    asm volatile("" : "+v"(s));  // or the weights move behind the branch, away from the products
     __builtin_amdgcn_sched_barrier(0);
     read_delta(0);
     if (least < near || (!sinks && most >= a.W) || key0 + 31 >= keys) {
@@ -820,7 +943,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   // The exchange: the first four waves' dv, then the others' dk, in the order they
   // are there for each lane.
   f32x4* const given = reinterpret_cast<f32x4*>(lds) + quarter * (kD / 8) * 64 + lane;
-  __syncthreads();  // the tiles are read out
+  meet();  // the tiles are read out, and what was fetched behind the last one is there
 #pragma unroll
   for (int turn = 0; turn < 2; ++turn) {
     if (half == (uint32_t)turn) {

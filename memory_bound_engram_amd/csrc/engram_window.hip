@@ -135,6 +135,18 @@ struct KeyTiles {
   __device__ __forceinline__ bool mix(int i) const { return i == full && mixed; }
   // What stands in a tile for tokens before this is seen by all rows.
   __device__ __forceinline__ int below(int i, int S) const { return mix(i) ? from : S; }
+  // Halves of tiles, 32 rows each, that rows of the tokens first .. last see all of: `count` from `from` on.
+  struct Whole {
+    int from;
+    uint32_t count;
+    __device__ __forceinline__ bool has(int half) const { return (uint32_t)(half - from) < count; }
+  };
+  __device__ __forceinline__ Whole whole(int first, int last, int W) const {
+    const int begin = from - mixed - full * kKeys;  // where the first tile would begin, were the sinks before it the window's
+    const int lo = last - W + 1 - begin, hi = first + 1 - begin;
+    const int at = lo > 0 ? (lo + 31) / 32 : 0, behind = hi > 0 ? hi / 32 : 0;
+    return Whole{at, behind > at ? (uint32_t)(behind - at) : 0u};
+  }
   // The token of a tile's row, or -1.
   __device__ __forceinline__ int token(int i, int row) const {
     const int j = start(i) + row;
@@ -242,12 +254,12 @@ __device__ __forceinline__ void store_rows(const uint16_t* mine, const RowTile& 
 }
 
 // The q-th pieces of tile i of the keys (or values) from `src` on, the sequence's
-// first; kMix: where sinks and window may meet in it.
-template <bool kMix, typename P>
+// first, where sinks and window may meet in it.
+template <typename P>
 __device__ __forceinline__ void fetch_keys(const P& pieces, int q, const uint16_t* tile, const uint16_t* src, int64_t ld,
                                            const KeyTiles& keys, int i, int D, uint32_t at, uint32_t wave) {
   const int start = keys.start(i), n = keys.end(i) - start;
-  if (kMix && keys.mix(i)) {
+  if (keys.mix(i)) {
     const uint64_t some = __ballot((int)pieces.row + q * pieces.kStep < keys.mixed);
     pieces.move_some(q, tile, src + i * kKeys * ld, ld, keys.mixed, D, at, wave, some);
     pieces.move_some(q, tile, src + start * ld, ld, n, D, at, wave, ~some);
@@ -255,6 +267,33 @@ __device__ __forceinline__ void fetch_keys(const P& pieces, int q, const uint16_
     pieces.move(q, tile, src + start * ld, ld, n, D, at, wave);
   }
 }
+
+// The tiles from one on that are all of the window (the third at the latest), one after
+// the other, with few scalar instructions a tile: where it begins and what is left.
+// A wave issues one instruction at a time, of any kind.
+template <typename P>
+struct Following {
+  uint64_t next;
+  uint32_t at[P::kMoves];  // of the pieces, in bytes from a tile's first row
+  uint32_t row_bytes;
+  int left;
+  __device__ __forceinline__ Following(const P& pieces, const uint16_t* src, int64_t ld, const KeyTiles& keys, int i, int D)
+      : next(reinterpret_cast<uint64_t>(src + (int64_t)keys.start(i) * ld)), row_bytes((uint32_t)(ld * 2)), left(keys.to - keys.start(i)) {
+    const uint32_t first = pieces.offset(ld, D);
+#pragma unroll
+    for (int q = 0; q < P::kMoves; ++q) at[q] = first == kBeyond ? kBeyond : first + q * P::kStep * row_bytes;
+  }
+  __device__ __forceinline__ u32x4 words(int D) const {
+    u32x4 w = buffer_words(reinterpret_cast<const void*>(next));
+    const int n = left < kKeys ? left : kKeys;
+    w[2] = n > 0 ? (uint32_t)(n - 1) * row_bytes + (uint32_t)(D * 2) : 0;
+    return w;
+  }
+  __device__ __forceinline__ void go_on() {
+    next += kKeys * row_bytes;
+    left -= kKeys;
+  }
+};
 
 // Whether they are all finite (a sum that is not finite has a term that is not).
 template <int kD>
@@ -300,11 +339,12 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   static_assert(ENGRAM_WINDOW_SINKS_MAX <= 2 * kKeys, "");
   const uint16_t* const k0 = a.k + r.base * a.ldk + (int64_t)r.head * a.D;
   const uint16_t* const v0 = a.v + r.base * a.ldv + (int64_t)r.head * a.D;
-  const auto fetch = [&](int x, int i, int slot, auto early) {
-    constexpr bool kMix = decltype(early)::value;
-    if (x % 2 == 0) fetch_keys<kMix>(pieces, x / 2, lds[slot % 2], k0, a.ldk, keys, i, a.D, k_at, wave);
-    else fetch_keys<kMix>(pieces, x / 2, lds[2 + slot % 3], v0, a.ldv, keys, i, a.D, v_at, wave);
+  const auto fetch_first = [&](int x, int i) {
+    if (x % 2 == 0) fetch_keys(pieces, x / 2, lds[i], k0, a.ldk, keys, i, a.D, k_at, wave);
+    else fetch_keys(pieces, x / 2, lds[2 + i], v0, a.ldv, keys, i, a.D, v_at, wave);
   };
+  Following<Pieces<kD, kKeys, kThreads>> next_k(pieces, k0, a.ldk, keys, 2, a.D), next_v(pieces, v0, a.ldv, keys, 2, a.D);
+  const auto whole = keys.whole(first, last, a.W);
   // Operands on their way from LDS: of the next half's scores, and of this half's values.
   constexpr int kX = kD / 16;  // products of a half's scores, and of its values
   u32x4 kf[kX], vf[kX];
@@ -344,8 +384,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   };
   // what rows do not see goes; the maximum, and what there is in its terms
   const auto settle = [&](f32x16& s, float top, int i, int u) {
-    const int start = keys.start(i) + 32 * u, end = keys.end(i), below = keys.below(i, a.S);
-    if (start + 32 > end || start + 31 > first || !(start > last - a.W || start + 32 <= below)) {
+    if (!whole.has(2 * i + u)) {
+      const int start = keys.start(i) + 32 * u, end = keys.end(i), below = keys.below(i, a.S);
       keep_seen(s, t, start + 4 * (int)h, end, a.W, below, -INFINITY);
       top = largest(s);
     }
@@ -387,6 +427,11 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (u == 0) meet();  // the next tile is there, and this one's keys are read out, the last one's values too
+    const u32x4 words_k = next_k.words(a.D), words_v = next_v.words(a.D);
+    if constexpr (u == 0) {
+      next_k.go_on();
+      next_v.go_on();
+    }
     float top = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
@@ -394,7 +439,10 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       o[x % (kD / 32)] = product<T>(vf[x], p[x / (kD / 32)], o[x % (kD / 32)]);
       // (behind the last tile these read what lies there, for no one)
       if constexpr (kNext) read_keys(slot + 1, u, x);
-      if constexpr (u == 0) fetch(x, i + 2, slot + 2, std::false_type{});
+      if constexpr (u == 0) {
+        if (x % 2 == 0) load_to_lds(pieces.lds_place(x / 2, lds[slot % 2], wave), words_k, next_k.at[x / 2]);
+        else load_to_lds(pieces.lds_place(x / 2, lds[2 + (slot + 2) % 3], wave), words_v, next_v.at[x / 2]);
+      }
       if (x < kX / 2) {
         weigh(8 + x * kEach, kEach);
       } else if constexpr (kNext) {
@@ -418,15 +466,15 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       return (int)(32 * wave + row) < r.rows ? t * (uint32_t)(a.ldq * 2) + g * (uint32_t)(a.D * 2) : kBeyond;
     });
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) fetch(x, 0, 0, std::true_type{});
+    for (int x = 0; x < kLoads; ++x) fetch_first(x, 0);
 #pragma unroll
-    for (int x = 0; x < kLoads; x += 2) fetch(x, 1, 1, std::true_type{});
+    for (int x = 0; x < kLoads; x += 2) fetch_first(x, 1);
     meet();
 #pragma unroll
     for (int x = 0; x < kX; ++x) q[x] = rows(lds_of(mine), 0, x);
     meet();
 #pragma unroll
-    for (int x = 1; x < kLoads; x += 2) fetch(x, 1, 1, std::true_type{});
+    for (int x = 1; x < kLoads; x += 2) fetch_first(x, 1);
   }
   f32x16 s0 = f32x16{}, s1;
 #pragma unroll
@@ -520,8 +568,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   const auto fetch = [&](int i, int slot) {
 #pragma unroll
     for (int q = 0; q < pieces.kMoves; ++q) {
-      fetch_keys<true>(pieces, q, lds[slot][0], k0, a.ldk, keys, i, a.D, k_at, wave);
-      fetch_keys<true>(pieces, q, lds[slot][1], v0, a.ldv, keys, i, a.D, v_at, wave);
+      fetch_keys(pieces, q, lds[slot][0], k0, a.ldk, keys, i, a.D, k_at, wave);
+      fetch_keys(pieces, q, lds[slot][1], v0, a.ldv, keys, i, a.D, v_at, wave);
     }
   };
   const RowReader<kD> rows(lane);
@@ -545,10 +593,23 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
     for (int dt = 0; dt < kD / 32; ++dt) {
       by_column[n][dt] = (uint32_t)(uintptr_t)lds_of(lds[0][0]) + columns.at[n][dt];
     }
+  Following<Pieces<kD, kKeys, kThreads>> next_k(pieces, k0, a.ldk, keys, 2, a.D), next_v(pieces, v0, a.ldv, keys, 2, a.D);
+  const auto whole = keys.whole(first, last, a.W);
   fetch(0, 0);
   for (int i = 0; i < keys.n; ++i) {
     meet();
-    if (i + 1 < keys.n) fetch(i + 1, (i + 1) & 1);
+    if (i == 0) {
+      if (keys.n > 1) fetch(1, 1);
+    } else if (i + 1 < keys.n) {
+      const u32x4 words_k = next_k.words(a.D), words_v = next_v.words(a.D);
+#pragma unroll
+      for (int q = 0; q < pieces.kMoves; ++q) {
+        load_to_lds(pieces.lds_place(q, lds[(i + 1) & 1][0], wave), words_k, next_k.at[q]);
+        load_to_lds(pieces.lds_place(q, lds[(i + 1) & 1][1], wave), words_v, next_v.at[q]);
+      }
+      next_k.go_on();
+      next_v.go_on();
+    }
 #pragma unroll
     for (int x = 0; x < kX; ++x) asm volatile("" : "+v"(by_row[x]), "+v"(by_column[x / (kD / 32)][x % (kD / 32)]));
     u32x4 f[kRing];
@@ -589,9 +650,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
       }
       asm volatile("" : "+v"(s));  // or it moves behind the branch, away from the products
       __builtin_amdgcn_sched_barrier(0);
-      const int start = keys.start(i) + 32 * u, end = keys.end(i), below = keys.below(i, a.S);
-      const bool some = start + 32 > end || start + 31 > first || !(start > last - a.W || start + 32 <= below);
-      if (some) keep_seen(s, t, start + 4 * (int)h, end, a.W, below, 0.0f);
+      if (!whole.has(2 * i + u))
+        keep_seen(s, t, keys.start(i) + 32 * u + 4 * (int)h, keys.end(i), a.W, keys.below(i, a.S), 0.0f);
       u32x4 e[2];
       const auto differ = [&](int from, int n) {
 #pragma unroll

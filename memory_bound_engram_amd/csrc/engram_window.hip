@@ -415,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
 #pragma unroll
       for (int e = from; e < from + n; ++e) {
         s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, less));
-        sum += s[e];
+        if (e > 0) sum += s[e - 1];  // not the one just made, which takes a moment
       }
       if ((from + n) % 8 == 0) p[(from + n) / 8 - 1] = operand<T>(s, (from + n) / 8 - 1);
     };
@@ -443,9 +443,9 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
         if (x % 2 == 0) load_to_lds(pieces.lds_place(x / 2, lds[slot % 2], wave), words_k, next_k.at[x / 2]);
         else load_to_lds(pieces.lds_place(x / 2, lds[2 + (slot + 2) % 3], wave), words_v, next_v.at[x / 2]);
       }
-      if (x < kX / 2) {
-        weigh(8 + x * kEach, kEach);
-      } else if constexpr (kNext) {
+      if (x < kX / 2) weigh(8 + x * kEach, kEach);
+      if (x == kX / 2) sum += s[15];
+      if (kNext && x >= kX / 2) {
 #pragma unroll
         for (int e = (x - kX / 2) * 2 * kEach; e < (x - kX / 2 + 1) * 2 * kEach; ++e) top = fmaxf(top, next[e]);
       }

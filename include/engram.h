@@ -559,6 +559,8 @@ size_t engram_window_attn_bwd_workspace_bytes(int64_t N, int64_t B, int64_t Hq, 
  *                  of the same slot with positions p, p + 1, ... are tokens of
  *                  one sequence, in order, each seeing those before it: n of them
  *                  need capacity >= sinks + window + n - 1, and n <= 64.
+ *                  A slot stands in the batch once or so: what other rows of one
+ *                  slot find of each other is not specified.
  *   workspace      engram_window_attn_step_workspace_bytes(B, Hq, Hk, D, capacity)
  *                  bytes, or NULL where that is 0
  *   B 1..ENGRAM_WINDOW_STEP_ROWS_MAX; Hq, Hk, D, sinks, scale, dtype as above;

@@ -25,6 +25,14 @@
 // carried through the groups and then the chunks before it, always in the same
 // order: one hop from workgroup to workgroup for every 64 chunks.
 //
+// What bounds it (29623 tokens of 5120 channels, bf16, forward: 261 us, 3.5 TB/s):
+// a workgroup's stages follow each other (ticket, loads, walk, words, stores),
+// two workgroups a CU overlap them only so far, and the vector units are at work
+// most of the time too: an exponential, a reciprocal and some fifteen more instructions a
+// value.  One level of words (a hop for every eight chunks) took 392; workgroups that stay and
+// take the next ticket, and ask for its values, before they are done with this
+// one 432: others wait for a chunk that is held but not begun.
+
 // Waiting.  A workgroup waits for words that others write.  Chunks are dealt by a
 // ticket (a counter in the workspace), so all chunks before a workgroup's own
 // belong to workgroups that run already.  A chunk's (P, x) is published before its

@@ -27,6 +27,21 @@
 // rows' part of their dk and dv is summed in pieces of the sequence by a
 // launch of its own and added by the workgroup that has the sinks' window part.
 //
+// What bounds them.  A wave issues one instruction at a time, of any kind, and a
+// SIMD's two waves (the registers let in no more) do not fill the matrix cores:
+// at 7 sequences up to 8192 tokens, 40 + 8 heads of 128, window 1024 (the forward, 605
+// to 625 us, 0.9 PFLOP/s) they are busy 45% of the time, the vector units 48%.  The
+// backward of 5 sequences up to 4096, 32 + 8 heads, takes 640 to 660 us: dq 280
+// (matrix cores 39%), dk and dv 360 (1040 workgroups' worth of rounds on 256 CUs, one
+// each).
+// So what counts is instructions: loops of a fixed
+// number of tiles, in which an operand's place in LDS is a constant behind an
+// address in a register (40 us of the forward's 676), few scalar instructions for a
+// tile's loads (25), no gap between sinks and window (40).  Tried and slower: 64 rows a wave, one
+// wave a SIMD (the products' results then lie where the vector unit cannot
+// read them, and registers spill); workgroups that stay and fetch the next
+// rows while they work on these, one a CU.
+//
 // Rounding.  Sums, maxima and the softmax are fp32.  p and d are rounded to the
 // element type as operands of the second products; the sum of p is taken
 // unrounded.  (fp16: p <= 1, and what is below 2^-24 of the largest may vanish; d
@@ -557,7 +572,6 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
 #pragma unroll
     for (int kk = 0; kk < kD / 16; ++kk) delta += dot8<T>(go[kk], o[kk]);
     delta = column_sum(delta);
-    if (there && h == 0) a.delta[at_head] = delta;
   }
 
   const KeyTiles keys(first, last, a.W, a.S);
@@ -596,10 +610,46 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   Following<Pieces<kD, kKeys, kThreads>> next_k(pieces, k0, a.ldk, keys, 2, a.D), next_v(pieces, v0, a.ldv, keys, 2, a.D);
   const auto whole = keys.whole(first, last, a.W);
   fetch(0, 0);
+  // Where rows see few keys, do . o is not exact enough: the rounding of o is large
+  // against what is left of do . v - delta (sequences of 10 tokens, fp16: it alone moves
+  // the gradients by 6e-4 to 9e-4 of their norms; they are off by 3e-4 in all with
+  // delta as the weights' mean of do . v).  Where they see many it adds little
+  // (window 1024, bf16: 2.5e-3 for 2.3e-3), and two more products for each key would
+  // cost a third of the call; here they cost a seventh (10496 tokens, window 48: 237 us for 201).
+  if (keys.n <= 2) {
+    if (keys.n > 1) fetch(1, 1);
+    meet();
+    float weights = 0.0f, mean = 0.0f;
+#pragma unroll 1
+    for (int half = 0; half < 2 * keys.n; ++half) {
+      const int n = half / 2, u = half % 2;
+      const lds_bytes tk = lds_of(lds[n][0]) + u * kTile / 2, tv = lds_of(lds[n][1]) + u * kTile / 2;
+      f32x16 s = f32x16{}, d = f32x16{};
+#pragma unroll
+      for (int x = 0; x < kX; ++x) s = product<T>(rows(tk, 0, x), q[x], s);
+#pragma unroll
+      for (int x = 0; x < kX; ++x) d = product<T>(rows(tv, 0, x), go[x], d);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse));
+      const int start = keys.start(n) + 32 * u + 4 * (int)h;
+      keep_seen(s, t, start, keys.end(n), a.W, keys.below(n, a.S), 0.0f);
+      keep_seen(d, t, start, keys.end(n), a.W, keys.below(n, a.S), 0.0f);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        weights += s[e];
+        mean = fmaf(s[e], d[e], mean);
+      }
+    }
+    weights = column_sum(weights);
+    mean = column_sum(mean);
+    // (where the weights do not add up to 1, lse is of other keys, or not finite)
+    if (fabsf(weights - 1.0f) <= 0x1p-12f && fabsf(mean) < INFINITY) delta = mean / weights;
+  }
+  if (there && h == 0) a.delta[at_head] = delta;
   for (int i = 0; i < keys.n; ++i) {
     meet();
     if (i == 0) {
-      if (keys.n > 1) fetch(1, 1);
+      if (keys.n > 2) fetch(1, 1);
     } else if (i + 1 < keys.n) {
       const u32x4 words_k = next_k.words(a.D), words_v = next_v.words(a.D);
 #pragma unroll

@@ -414,7 +414,8 @@ hipError_t launch_window_fill(const WindowStepCall& w, hipStream_t stream) {
   a.k = w.k; a.v = w.v; a.cache_k = w.cache_k; a.cache_v = w.cache_v; a.cu = w.cu; a.slots = w.slots;
   a.N = w.N; a.n_slots = w.n_slots; a.ldk = w.ldk; a.ldv = w.ldv;
   a.B = (int)w.B; a.Hk = (int)w.Hk; a.D = (int)w.D; a.S = (int)w.sinks; a.R = (int)(w.capacity - w.sinks);
-  const int64_t parts = (w.capacity + kFillLines - 1) / kFillLines;
+  const int64_t lines = w.capacity < w.N ? w.capacity : w.N;  // no sequence reaches the others
+  const int64_t parts = (lines + kFillLines - 1) / kFillLines;
   void* args[] = {&a};
   return hipLaunchKernel((const void*)&window_fill_kernel, dim3((unsigned)parts, (unsigned)w.B), dim3(kFillThreads), args, 0, stream);
 }

@@ -95,8 +95,9 @@ def run_forward(c, dev, lse=True, stream=None):
     return o, ls
 
 
-def backward64(c, o, lse):
-    """Gradients and bounds, given the forward's rounded o and lse."""
+def backward64(c, o, lse, mean=False):
+    """Gradients and bounds, given the forward's rounded o and lse; with `mean`, where delta is to be the weights' mean of
+    the products with v, which keeps the digits that a rounded o has lost."""
     u = HALF_STEP[c["dtype"]]
     dev = c["q"].device
     gq, eq = (torch.zeros(c["q"].shape, dtype=torch.float64, device=dev) for _ in range(2))
@@ -113,6 +114,8 @@ def backward64(c, o, lse):
             edelta = (g.abs() * (o[rows, h].double() - p @ v).abs()).sum(1, keepdim=True) + \
                 F32 * (c["d"] + 8) * (g.abs() * o[rows, h].double().abs()).sum(1, keepdim=True)
             edp = F32 * (c["d"] + 4) * (g.abs() @ v.abs().t())
+            if mean:  # a common factor of the weights cancels: their errors move the mean by what each is away from it
+                edelta = 1.01 * (p * (off * (dp - delta).abs() + edp + F32 * (n + 8) * dp.abs())).sum(1, keepdim=True)
             ds = p * (dp - delta)
             eds = p * ((edp + edelta) * (1 + off) + off * (dp - delta).abs()) + 4 * F32 * ds.abs()
             tiny = 2.0 ** -25 if c["dtype"] is FP else 0.0  # what a weight or d rounded to fp16 may lose below its smallest steps
@@ -185,6 +188,18 @@ def test_long(gpu, window, sinks):
 @pytest.mark.parametrize("sinks", [1, 63, 64, 65, 127, 128])
 def test_sinks_and_window_in_one_tile(gpu, sinks):
     check_all(case([400, 190], 4, 2, 72, BF, gpu, 30, sinks, seed=7), gpu)
+
+
+@pytest.mark.parametrize("lens,window,sinks", [([2, 10, 3, 64], 64, 0), ([30, 128], 128, 0), ([200, 7], 50, 3)], ids=str)
+def test_gradients_of_rows_that_see_few_keys(gpu, lens, window, sinks):
+    """Up to two tiles of keys: the gradients are as exact as their own roundings, not as that of o."""
+    for dtype in (BF, FP):
+        c = case(lens, 2, 1, 128, dtype, gpu, window, sinks, seed=8)
+        o, lse = run_forward(c, gpu)
+        for name, g, (want, bound) in zip(("grad_q", "grad_k", "grad_v"), run_backward(c, o, lse, gpu),
+                                          backward64(c, o, lse, mean=True)):
+            print(f"window attn few keys {lens} {dtype} {name}", flush=True)
+            check(name, g, want, bound)
 
 
 def test_peaked_and_even_weights(gpu):

@@ -30,10 +30,10 @@
 // What bounds them.  A wave issues one instruction at a time, of any kind, and a
 // SIMD's two waves (the registers let in no more) do not fill the matrix cores:
 // at 7 sequences up to 8192 tokens, 40 + 8 heads of 128, window 1024 (the forward, 605
-// to 625 us, 0.9 PFLOP/s) they are busy 45% of the time, the vector units 48%.  The
-// backward of 5 sequences up to 4096, 32 + 8 heads, takes 640 to 660 us: dq 280
-// (matrix cores 39%), dk and dv 360 (1040 workgroups' worth of rounds on 256 CUs, one
-// each).
+// to 625 us, 0.9 PFLOP/s), they are busy 49% of the time, the vector units 53%.  The
+// backward of 5 sequences up to 4096, 32 + 8 heads, takes 640 to 660 us: dq 260
+// (matrix cores 43%), dk and dv 380 (36%, CUs 83%: 760 workgroups, one a CU at a
+// time, and the sinks' behind them).
 // So what counts is instructions: loops of a fixed
 // number of tiles, in which an operand's place in LDS is a constant behind an
 // address in a register (40 us of the forward's 676), few scalar instructions for a

@@ -44,7 +44,7 @@
 //
 // Rounding.  Sums, maxima and the softmax are fp32.  p and d are rounded to the
 // element type as operands of the second products; the sum of p is taken
-// unrounded.  (fp16: p <= 1, and what is below 2^-24 of the largest may vanish; d
+// unrounded.  (fp16: p <= 2^8, and what is below 2^-24 of the largest may vanish; d
 // beyond 65504 becomes infinite.)
 //
 // Where p is 0 because j is not seen, the product with v_j would still be NaN if

@@ -181,6 +181,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   const auto get = [&](const void* p, int64_t ld, int64_t t, bool in) {
     return in && mine ? load_raw4(static_cast<const T*>(p) + t * ld + ch) : zero_raw4<T>();
   };
+  const Sequences seqs{a.cu, a.N, a.B};
+  const int64_t asked = seqs.ask();  // before the values, as loads come back in order
+  __builtin_amdgcn_sched_barrier(0);
   Raw4<T> gate[kTok], in[kTok];  // in: u, or the gradient of h
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
@@ -189,13 +192,12 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   }
 
   // Whose tokens they are: the sequence of each, or -1; whether it is the first or the last.
-  const Sequences seqs{a.cu, a.N, a.B};
   int seq[kTok];
+  const int64_t low = kBack ? token(kTok - 1) : first;
+  int64_t start, end;
+  int b = seqs.last_at_most(low < 0 ? 0 : low, [](int64_t at, int) { return at; }, &start, &end, asked);
   uint32_t begins = 0, ends_here = 0;
   {
-    const int64_t low = kBack ? token(kTok - 1) : first;
-    int b = seqs.first_behind(low < 0 ? 0 : low);
-    int64_t start = b < a.B ? seqs.start(b) : a.N, end = b < a.B ? seqs.end(b) : a.N;
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       const int i = kBack ? kTok - 1 - j : j;

@@ -25,13 +25,22 @@ struct Sequences {
   // The last sequence whose key(its start, its number) is at most `most`, for keys
   // that rise with the number (0 if none is), and its bounds: sixty-four starts at
   // a time, one load for up to 63 sequences.
+  // `asked`: the first of these loads, which may so be on its way before others are.
+  __device__ __forceinline__ int64_t ask() const {
+    const int i = (int)(threadIdx.x & 63) * ((B + 63) / 64);
+    return cu[i <= B ? i : B];
+  }
   template <typename F>
   __device__ __forceinline__ int last_at_most(int64_t most, F key, int64_t* start, int64_t* end) const {
+    return last_at_most(most, key, start, end, ask());
+  }
+  template <typename F>
+  __device__ __forceinline__ int last_at_most(int64_t most, F key, int64_t* start, int64_t* end, int64_t asked) const {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = B;
-    for (;;) {
+    for (int64_t raw = asked;; raw = cu[lo + lane * ((n + 63) / 64) <= B ? lo + lane * ((n + 63) / 64) : B]) {
       const int step = (n + 63) / 64, i = lo + lane * step;
-      const int64_t raw = cu[i <= B ? i : B], at = raw < 0 ? 0 : (raw > N ? N : raw);
+      const int64_t at = raw < 0 ? 0 : (raw > N ? N : raw);
       const uint64_t in = __ballot(lane * step < n && key(at, i) <= most);
       const int last = in ? 63 - __builtin_clzll(in) : 0;
       if (step == 1) {
@@ -51,16 +60,6 @@ struct Sequences {
   static __device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
     return (int64_t)((uint64_t)hi << 32 | lo);
-  }
-  // the first sequence that ends behind a token (B if none does)
-  __device__ int first_behind(int64_t token) const {
-    int lo = 0, hi = B;
-    while (lo < hi) {
-      const int mid = lo + (hi - lo) / 2;
-      if (end(mid) > token) hi = mid;
-      else lo = mid + 1;
-    }
-    return lo;
   }
 };
 

@@ -25,14 +25,17 @@
 // carried through the groups and then the chunks before it, always in the same
 // order: one hop from workgroup to workgroup for every 64 chunks.
 //
-// What bounds it (29623 tokens of 5120 channels, bf16, forward: 261 us, 3.5 TB/s):
-// a workgroup's stages follow each other (ticket, loads, walk, words, stores),
-// two workgroups a CU overlap them only so far, and the vector units are at work
-// most of the time too: an exponential, a reciprocal and some fifteen more instructions a
-// value.  One level of words (a hop for every eight chunks) took 392; workgroups that stay and
-// take the next ticket, and ask for its values, before they are done with this
-// one 432: others wait for a chunk that is held but not begun.
-
+// What bounds it (29623 tokens of 5120 channels, bf16, forward: 237 us, 3.8 TB/s;
+// backward of 8455: 132 us, 3.9 TB/s): a workgroup's stages follow each other (ticket,
+// loads, walk, words, stores), two workgroups a CU overlap them only so far, and
+// the vector units are at work most of the time too: an exponential, a reciprocal and some
+// fifteen more instructions a value.  One level of words (a hop for every eight
+// chunks) took 392.  Loads come back in order, so what the walk needs besides the values
+// is asked for before them (261 without).  Slower: chunks of 32 tokens with
+// three workgroups a CU (327), chunk and group words looked at together (249), workgroups that
+// stay and take the next ticket, and ask for its values, before they are done with this
+// one (432: others wait for a chunk that is held but not begun).
+//
 // Waiting.  A workgroup waits for words that others write.  Chunks are dealt by a
 // ticket (a counter in the workspace), so all chunks before a workgroup's own
 // belong to workgroups that run already.  A chunk's (P, x) is published before its
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   const auto token = [&](int i) { return kBack ? first - i : first + i; };
   const auto there = [&](int i) { return walked + i < a.N; };
   const auto get = [&](const void* p, int64_t ld, int64_t t, bool in) {
-    return in && mine ? load_raw4(static_cast<const T*>(p) + t * ld + ch) : zero_raw4<T>();
+    return in && mine ? load_raw4<true>(static_cast<const T*>(p) + t * ld + ch) : zero_raw4<T>();
   };
   const Sequences seqs{a.cu, a.N, a.B};
   const int64_t asked = seqs.ask();  // before the values, as loads come back in order

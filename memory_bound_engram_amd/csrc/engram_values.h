@@ -83,9 +83,10 @@ template <typename T>
 struct Raw4 {
   u32x2 w[sizeof(T) / 2];
 };
-template <typename T>
+template <bool kStream = false, typename T>
 __device__ __forceinline__ Raw4<T> load_raw4(const T* p) {
-  if constexpr (sizeof(T) == 4) return __builtin_bit_cast(Raw4<T>, load16(p));
+  if constexpr (sizeof(T) == 4) return __builtin_bit_cast(Raw4<T>, kStream ? load16_stream(p) : load16(p));
+  else if constexpr (kStream) return Raw4<T>{{__builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p))}};
   else return Raw4<T>{{*reinterpret_cast<const u32x2*>(p)}};
 }
 template <typename T>

@@ -561,19 +561,6 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   const int first = r.t0, last = r.t0 + (int)r.token(r.rows - 1, a, &g_last);
   const int head = r.head * a.G + (int)g;
   const int64_t token = r.base + (there ? t : 0), at_head = token * (a.Hk * a.G) + head;
-  u32x4 q[kD / 16], go[kD / 16];
-  load_row<kD>(q, a.q + token * a.ldq + (int64_t)head * a.D, there, a.D, h);
-  load_row<kD>(go, a.grad_o + token * a.ldgo + (int64_t)head * a.D, there, a.D, h);
-  const float lse = there ? a.lse_in[at_head] * kLog2e : 0.0f;
-  float delta = 0.0f;
-  {
-    u32x4 o[kD / 16];
-    load_row<kD>(o, a.o + token * a.ldo + (int64_t)head * a.D, there, a.D, h);
-#pragma unroll
-    for (int kk = 0; kk < kD / 16; ++kk) delta += dot8<T>(go[kk], o[kk]);
-    delta = column_sum(delta);
-  }
-
   const KeyTiles keys(first, last, a.W, a.S);
   const Pieces<kD, kKeys, kThreads> pieces(threadIdx.x);
   const uint32_t k_at = pieces.offset(a.ldk, a.D), v_at = pieces.offset(a.ldv, a.D);
@@ -586,6 +573,21 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
       fetch_keys(pieces, q, lds[slot][1], v0, a.ldv, keys, i, a.D, v_at, wave);
     }
   };
+  // (the first tiles before the rows, whose loads are many)
+  fetch(0, 0);
+  if (keys.n > 1) fetch(1, 1);
+  u32x4 q[kD / 16], go[kD / 16];
+  load_row<kD>(q, a.q + token * a.ldq + (int64_t)head * a.D, there, a.D, h);
+  load_row<kD>(go, a.grad_o + token * a.ldgo + (int64_t)head * a.D, there, a.D, h);
+  const float lse = there ? a.lse_in[at_head] * kLog2e : 0.0f;
+  float delta = 0.0f;
+  {
+    u32x4 o[kD / 16];
+    load_row<kD>(o, a.o + token * a.ldo + (int64_t)head * a.D, there, a.D, h);
+#pragma unroll
+    for (int kk = 0; kk < kD / 16; ++kk) delta += dot8<T>(go[kk], o[kk]);
+    delta = column_sum(delta);
+  }
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
   const float c = a.scale * kLog2e;
@@ -609,15 +611,13 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
     }
   Following<Pieces<kD, kKeys, kThreads>> next_k(pieces, k0, a.ldk, keys, 2, a.D), next_v(pieces, v0, a.ldv, keys, 2, a.D);
   const auto whole = keys.whole(first, last, a.W);
-  fetch(0, 0);
   // Where rows see few keys, do . o is not exact enough: the rounding of o is large
   // against what is left of do . v - delta (sequences of 10 tokens, fp16: it alone moves
   // the gradients by 6e-4 to 9e-4 of their norms; they are off by 3e-4 in all with
   // delta as the weights' mean of do . v).  Where they see many it adds little
   // (window 1024, bf16: 2.5e-3 for 2.3e-3), and two more products for each key would
-  // cost a third of the call; here they cost a seventh (10496 tokens, window 48: 237 us for 201).
+  // cost a third of the call; here they cost a seventh (10496 tokens, window 48: 237 us, 201 without).
   if (keys.n <= 2) {
-    if (keys.n > 1) fetch(1, 1);
     meet();
     float weights = 0.0f, mean = 0.0f;
 #pragma unroll 1
@@ -648,9 +648,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   if (there && h == 0) a.delta[at_head] = delta;
   for (int i = 0; i < keys.n; ++i) {
     meet();
-    if (i == 0) {
-      if (keys.n > 2) fetch(1, 1);
-    } else if (i + 1 < keys.n) {
+    if (i > 0 && i + 1 < keys.n) {
       const u32x4 words_k = next_k.words(a.D), words_v = next_v.words(a.D);
 #pragma unroll
       for (int q = 0; q < pieces.kMoves; ++q) {

@@ -293,7 +293,9 @@ struct Following {
   uint32_t row_bytes;
   int left;
   __device__ __forceinline__ Following(const P& pieces, const uint16_t* src, int64_t ld, const KeyTiles& keys, int i, int D)
-      : next(reinterpret_cast<uint64_t>(src + (int64_t)keys.start(i) * ld)), row_bytes((uint32_t)(ld * 2)), left(keys.to - keys.start(i)) {
+      : next(reinterpret_cast<uint64_t>(src + (int64_t)keys.start(i) * ld)),
+        row_bytes((uint32_t)(ld * 2)),
+        left(keys.to - keys.start(i)) {
     const uint32_t first = pieces.offset(ld, D);
 #pragma unroll
     for (int q = 0; q < P::kMoves; ++q) at[q] = first == kBeyond ? kBeyond : first + q * P::kStep * row_bytes;
@@ -367,7 +369,6 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   // both in six steps, so that an operand's place is a constant behind an address
   // that stays in a register.
   constexpr int kRound = 6, kTile = kKeys * kD * 2;
-  typedef __attribute__((address_space(3))) const u32x4* lds_words;
   uint32_t k_from[kX], v_from[2][kD / 32];
 #pragma unroll
   for (int x = 0; x < kX; ++x) {
@@ -382,14 +383,11 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       asm volatile("" : "+v"(v_from[n][dt]));
     }
   const auto read_keys = [&](int slot, int u, int x) {
-    kf[x] = *(lds_words)(lds_bytes)(uintptr_t)(k_from[x] + slot % 2 * kTile + u * kTile / 2);
+    kf[x] = lds_read(k_from[x] + slot % 2 * kTile + u * kTile / 2);
   };
   const auto read_values = [&](int slot, int u, int x) {
     const uint32_t at = slot % 3 * kTile + (u * 2 + x / (kD / 32)) * kTile / 4;
-    const lds_bytes lo = (lds_bytes)(uintptr_t)(v_from[0][x % (kD / 32)] + at), hi = (lds_bytes)(uintptr_t)(v_from[1][x % (kD / 32)] + at);
-    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)lo));
-    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)hi));
-    vf[x] = u32x4{a[0], a[1], b[0], b[1]};
+    vf[x] = lds_read_turned(v_from[0][x % (kD / 32)] + at, v_from[1][x % (kD / 32)] + at);
   };
   const auto largest = [&](const f32x16& s) {
     float top = s[0];
@@ -597,7 +595,6 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   // Places as constants behind addresses that stay in registers, as in the forward; they go
   // to and fro between the two tiles' places.
   constexpr int kX = kD / 16, kEach = 16 / kX, kRing = 4, kTile = kKeys * kD * 2;
-  typedef __attribute__((address_space(3))) const u32x4* lds_words;
   uint32_t by_row[kX], by_column[2][kD / 32];
 #pragma unroll
   for (int x = 0; x < kX; ++x) {
@@ -666,14 +663,10 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
       if (n >= 6 * kX) return;
       const int u = n / (3 * kX), side = n / kX % 3, x = n % kX;
       if (side < 2) {
-        f[n % kRing] = *(lds_words)(lds_bytes)(uintptr_t)(by_row[x] + side * kTile + u * kTile / 2);
+        f[n % kRing] = lds_read(by_row[x] + side * kTile + u * kTile / 2);
       } else {
         const uint32_t at = (u * 2 + x / (kD / 32)) * kTile / 4;
-        const lds_bytes lo = (lds_bytes)(uintptr_t)(by_column[0][x % (kD / 32)] + at);
-        const lds_bytes hi = (lds_bytes)(uintptr_t)(by_column[1][x % (kD / 32)] + at);
-        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)lo));
-        const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)hi));
-        f[n % kRing] = u32x4{y[0], y[1], z[0], z[1]};
+        f[n % kRing] = lds_read_turned(by_column[0][x % (kD / 32)] + at, by_column[1][x % (kD / 32)] + at);
       }
     };
 #pragma unroll
@@ -917,7 +910,6 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   // Places as constants behind addresses that stay in registers and go to and fro
   // between the two tiles' places; those of keys and values in an instruction each.
   constexpr int kBytes = kTile * 2;
-  typedef __attribute__((address_space(3))) const u32x4* lds_words;
   uint32_t by_row[kX], by_column[2][kD / 32];
   const uint32_t of_half = (uint32_t)(uintptr_t)lds_of(tiles) + half * kBytes / 2;
   const uint32_t of_key = (uint32_t)(uintptr_t)lds_of(lds) + rows.at + quarter * kBytes / 2;
@@ -967,21 +959,17 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
       if (side >= 4) return;
       const int tile = side == 0 || side == 3 ? 0 : kBytes;  // queries, gradients
       if (side < 2) {
-        f[n % kRing] = *(lds_words)(lds_bytes)(uintptr_t)(by_row[x] + tile);
+        f[n % kRing] = lds_read(by_row[x] + tile);
       } else {
         const uint32_t at = tile + x / (kD / 32) * kBytes / 4;
-        const lds_bytes lo = (lds_bytes)(uintptr_t)(by_column[0][x % (kD / 32)] + at);
-        const lds_bytes hi = (lds_bytes)(uintptr_t)(by_column[1][x % (kD / 32)] + at);
-        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)lo));
-        const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)hi));
-        f[n % kRing] = u32x4{y[0], y[1], z[0], z[1]};
+        f[n % kRing] = lds_read_turned(by_column[0][x % (kD / 32)] + at, by_column[1][x % (kD / 32)] + at);
       }
     };
     uint32_t swap = rows.swap;
     asm volatile("" : "+v"(swap));  // or it keeps the addresses for the next tile
     const auto read_key = [&](int n) {
       if (n >= 2 * kX) return;
-      kv[n % kRing] = *(lds_words)(lds_bytes)(uintptr_t)(of_key + ((32 * (n % kX)) ^ swap) + (n < kX ? kRows * kD * 2 : 0));
+      kv[n % kRing] = lds_read(of_key + ((32 * (n % kX)) ^ swap) + (n < kX ? kRows * kD * 2 : 0));
     };
     f32x16 s = f32x16{}, d = f32x16{};
     f32x4 row[2];
@@ -1092,7 +1080,8 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
       for (int j = 0; j < 4; ++j) {
         const int col = 32 * dt + 8 * j + 4 * (int)h;
         if (col < a.D)
-          *reinterpret_cast<f32x4*>(out + col) = f32x4{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
+          *reinterpret_cast<f32x4*>(out + col) =
+              f32x4{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
       }
   }
   if (sinks) return;
@@ -1138,7 +1127,8 @@ __global__ __launch_bounds__(kJoinThreads) void window_sinks_kernel(WindowArgs a
   const int length = (int)all, d = 2 * lane;
   const bool mine = d < a.D;
   const auto add = [&](float (&y)[2], int64_t piece) {
-    const f32x2 x = mine ? *reinterpret_cast<const f32x2*>(piece_sums(a, piece, head, which) + (int64_t)j * a.D + d) : f32x2{0, 0};
+    const float* from = piece_sums(a, piece, head, which) + (int64_t)j * a.D + d;
+    const f32x2 x = mine ? *reinterpret_cast<const f32x2*>(from) : f32x2{0, 0};
     y[0] += x[0];
     y[1] += x[1];
   };

@@ -417,7 +417,8 @@ hipError_t launch_window_fill(const WindowStepCall& w, hipStream_t stream) {
   const int64_t lines = w.capacity < w.N ? w.capacity : w.N;  // no sequence reaches the others
   const int64_t parts = (lines + kFillLines - 1) / kFillLines;
   void* args[] = {&a};
-  return hipLaunchKernel((const void*)&window_fill_kernel, dim3((unsigned)parts, (unsigned)w.B), dim3(kFillThreads), args, 0, stream);
+  return hipLaunchKernel((const void*)&window_fill_kernel, dim3((unsigned)parts, (unsigned)w.B), dim3(kFillThreads), args, 0,
+                         stream);
 }
 
 }  // namespace engram

@@ -76,12 +76,15 @@ __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t col) {
 // A tile's place as LDS sees it.
 typedef __attribute__((address_space(3))) const char* lds_bytes;
 __device__ __forceinline__ lds_bytes lds_of(const uint16_t* tile) { return (lds_bytes)(lds_ptr)tile; }
-// The same in a scalar register, as a value the compiler knows nothing of: or it
-// keeps every address that depends on it as a variable of the loop.
-__device__ __forceinline__ lds_bytes opaque(lds_bytes tile) {
-  uint32_t at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)tile);
-  asm volatile("" : "+s"(at));
-  return (lds_bytes)(uintptr_t)at;
+// What lies at a place of LDS; and through the transposing read, at two.
+__device__ __forceinline__ u32x4 lds_read(uint32_t at) {
+  typedef __attribute__((address_space(3))) const u32x4* words;
+  return *(words)(lds_bytes)(uintptr_t)at;
+}
+__device__ __forceinline__ u32x4 lds_read_turned(uint32_t lo, uint32_t hi) {
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(lds_bytes)(uintptr_t)lo));
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(lds_bytes)(uintptr_t)hi));
+  return u32x4{a[0], a[1], b[0], b[1]};
 }
 
 // An operand whose rows are rows of the tile, row0 + l % 32 (row0 a multiple of
@@ -92,8 +95,7 @@ struct RowReader {
   __device__ __forceinline__ explicit RowReader(uint32_t lane)
       : at((lane & 31) * kD * 2), swap((turn<kD>(lane & 31) ^ (lane >> 5)) * 16) {}
   __device__ __forceinline__ u32x4 operator()(lds_bytes tile, int row0, int kk) const {
-    typedef __attribute__((address_space(3))) const u32x4* p;
-    return *(p)(tile + (at + ((32 * kk) ^ swap)) + row0 * kD * 2);
+    return lds_read((uint32_t)(uintptr_t)tile + (at + ((32 * kk) ^ swap)) + row0 * kD * 2);
   }
 };
 
@@ -110,12 +112,6 @@ struct ColumnReader {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int dt = 0; dt < kD / 32; ++dt) at[i][dt] = place<kD>(row + 8 * i, col + 32 * dt) * 2;
-  }
-  __device__ __forceinline__ u32x4 operator()(lds_bytes tile, int row0, int dt) const {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at[0][dt] + row0 * kD * 2));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at[1][dt] + row0 * kD * 2));
-    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-    return u32x4{a[0], a[1], b[0], b[1]};
   }
 };
 

@@ -23,9 +23,9 @@
 // The backward has two such kernels: over the keys of 128 rows for dq (and
 // delta, which it leaves for the other), and over the rows of 128 keys for dk and
 // dv: seven products where five are the least, but no sums of atomics and no partial
-// sums in memory.  Sinks are seen by all rows behind the window as well; those
-// rows' part of their dk and dv is summed in pieces of the sequence by a
-// launch of its own and added by the workgroup that has the sinks' window part.
+// sums in memory but for the sinks.  These are seen by all rows behind the window as
+// well; those rows' part of their dk and dv is summed in pieces of the sequence by
+// workgroups of their own, and a last, small launch joins it with the window's part.
 //
 // What bounds them.  A wave issues one instruction at a time, of any kind, and a
 // SIMD's two waves (the registers let in no more) do not fill the matrix cores:

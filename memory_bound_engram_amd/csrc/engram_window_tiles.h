@@ -11,6 +11,7 @@
 
 #include "engram_layers_device.h"
 #include "engram_values.h"
+#include "engram_window_bounds.h"
 
 namespace engram {
 namespace {
@@ -143,8 +144,9 @@ struct Pieces {
     static_assert(kSame, "one offset serves all of a lane's pieces");
     return col < (uint32_t)D ? row * (uint32_t)(ld * 2) + col * 2 : kBeyond;
   }
-  // Of n rows (or fewer: zeros; the memory's bound sees to it) from src on, ld apart,
-  // the q-th pieces; `at`: the above.  No vector instruction but the load.
+  // Of n rows (n may be more than the tile has; what is not there is zeros, the memory's
+  // bound sees to it) from src on, ld apart, the q-th pieces; `at`: the above.  No vector
+  // instruction but the load.
   __device__ __forceinline__ void move(int q, const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,
                                        uint32_t wave) const {
     load_to_lds(lds_place(q, tile, wave), words_of(q, src, ld, n, D), at);
@@ -159,7 +161,7 @@ struct Pieces {
   }
   static __device__ __forceinline__ u32x4 words_of(int q, const uint16_t* src, int64_t ld, int n, int D) {
     u32x4 words = buffer_words(src + (int64_t)(q * kStep) * ld);
-    words[2] = n > q * kStep ? (uint32_t)(n - q * kStep - 1) * (uint32_t)(ld * 2) + (uint32_t)(D * 2) : 0;
+    words[2] = readable_bytes(n - q * kStep, kStep, ld, D);
     return words;
   }
   __device__ __forceinline__ void fetch(const uint16_t* tile, const uint16_t* src, int64_t ld, int n, int D, uint32_t at,

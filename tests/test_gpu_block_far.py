@@ -61,6 +61,26 @@ def test_window_attention(gpu, space):  # noqa: F811
                  "go": normal(gpu, *q, seed=4), "o": blank_q, "gq": blank_q, "gk": blank_k, "gv": blank_k}, call)
 
 
+@pytest.mark.parametrize("window,sinks,hq,hk,d", [(1 << 40, 0, 2, 2, 64), (2048, 0, 2, 1, 128), (2048, 5, 2, 1, 128),
+                                                  (1950, 0, 2, 1, 72), (2500, 70, 2, 2, 40)])
+def test_window_attention_over_more_than_four_gigabytes(gpu, space, window, sinks, hq, hk, d):  # noqa: F811
+    """Rows that see 2^32 bytes and more of keys and values, from their first to their last."""
+    cu = torch.tensor([0, N - 3], device=gpu)
+
+    def call(p):
+        lse = poisoned((N, hq), F4, gpu)
+        print(f"far window {window} sinks {sinks} d {d}", flush=True)
+        eg.engram_window_attn_fwd(p["q"], p["k"], p["v"], cu, p["o"], window, sinks=sinks, lse=lse, scale=0.1)
+        eg.engram_window_attn_bwd(p["go"], p["q"], p["k"], p["v"], p["o"], lse, cu, p["gq"], p["gk"], p["gv"],
+                                  ws(eg.engram_window_attn_bwd_workspace_bytes(N, 1, hq, hk, d, window, sinks), gpu), window,
+                                  sinks=sinks, scale=0.1)
+        return {"lse": lse}
+    q, k = (N, hq, d), (N, hk, d)
+    blank_q, blank_k = poisoned(q, BF, gpu), poisoned(k, BF, gpu)
+    both(space, {"q": normal(gpu, *q, seed=1), "k": normal(gpu, *k, seed=2), "v": normal(gpu, *k, seed=3),
+                 "go": normal(gpu, *q, seed=4), "o": blank_q, "gq": blank_q, "gk": blank_k, "gv": blank_k}, call)
+
+
 def test_gated_scan(gpu, space):  # noqa: F811
     d = 264
     cu = torch.tensor([0, 3000, 3000, N - 5], device=gpu)

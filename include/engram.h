@@ -508,7 +508,8 @@ size_t engram_layer_norm_bwd_workspace_bytes(int64_t N, int64_t D);
  *   ENGRAM_WINDOW_HEADS_MAX; N * Hq <= ENGRAM_WINDOW_HEAD_ROWS_MAX; B >= 1,
  *   B * Hk <= ENGRAM_WINDOW_SEQ_HEADS_MAX; D a multiple of 8,
  *   8..ENGRAM_WINDOW_D_MAX; window >= 1 (N or more: all of the past);
- *   sinks 0..ENGRAM_WINDOW_SINKS_MAX; scale positive and finite
+ *   sinks 0..ENGRAM_WINDOW_SINKS_MAX; scale positive, at most 2^126 (scale
+ *   log2(e) has to be finite)
  *   dtype         ENGRAM_BF16 or ENGRAM_FP16, of q, k, v and o
  * Scores, maxima and sums are fp32; the softmax's weights are rounded to the
  * element type as operands of the product with v.  What a token does not see

@@ -4,7 +4,6 @@
 // synchronises.
 #include <hip/hip_runtime.h>
 
-#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -42,7 +41,8 @@ bool step_sizes_ok(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t capacit
   return window_sizes_ok(1, 1, Hq, Hk, D, 1, 0) && in(B, 1, ENGRAM_WINDOW_STEP_ROWS_MAX) &&
          in(capacity, 1, ENGRAM_WINDOW_CAPACITY_MAX);
 }
-bool scale_ok(float scale) { return scale > 0.0f && isfinite(scale); }
+// (the kernels' exponents are of 2: with scale log2(e) infinite a score of 0 would be NaN)
+bool scale_ok(float scale) { return scale > 0.0f && scale <= 0x1p126f; }
 
 Rows heads(const void* p, int64_t rows, int64_t ld, int64_t H, int64_t D) { return Rows{p, rows, ld * 2, H * D * 2}; }
 

@@ -206,6 +206,15 @@ def test_scalars(name):
         assert c(dtype=v) == eg.ERR_KIND
 
 
+@pytest.mark.parametrize("name", ["window_fwd", "window_bwd", "window_step"])
+def test_a_scale_whose_exponents_would_be_infinite(name):
+    """scale log2(e) has to be finite; the largest scale is let through, up to the misaligned pointer."""
+    c = CALLS[name]()
+    for v in (2.0 ** 126 * (1 + 2.0 ** -23), 2.0 ** 127, 3.4e38):
+        assert c(scale=v) == eg.ERR_N_RANGE, v
+    assert c(scale=2.0 ** 126, q=c.args["q"] + 8) == eg.ERR_ALIGN
+
+
 @pytest.mark.parametrize("name", CALLS)
 def test_outputs_overlap_nothing(name):
     c = CALLS[name]()

@@ -44,8 +44,8 @@
 //
 // Rounding.  Sums, maxima and the softmax are fp32.  p and d are rounded to the
 // element type as operands of the second products; the sum of p is taken
-// unrounded.  (fp16: p <= 2^8, and what is below 2^-24 of the largest may vanish; d
-// beyond 65504 becomes infinite.)
+// unrounded.  (fp16: p <= 2^8, and what is below 2^-24 of the largest may vanish; d is
+// taken times a power of two, see keep_in_range.)
 //
 // Where p is 0 because j is not seen, the product with v_j would still be NaN if
 // v_j is not finite.  Results that come out not finite are computed again by the
@@ -129,6 +129,34 @@ __device__ __forceinline__ void keep_seen(f32x16& s, int t, int start, int end, 
 // of a wave's 32 rows always finds a larger score).  Terms keep their digits, and
 // in fp16 are far from its largest value.
 constexpr float kSlack = 8.0f;
+
+// d as an operand in fp16, whose steps below 2^-14 are all 2^-24: d of ordinary small
+// gradients over many keys lies there (4096 keys, grad_o of 1e-4: dq off by 4% of
+// its norm), and d itself may pass 65504.  So the kernels hold 2^up d: `up` is a
+// lane's own, as its row's (dq) or key's (dk) sums are, and goes down, the sums with
+// it, where a value would pass 2^kMostBits.  The largest then lies at 2^4 or more below
+// 2^5, so that this is rare, and what is less than 2^-18 of the largest loses digits:
+// 2^-30 of the largest at most.  (5 sequences up to 4096, 32 + 8 heads of 128, window
+// 1024, fp16: 696 us, 677 without.)
+constexpr float kUp = 60.0f;      // where it begins: do . v is below 2^39
+constexpr int kMostBits = 15, kAimBits = 5;
+template <int kD>
+__device__ __forceinline__ void keep_in_range(f32x16& d, f32x16 (&sums)[kD / 32], float& up) {
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(d[e]));
+  if (__any(top > (float)(1 << kMostBits))) {
+    top = column_max(top);
+    // (an infinite or NaN result is made again by the definition)
+    const int down = top > (float)(1 << kMostBits) && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - kAimBits : 0;
+    const float times = __builtin_amdgcn_ldexpf(1.0f, -down);
+    up -= (float)down;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) d[e] *= times;
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt) sums[dt] *= times;
+  }
+}
 
 // The keys of a run of tokens, as tiles of kKeys: first the sinks before the window,
 // then the window, without a gap.  So the last sinks may lie in the window's first
@@ -589,6 +617,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
   const float c = a.scale * kLog2e;
+  constexpr bool kHalf = __is_same(T, _Float16);
+  float up = kHalf ? kUp : 0.0f;
   f32x16 dq[kD / 32];
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) dq[dt] = f32x16{};
@@ -674,6 +704,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int at = u * 3 * kX;
+      const float less = kHalf ? up - lse : -lse;  // (s is there for d alone)
       f32x16 s = f32x16{}, d = f32x16{};
 #pragma unroll
       for (int x = 0; x < kX; ++x) {
@@ -687,7 +718,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
         d = product<T>(f[x % kRing], go[x], d);
         read(at + kX + x + kRing);
 #pragma unroll
-        for (int m = x * kEach; m < (x + 1) * kEach; ++m) s[m] = __builtin_amdgcn_exp2f(fmaf(s[m], c, -lse));
+        for (int m = x * kEach; m < (x + 1) * kEach; ++m) s[m] = __builtin_amdgcn_exp2f(fmaf(s[m], c, less));
       }
       asm volatile("" : "+v"(s));  // or it moves behind the branch, away from the products
       __builtin_amdgcn_sched_barrier(0);
@@ -699,13 +730,21 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
         for (int m = from; m < from + n; ++m) d[m] = s[m] * (d[m] - delta);
         if ((from + n) % 8 == 0) e[(from + n) / 8 - 1] = operand<T>(d, (from + n) / 8 - 1);
       };
-      differ(0, 8);
+      if constexpr (kHalf) {
+#pragma unroll
+        for (int m = 0; m < 16; ++m) d[m] = s[m] * (d[m] - delta);
+        keep_in_range<kD>(d, dq, up);
+        e[0] = operand<T>(d, 0);
+        e[1] = operand<T>(d, 1);
+      } else {
+        differ(0, 8);
+      }
 #pragma unroll
       for (int x = 0; x < kX; ++x) {
         __builtin_amdgcn_sched_barrier(0);
         dq[x % (kD / 32)] = product<T>(f[x % kRing], e[x / (kD / 32)], dq[x % (kD / 32)]);
         read(at + 2 * kX + x + kRing);
-        if (x < kX / 2) differ(8 + x * kEach, kEach);
+        if (!kHalf && x < kX / 2) differ(8 + x * kEach, kEach);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -719,7 +758,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
 
   __syncthreads();  // the tiles are read out
   uint16_t* mine = lds[0][0] + wave * 32 * kD;
-  put_rows<T, kD>(mine, dq, a.scale, lane);
+  put_rows<T, kD>(mine, dq, kHalf ? a.scale * __builtin_amdgcn_ldexpf(1.0f, -(int)up) : a.scale, lane);
   const uint64_t redo = __ballot(there && !finite_rows<kD>(dq) && fabsf(lse) < INFINITY && fabsf(delta) < INFINITY);
   between_lanes();
   for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
@@ -902,6 +941,8 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   const RowReader<kD> rows(lane);
   const ColumnReader<kD> columns(lane);
   const float c = a.scale * kLog2e;
+  constexpr bool kHalf = __is_same(T, _Float16);
+  float up = kHalf ? kUp : 0.0f;
   f32x16 dk[kD / 32], dv[kD / 32];
 #pragma unroll
   for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
@@ -1017,6 +1058,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int w = 0; w < 2; ++w) p[w] = operand<T>(s, w);
+    const float raised = kHalf ? __builtin_amdgcn_ldexpf(1.0f, (int)up) : 1.0f;
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       __builtin_amdgcn_sched_barrier(0);
@@ -1024,8 +1066,16 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
       read(2 * kX + x + kRing);
       if (x * kEach % 4 == 0 && x * kEach < 12) read_delta(x * kEach / 4 + 1);
 #pragma unroll
-      for (int m = x * kEach; m < (x + 1) * kEach; ++m) d[m] = s[m] * (d[m] - row[m / 4 & 1][m % 4]);
-      if ((x + 1) * kEach % 8 == 0) e[(x + 1) * kEach / 8 - 1] = operand<T>(d, (x + 1) * kEach / 8 - 1);
+      for (int m = x * kEach; m < (x + 1) * kEach; ++m) {
+        d[m] = s[m] * (d[m] - row[m / 4 & 1][m % 4]);
+        if (kHalf) d[m] *= raised;
+      }
+      if (!kHalf && (x + 1) * kEach % 8 == 0) e[(x + 1) * kEach / 8 - 1] = operand<T>(d, (x + 1) * kEach / 8 - 1);
+    }
+    if constexpr (kHalf) {
+      keep_in_range<kD>(d, dk, up);
+      e[0] = operand<T>(d, 0);
+      e[1] = operand<T>(d, 1);
     }
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
@@ -1034,6 +1084,12 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
       read(3 * kX + x + kRing);
     }
     __builtin_amdgcn_sched_barrier(0);
+  }
+
+  if (kHalf) {
+    const float lowered = __builtin_amdgcn_ldexpf(1.0f, -(int)up);
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt) dk[dt] *= lowered;
   }
 
   // The exchange: the first four waves' dv, then the others' dk, in the order they

@@ -512,8 +512,9 @@ size_t engram_layer_norm_bwd_workspace_bytes(int64_t N, int64_t D);
  *   log2(e) has to be finite)
  *   dtype         ENGRAM_BF16 or ENGRAM_FP16, of q, k, v and o
  * Scores, maxima and sums are fp32; the softmax's weights are rounded to the
- * element type as operands of the product with v.  What a token does not see
- * does not reach it, infinite or NaN as it may be.
+ * element type as operands of the product with v (fp16: those below 2^-21 of a
+ * row's largest to 2^-32 of it).  What a token does not see does not reach it,
+ * infinite or NaN as it may be.
  */
 #define ENGRAM_WINDOW_ROWS_MAX 4194304
 #define ENGRAM_WINDOW_HEADS_MAX 1024

@@ -44,8 +44,9 @@
 //
 // Rounding.  Sums, maxima and the softmax are fp32.  p and d are rounded to the
 // element type as operands of the second products; the sum of p is taken
-// unrounded.  (fp16: p <= 2^8, and what is below 2^-24 of the largest may vanish; d is
-// taken times a power of two, see keep_in_range.)
+// unrounded.  (fp16: p and d are taken times powers of two, so that a weight down to 2^-21 of
+// a row's largest keeps its digits, and what a smaller one loses is 2^-32 of the largest
+// at most; backward, weights down to 2^-28.)
 //
 // Where p is 0 because j is not seen, the product with v_j would still be NaN if
 // v_j is not finite.  Results that come out not finite are computed again by the
@@ -129,6 +130,14 @@ __device__ __forceinline__ void keep_seen(f32x16& s, int t, int start, int end, 
 // of a wave's 32 rows always finds a larger score).  Terms keep their digits, and
 // in fp16 are far from its largest value.
 constexpr float kSlack = 8.0f;
+
+// Weights as operands in fp16, whose steps below 2^-14 are all 2^-24: the forward's terms
+// (2^kSlack at most) and the backward's weights (1 at most) are taken times a power
+// of two, which the exponential gives for nothing.
+template <typename T>
+constexpr float kTermsUp = __is_same(T, _Float16) ? 7.0f : 0.0f;
+template <typename T>
+constexpr float kWeightsUp = __is_same(T, _Float16) ? 14.0f : 0.0f;
 
 // d as an operand in fp16, whose steps below 2^-14 are all 2^-24: d of ordinary small
 // gradients over many keys lies there (4096 keys, grad_o of 1e-4: dq off by 4% of
@@ -448,7 +457,8 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
     constexpr int u = decltype(half)::value, kEach = 16 / kX;
     constexpr bool kNext = decltype(more)::value;
     static_assert(kLoads == kX, "a load beside each product");
-    const float less = m == -INFINITY ? 0.0f : -m * c;
+    float less = m == -INFINITY ? 0.0f : -m * c;
+    if constexpr (kTermsUp<T> != 0) less += kTermsUp<T>;
     u32x4 p[2];
     next = f32x16{};
     __builtin_amdgcn_sched_barrier(0);
@@ -534,7 +544,10 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   step(s1, s0, keys.n - 1, (keys.n - 1) % kRound, second_half, std::false_type{});
   sum = column_sum(sum);
   const float inverse = 1.0f / sum;
-  if (a.lse && there && h == 0) a.lse[(r.base + t) * (int64_t)(a.Hk * a.G) + head] = fmaf(m, c, __log2f(sum)) * kLn2;
+  if (a.lse && there && h == 0) {
+    const float one = kTermsUp<T> == 0 ? sum : __builtin_amdgcn_ldexpf(sum, -(int)kTermsUp<T>);
+    a.lse[(r.base + t) * (int64_t)(a.Hk * a.G) + head] = fmaf(m, c, __log2f(one)) * kLn2;
+  }
 
   meet();  // the tiles are read out, and what was fetched behind the last one is there
   uint16_t* mine = lds[0] + wave * 32 * kD;
@@ -552,7 +565,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
       const int j = keys.token(i, (int)lane);
       const bool seen = j >= 0 && sees(tx, j, a.W, a.S);
       const float s = seen ? dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D) : 0.0f;
-      const float p = __builtin_amdgcn_exp2f((s - mx) * c) * ix;
+      const float p = __builtin_amdgcn_exp2f(fmaf(s - mx, c, kTermsUp<T>)) * ix;
       for (uint64_t left = __ballot(seen); left; left &= left - 1) {
         const int n = __builtin_ctzll(left);
         const uint16_t* vx = a.v + (r.base + __shfl(j, n)) * a.ldv + (int64_t)r.head * a.D;
@@ -921,7 +934,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
       const bool in = row_at(lane, &t, &g) && i < n;
       const int64_t at = (base + t0 + (in ? t : 0)) * Hq + head * a.G + (in ? g : 0);
       // a row that is not there has weights of 0
-      lse = in ? a.lse_in[at] * kLog2e : INFINITY;
+      lse = in ? fmaf(a.lse_in[at], kLog2e, -kWeightsUp<T>) : INFINITY;
       delta = in ? a.delta[at] : 0.0f;
     }
     x0 += kKeys;
@@ -1058,7 +1071,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int w = 0; w < 2; ++w) p[w] = operand<T>(s, w);
-    const float raised = kHalf ? __builtin_amdgcn_ldexpf(1.0f, (int)up) : 1.0f;
+    const float raised = kHalf ? __builtin_amdgcn_ldexpf(1.0f, (int)(up - kWeightsUp<T>)) : 1.0f;
 #pragma unroll
     for (int x = 0; x < kX; ++x) {
       __builtin_amdgcn_sched_barrier(0);
@@ -1089,7 +1102,10 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   if (kHalf) {
     const float lowered = __builtin_amdgcn_ldexpf(1.0f, -(int)up);
 #pragma unroll
-    for (int dt = 0; dt < kD / 32; ++dt) dk[dt] *= lowered;
+    for (int dt = 0; dt < kD / 32; ++dt) {
+      dk[dt] *= lowered;
+      dv[dt] *= __builtin_amdgcn_ldexpf(1.0f, -(int)kWeightsUp<T>);
+    }
   }
 
   // The exchange: the first four waves' dv, then the others' dk, in the order they

@@ -217,7 +217,9 @@ __global__ __launch_bounds__(kWaves * 64) void window_step_kernel(StepArgs a) {
       for (int dt = 0; dt < kD / 16; ++dt) o[dt] *= keep;
       m = top;
     }
-    const float less = m == -INFINITY ? 0.0f : -m * c;
+    float less = m == -INFINITY ? 0.0f : -m * c;
+    // (fp16, whose steps below 2^-14 are all 2^-24: times 2^7, which leaves 2^15 at most)
+    if constexpr (__is_same(T, _Float16)) less += 7.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll

@@ -609,8 +609,8 @@ engram_status engram_window_cache_fill(const void *k, const void *v, const int64
  *   8..ENGRAM_SCAN_D_MAX; N * D <= ENGRAM_SCAN_VALUES_MAX
  *   dtype           ENGRAM_BF16, ENGRAM_FP16 or ENGRAM_FP32, of gate, u and h
  * States are fp32 throughout, and f and 1 - f are each accurate relative to
- * themselves down to 2^-126; below that they, and products of factors f, may
- * count as 0.
+ * themselves down to 2^-126: to 2^-21 for gates in fp32, to (|gate| + 4) 2^-23
+ * for 16-bit ones.  Below that they, and products of factors f, may count as 0.
  */
 #define ENGRAM_SCAN_ROWS_MAX 16777216
 #define ENGRAM_SCAN_STATES_MAX 4194304

@@ -7,8 +7,8 @@
 //   dh_t = grad_h_t + e_{t+1},  e_t = f_t dh_t        (e behind the last: grad_state_out)
 //   du_t = n_t dh_t,  dgate_t = dh_t (h_{t-1} - u_t) f_t n_t,  dstate_in = e_first
 //
-// Digits.  Of f and n the smaller one, s = t / (1 + t) with t = exp(-|gate|), keeps
-// all its digits; the other is 1 - s.  f x is taken as x - s x where the gate is
+// Digits.  Of f and n the smaller one, s = t / (1 + t) with t = exp(-|gate|), is exact
+// relative to itself up to a few units (see Gate); the other is 1 - s.  f x is taken as x - s x where the gate is
 // positive and as s x where it is not: a memory of 1 / n tokens needs n, not the
 // 24 bits of a factor near 1 (which at n = 6e-6 would be off by half a percent of
 // n), and a small f loses none either.
@@ -60,7 +60,7 @@ constexpr int kCh = 4;                       // channels of a lane
 constexpr int kTile = 64 * kCh;              // channels of a workgroup
 constexpr int kGroup = 8;                    // chunks of a group, groups of a span: a wave looks at one of each
 constexpr uint64_t kAbsent = ~0ull;
-constexpr float kLog2e = 1.44269504f;
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;
 
 // Tokens of a lane: as many as the registers of two workgroups a CU hold.
 template <typename T>
@@ -79,12 +79,21 @@ __device__ __forceinline__ f32x2 joined(f32x2 before, f32x2 after) {
   return f32x2{before[0] == kFresh ? kFresh : after[0] * before[0], fmaf(after[0], before[1], after[1])};
 }
 
+// The exponent -|g| log2(e), rounded, is off by up to |g| 2^-24: for gates in fp32
+// what it lacks, -|g| - x ln 2 by two fmas, is put back (without, s is off by up to 64 units of
+// 2^-24 at |g| = 87, 16 at 12; with it by 7, as exp2, the reciprocal and three roundings are).
+// For 16-bit gates, which are themselves off by 2^-12 or 2^-9 of |g|, it is not worth its
+// four instructions a value (29623 tokens x 5120, bf16: 242 us, 236 without; 14811 in fp32: 189, 188).
+template <typename T>
 struct Gate {
   float s, n;   // the smaller of f and n, and n
   float a;      // -s, or s where that is f
   bool keeps;   // f is the larger
   __device__ __forceinline__ explicit Gate(float g) {
-    const float t = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(g));
+    const float m = __builtin_fabsf(g), x = -kLog2e * m;
+    float t = __builtin_amdgcn_exp2f(x);
+    // (an infinite gate's t is 0, whatever it is times; a NaN's is NaN)
+    if constexpr (sizeof(T) == 4) t = fmaf(t, fminf(fmaf(-kLn2Low, x, fmaf(-kLn2, x, -m)), 1.0f), t);
     const float r = __builtin_amdgcn_rcpf(1.0f + t);
     s = t * r;
     keeps = g > 0.0f;
@@ -239,7 +248,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
     unpack4(in[i], v);
 #pragma unroll
     for (int k = 0; k < kCh; ++k) {
-      const Gate q(g[k]);
+      const Gate<T> q(g[k]);
       if constexpr (kBack) {
         x[i][k] = v[k] + last[k][1];
         last[k] = f32x2{q.f_of(last[k][0]), q.f_times(x[i][k])};
@@ -340,7 +349,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
       if (i + 2 < kTok) fetch(i + 2);
 #pragma unroll
       for (int k = 0; k < kCh; ++k) {
-        const Gate q(g[k]);
+        const Gate<T> q(g[k]);
         du[k] = q.n * v[k];
         dg[k] = du[k] * (h[k] - u[k]) * (q.keeps ? 1.0f - q.s : q.s);
         e[k] = q.f_times(v[k]);
@@ -414,7 +423,7 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(StepArgs a) {
       unpack8(load_raw(static_cast<const T*>(a.u) + (int64_t)row * a.ldu + ch), u);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const Gate q(g[k]);
+        const Gate<T> q(g[k]);
         s[k] = fmaf(q.n, u[k], q.f_times(s[k]));
       }
       store8<false>(static_cast<T*>(a.h) + (int64_t)row * a.ldh + ch, s);

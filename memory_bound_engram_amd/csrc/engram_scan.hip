@@ -25,8 +25,8 @@
 // carried through the groups and then the chunks before it, always in the same
 // order: one hop from workgroup to workgroup for every 64 chunks.
 //
-// What bounds it (29623 tokens of 5120 channels, bf16, forward: 237 us, 3.8 TB/s;
-// backward of 8455: 132 us, 3.9 TB/s): a workgroup's stages follow each other (ticket,
+// What bounds it (29623 tokens of 5120 channels, bf16, forward: 231 us, 3.9 TB/s;
+// backward of 8455: 130 us, 4.0 TB/s): a workgroup's stages follow each other (ticket,
 // loads, walk, words, stores), two workgroups a CU overlap them only so far, and
 // the vector units are at work most of the time too: an exponential, a reciprocal and some
 // fifteen more instructions a value.  One level of words (a hop for every eight
@@ -117,7 +117,7 @@ struct ScanArgs {
   void *out, *out2;             // forward: h; backward: grad_gate, grad_u
   uint64_t* words;              // tickets, (P, x) of chunks, states of groups; null: one chunk is all
   int64_t N, ldg, ldu, ldh, ldgh, ldout, ldout2;
-  int B, D, tiles, chunks;
+  int B, D, tiles, chunks, handing;  // handing: workgroups of a tile for empty sequences alone
 };
 
 // Words: the ticket in a line of its own; then, a tile's words for each, the chunks,
@@ -167,6 +167,22 @@ __device__ __forceinline__ void load_state(const float* p, bool mine, float (&v)
   else unpack4(zero_raw4<float>(), v);
 }
 
+// The states of empty sequences go through unchanged: dealt out over the waves of all
+// chunks, and of workgroups that are there for these alone where a wave would
+// have more than kHanded of them (2^20 empty sequences behind one chunk).
+constexpr int kHanded = 8;
+template <bool kBack>
+__device__ __forceinline__ void hand_on(const ScanArgs& a, const Sequences& seqs, int chunk, int wave, int ch) {
+  const float* from = kBack ? a.state_end : a.state_in;
+  const int64_t all = a.chunks + a.handing;
+  for (int64_t b = chunk + all * wave; b < a.B; b += all * kWaves) {
+    if (seqs.start((int)b) < seqs.end((int)b)) continue;
+    float s[kCh];
+    load_state(from ? from + b * a.D + ch : nullptr, true, s);
+    store4<false>(a.state_out + b * a.D + ch, s);
+  }
+}
+
 template <typename T, bool kBack>
 __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   constexpr int kTok = tokens_of<T>(), kChunk = kTok * kWaves;
@@ -184,6 +200,11 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   }
   const int chunk = (int)(ticket / a.tiles), tile = (int)(ticket % a.tiles), ch = tile * kTile + lane * kCh;
   const bool mine = ch < a.D;
+  const Sequences seqs{a.cu, a.N, a.B};
+  if (chunk >= a.chunks) {
+    if (mine) hand_on<kBack>(a, seqs, chunk, wave, ch);
+    return;
+  }
 
   // The wave's tokens, in the order of the walk: step i is token first + i, or first - i.
   const int64_t walked = (int64_t)chunk * kChunk + wave * kTok;
@@ -193,7 +214,6 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   const auto get = [&](const void* p, int64_t ld, int64_t t, bool in) {
     return in && mine ? load_raw4<true>(static_cast<const T*>(p) + t * ld + ch) : zero_raw4<T>();
   };
-  const Sequences seqs{a.cu, a.N, a.B};
   const int64_t asked = seqs.ask();  // before the values, as loads come back in order
   __builtin_amdgcn_sched_barrier(0);
   Raw4<T> gate[kTok], in[kTok];  // in: u, or the gradient of h
@@ -206,22 +226,34 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
   // Whose tokens they are: the sequence of each, or -1; whether it is the first or the last.
   int seq[kTok];
   const int64_t low = kBack ? token(kTok - 1) : first;
+  const auto start_of = [](int64_t at, int) { return at; };
   int64_t start, end;
-  int b = seqs.last_at_most(low < 0 ? 0 : low, [](int64_t at, int) { return at; }, &start, &end, asked);
+  int b = seqs.last_at_most(low < 0 ? 0 : low, start_of, &start, &end, asked);
   uint32_t begins = 0, ends_here = 0;
-  {
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) seq[i] = -1;
+  // One sequence after the other, `t` the first token that none of them had (a test of each token's
+  // own: 235 us for 231).
+  for (int64_t t = low; t < low + kTok; t = end) {
+    if (end <= t) {
+      ++b;
+      if (b < a.B) {
+        start = seqs.start(b);
+        end = seqs.end(b);
+        // empty ones, of which there may be millions, are not walked through
+        if (end <= t) b = seqs.last_at_most(t, start_of, &start, &end);
+      }
+      if (b >= a.B || end <= t) break;
+    }
+    const int from = (int)((start > t ? start : t) - low < kTok ? (start > t ? start : t) - low : kTok);
+    const int to = (int)(end - low < kTok ? end - low : kTok);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       const int i = kBack ? kTok - 1 - j : j;
-      const int64_t t = low + j;
-      while (b < a.B && end <= t) {
-        ++b;
-        start = b < a.B ? seqs.start(b) : a.N;
-        end = b < a.B ? seqs.end(b) : a.N;
-      }
-      seq[i] = b < a.B && t >= start && t >= 0 && t < a.N ? b : -1;
-      if (seq[i] >= 0 && t == start) begins |= 1u << i;
-      if (seq[i] >= 0 && t == end - 1) ends_here |= 1u << i;
+      if (j < from || j >= to) continue;
+      seq[i] = b;
+      if (low + j == start) begins |= 1u << i;
+      if (low + j == end - 1) ends_here |= 1u << i;
     }
   }
   const uint32_t enters = kBack ? ends_here : begins, leaves = kBack ? begins : ends_here;
@@ -366,16 +398,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_kernel(ScanArgs a) {
     }
   }
 
-  // The states of empty sequences go through unchanged.
-  if (a.state_out && mine) {
-    const float* from = kBack ? a.state_end : a.state_in;
-    for (int64_t b = chunk + (int64_t)a.chunks * wave; b < a.B; b += (int64_t)a.chunks * kWaves) {
-      if (seqs.start((int)b) < seqs.end((int)b)) continue;
-      float s[kCh];
-      load_state(from ? from + b * a.D + ch : nullptr, true, s);
-      store4<false>(a.state_out + b * a.D + ch, s);
-    }
-  }
+  if (a.state_out && mine) hand_on<kBack>(a, seqs, chunk, wave, ch);
 }
 
 // The step: row i of the batch is one token of the sequence whose state is slot
@@ -458,6 +481,8 @@ hipError_t launch_scan(ScanArgs a, int dtype, bool back, void* workspace, hipStr
   a.tiles = (int)tiles_of(a.D);
   a.chunks = (int)((a.N + chunk - 1) / chunk);
   a.words = a.chunks > 1 ? static_cast<uint64_t*>(workspace) : nullptr;
+  const int most = a.state_out ? (a.B + kHanded * kWaves - 1) / (kHanded * kWaves) : 0;
+  a.handing = most > a.chunks ? most - a.chunks : 0;
   if (a.words) {
     uint64_t* words = a.words;
     int64_t n = words_of(a.chunks, a.tiles);
@@ -469,7 +494,7 @@ hipError_t launch_scan(ScanArgs a, int dtype, bool back, void* workspace, hipStr
   const void* kernel = dtype == ENGRAM_BF16 ? scan_of<bf16_t>(back)
                        : dtype == ENGRAM_FP16 ? scan_of<_Float16>(back) : scan_of<float>(back);
   void* args[] = {&a};
-  return hipLaunchKernel(kernel, dim3((unsigned)((int64_t)a.chunks * a.tiles)), dim3(kThreads), args, 0, stream);
+  return hipLaunchKernel(kernel, dim3((unsigned)((int64_t)(a.chunks + a.handing) * a.tiles)), dim3(kThreads), args, 0, stream);
 }
 
 }  // namespace

@@ -604,7 +604,9 @@ engram_status engram_window_cache_fill(const void *k, const void *v, const int64
  *   h [N][D]        out, leading dimension ldh
  *   state_out [B][D] fp32, out: h behind each sequence's last token, or NULL
  *                   (not wanted)
- *   workspace       engram_gated_scan_fwd_workspace_bytes(N, B, D) bytes
+ *   workspace       engram_gated_scan_fwd_workspace_bytes(N, B, D) bytes, the
+ *                   same for every dtype (what fp32 needs, twice what 16-bit
+ *                   types write) and never NULL; all of it is the call's
  *   N 1..ENGRAM_SCAN_ROWS_MAX; B 1..ENGRAM_SCAN_STATES_MAX; D a multiple of 8,
  *   8..ENGRAM_SCAN_D_MAX; N * D <= ENGRAM_SCAN_VALUES_MAX
  *   dtype           ENGRAM_BF16, ENGRAM_FP16 or ENGRAM_FP32, of gate, u and h

@@ -514,7 +514,8 @@ size_t engram_layer_norm_bwd_workspace_bytes(int64_t N, int64_t D);
  * Scores, maxima and sums are fp32; the softmax's weights are rounded to the
  * element type as operands of the product with v (fp16: those below 2^-21 of a
  * row's largest to 2^-32 of it).  What a token does not see does not reach it,
- * infinite or NaN as it may be.
+ * infinite or NaN as it may be; where the formulas are not finite for what it
+ * sees, the results are infinite or NaN, in no fixed choice.
  */
 #define ENGRAM_WINDOW_ROWS_MAX 4194304
 #define ENGRAM_WINDOW_HEADS_MAX 1024

@@ -49,8 +49,13 @@
 // at most; backward, weights down to 2^-28.)
 //
 // Where p is 0 because j is not seen, the product with v_j would still be NaN if
-// v_j is not finite.  Results that come out not finite are computed again by the
-// definition, row by row, over what is seen alone.
+// v_j is not finite.  Where results come out not finite, what is seen is looked
+// through, for 32 rows or keys at once, for values that leave them infinite or NaN by the
+// definition too.  If some column has none, the workgroup goes through its tiles once
+// more with such values as 0 in the second products, and what is then finite takes
+// the place of those columns alone.  (One infinite value, 8000 tokens that see all of their
+// past, 16 + 4 heads of 128, fp16: in grad_o at most 4.0 ms, ordinary
+// 1.5, in v 1.0, ordinary 0.36; 714 and 143 when such rows were computed again one by one.)
 #include "engram_launch.h"
 #include "engram_sequences.h"
 #include "engram_window_tiles.h"
@@ -220,8 +225,8 @@ struct RowTile {
   }
 };
 
-__device__ __forceinline__ bool row_tile(const WindowArgs& a, RowTile* r) {
-  const int at = neighbours(blockIdx.x, gridDim.x);
+__device__ __forceinline__ bool row_tile(const WindowArgs& a, int block, RowTile* r) {
+  const int at = neighbours(block, gridDim.x);
   r->head = at / a.tiles;
   const Sequence s(a, at % a.tiles, a.G, kRows);
   const int64_t all = s.length * a.G;
@@ -235,6 +240,12 @@ __device__ __forceinline__ bool row_tile(const WindowArgs& a, RowTile* r) {
   return true;
 }
 
+// Of a wave's 32 rows, how many there are.
+__device__ __forceinline__ int wave_rows(const RowTile& r, uint32_t wave) {
+  const int left = r.rows - 32 * (int)wave;
+  return left < 32 ? left : 32;
+}
+
 // A lane's row of 8-value pieces, as the operand of kD / 16 products.
 template <int kD>
 __device__ __forceinline__ void load_row(u32x4 (&to)[kD / 16], const uint16_t* p, bool there, int D, int h) {
@@ -246,11 +257,6 @@ __device__ __forceinline__ void load_row(u32x4 (&to)[kD / 16], const uint16_t* p
 }
 
 template <typename T>
-__device__ __forceinline__ float one_value(uint16_t v) {
-  if constexpr (__is_same(T, bf16_t)) return __uint_as_float((uint32_t)v << 16);
-  else return (float)__builtin_bit_cast(_Float16, v);
-}
-template <typename T>
 __device__ __forceinline__ float dot8(u32x4 a, u32x4 b) {
   float x[8], y[8], s = 0.0f;
   unpack8(Raw<T>{{a}}, x);
@@ -259,14 +265,6 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b) {
   for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
   return s;
 }
-// The product of two rows, by one lane.
-template <typename T>
-__device__ __forceinline__ float dot_row(const uint16_t* a, const uint16_t* b, int D) {
-  float s = 0.0f;
-  for (int d = 0; d < D; d += 8) s += dot8<T>(load16(a + d), load16(b + d));
-  return s;
-}
-
 // Between a wave's writes to LDS and its lanes' reads of each other's.
 __device__ __forceinline__ void between_lanes() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -360,6 +358,253 @@ __device__ __forceinline__ bool finite_rows(const f32x16 (&v)[kD / 32]) {
   return fabsf(s) < INFINITY;
 }
 
+// Which of two values, the lower at bit 15 and the upper at bit 31, are not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t exponents = __is_same(T, bf16_t) ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t one = __is_same(T, bf16_t) ? 0x00800080u : 0x04000400u;
+  return ((w & exponents) + one) & 0x80008000u;
+}
+// Of eight, as eight bits.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite8(u32x4 v) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t f = not_finite<T>(v[w]);
+    bits |= (f >> 15 & 1) << 2 * w | (f >> 31) << (2 * w + 1);
+  }
+  return bits;
+}
+
+// The columns in which rows first .. last - 1 (row(i) says where they are) hold a value that is
+// not finite, beside those in `found`, and as far as `wanted` asks: bits of columns
+// 8 (l % (kD / 8)) on in lane l.  By a wave.
+template <typename T, int kD, typename Row>
+__device__ __forceinline__ uint32_t columns_not_finite(int first, int last, int D, uint32_t wanted, uint32_t found, Row row) {
+  constexpr int kPieces = kD / 8, kAt = 64 / kPieces, kAhead = 8;
+  const int lane = threadIdx.x & 63, col = lane % kPieces * 8, sub = lane / kPieces;
+  for (int i = first; i < last && __any(wanted & ~found); i += kAt * kAhead) {
+    u32x4 v[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int at = i + n * kAt + sub;
+      const u32x4 zero = {0, 0, 0, 0};
+      v[n] = at < last && col < D ? load16(row(at) + col) : zero;
+    }
+    uint32_t bits = 0;
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) bits |= not_finite8<T>(v[n]);
+#pragma unroll
+    for (int d = kPieces; d < 64; d *= 2) bits |= __shfl_xor(bits, d);
+    found |= bits;
+  }
+  return found;
+}
+// Those of row x of a wave's rows in LDS.
+template <typename T, int kD>
+__device__ __forceinline__ uint32_t columns_lost(const uint16_t* mine, int x, int D) {
+  const int col = (int)(threadIdx.x & 63) % (kD / 8) * 8;
+  return col < D ? not_finite8<T>(load16(mine + place<kD>(x, col))) : 0u;
+}
+
+// What of a wave's 32 rows (or keys) is to be made again: row x's columns lane and lane + 64 if bit
+// x is set.
+struct Again {
+  uint32_t columns[2] = {0, 0};
+  __device__ __forceinline__ bool any() const { return __any(columns[0] | columns[1]); }
+  // Row x's columns in `bits`, which lie as columns_not_finite has them.
+  template <int kD>
+  __device__ __forceinline__ void add(int x, uint32_t bits) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int e = 0; e < kD / 64; ++e) columns[e] |= (__shfl(bits, (lane + 64 * e) / 8) >> lane % 8 & 1) << x;
+  }
+  // Into `out(x)`, from rows in LDS, the row `first` at the earliest.
+  template <int kD, typename F>
+  __device__ __forceinline__ void put(const uint16_t* mine, F out, int first = 0) const {
+    const int lane = threadIdx.x & 63;
+    for (int x = first > 0 ? first : 0; x < 32; ++x) {
+      if (!__any((columns[0] | columns[1]) >> x & 1)) continue;
+      uint16_t* to = out(x);
+#pragma unroll
+      for (int e = 0; e < kD / 64; ++e)
+        if (columns[e] >> x & 1) to[lane + 64 * e] = mine[place<kD>(x, lane + 64 * e)];
+    }
+  }
+};
+
+// Of a wave's rows in `bad`, which lie in LDS and are not finite, the columns that are to be
+// made again: those in which all rows of `src` (keys or values) that they see are finite.
+// What the tokens low .. high of the wave's rows all see is looked through once, what
+// one of them sees besides for it alone.  `t`: a lane's row's token.
+template <typename T, int kD>
+__device__ __forceinline__ Again rows_again(uint32_t bad, const uint16_t* mine, const uint16_t* src, int64_t ld, int t,
+                                            int low, int high, const WindowArgs& a) {
+  const auto row = [&](int i) { return src + i * ld; };
+  uint32_t wanted = 0;
+  for (uint32_t left = bad; left; left &= left - 1) wanted |= columns_lost<T, kD>(mine, __builtin_ctz(left), a.D);
+  const int begin = high - a.W + 1 > 0 ? high - a.W + 1 : 0;  // of the window that all of them have
+  const int few = a.S < begin ? a.S : begin, sinks = few < low + 1 ? few : low + 1;
+  uint32_t common = columns_not_finite<T, kD>(0, sinks, a.D, wanted, 0, row);
+  common = columns_not_finite<T, kD>(begin, low + 1, a.D, wanted, common, row);
+  Again again;
+  for (uint32_t left = bad; left; left &= left - 1) {
+    const int x = __builtin_ctz(left), tx = __shfl(t, x);
+    const uint32_t need = columns_lost<T, kD>(mine, x, a.D);
+    const int before = begin < tx + 1 ? begin : tx + 1, behind = before > low + 1 ? before : low + 1;
+    uint32_t found = columns_not_finite<T, kD>(sinks, a.S < tx + 1 ? a.S : tx + 1, a.D, need, common, row);
+    found = columns_not_finite<T, kD>(tx - a.W + 1 > 0 ? tx - a.W + 1 : 0, before, a.D, need, found, row);
+    found = columns_not_finite<T, kD>(behind, tx + 1, a.D, need, found, row);
+    again.add<kD>(x, need & ~found);
+  }
+  return again;
+}
+
+// Whether `one` holds for some wave of the workgroup, through LDS that no one uses.
+template <int kOfWaves>
+__device__ __forceinline__ bool any_wave(uint16_t* lds, bool one) {
+  uint32_t* const flags = reinterpret_cast<uint32_t*>(lds);
+  if ((threadIdx.x & 63) == 0) flags[threadIdx.x >> 6] = one;
+  __syncthreads();
+  uint32_t some = 0;
+#pragma unroll
+  for (int w = 0; w < kOfWaves; ++w) some |= flags[w];
+  return __builtin_amdgcn_readfirstlane(some) != 0;
+}
+
+// A tile's values that are not finite become 0; the n-th of kThreads threads of the workgroup.
+template <typename T, int kD, int kTileRows, int kTileThreads>
+__device__ __forceinline__ void make_finite(uint16_t* tile) {
+#pragma unroll
+  for (int n = threadIdx.x; n < kTileRows * kD / 8; n += kTileThreads) {
+    u32x4 v = load16(tile + 8 * n);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t f = not_finite<T>(v[w]);
+      v[w] &= ~((f >> 15 & 1) * 0xffffu | (f >> 31) * 0xffff0000u);
+    }
+    store16(tile + 8 * n, v);
+  }
+}
+
+// A thread and its workgroup as the compiler does not know them: what follows from these is
+// worked out anew, for the second way through the tiles, instead of being kept in registers
+// along the first, which has none to spare.
+struct Afresh {
+  int block = blockIdx.x;
+  uint32_t thread = threadIdx.x;
+  __device__ __forceinline__ Afresh() {
+    asm volatile("" : "+s"(block));
+    asm volatile("" : "+v"(thread));
+  }
+};
+
+// A lane's row of a workgroup, and what it needs of the keys.
+struct OwnRow {
+  RowTile r;
+  uint32_t lane, wave, h;
+  int t, head;  // t: -1 if there is no such row, which sees nothing
+  KeyTiles keys;
+  const uint16_t *k0, *v0;
+  static __device__ __forceinline__ RowTile tile(const WindowArgs& a, int block) {
+    RowTile r;
+    row_tile(a, block, &r);
+    return r;
+  }
+  __device__ __forceinline__ int last(const WindowArgs& a) const {
+    uint32_t g;
+    return r.t0 + (int)r.token(r.rows - 1, a, &g);
+  }
+  __device__ __forceinline__ OwnRow(const WindowArgs& a, const Afresh& at)
+      : r(tile(a, at.block)), lane(at.thread & 63), wave(__builtin_amdgcn_readfirstlane(at.thread >> 6)), h(lane >> 5),
+        keys(r.t0, last(a), a.W, a.S), k0(a.k + r.base * a.ldk + (int64_t)r.head * a.D),
+        v0(a.v + r.base * a.ldv + (int64_t)r.head * a.D) {
+    const int row = 32 * (int)wave + (int)(lane & 31);
+    uint32_t g;
+    const uint32_t ahead = r.token(row, a, &g);
+    t = row < r.rows ? r.t0 + (int)ahead : -1;
+    head = r.head * a.G + (int)g;
+  }
+  __device__ __forceinline__ int64_t token() const { return r.base + (t < 0 ? 0 : t); }
+  // A row of queries, or of gradients.
+  template <int kD>
+  __device__ __forceinline__ void load(u32x4 (&to)[kD / 16], const uint16_t* from, int64_t ld, const WindowArgs& a) const {
+    load_row<kD>(to, from + token() * ld + (int64_t)head * a.D, t >= 0, a.D, h);
+  }
+  // Tile i's keys and values into LDS.
+  template <int kD>
+  __device__ __forceinline__ void fetch(uint16_t* keys_to, uint16_t* values_to, const Afresh& at, int i,
+                                        const WindowArgs& a) const {
+    const Pieces<kD, kKeys, kThreads> pieces(at.thread);
+    const uint32_t k_at = pieces.offset(a.ldk, a.D), v_at = pieces.offset(a.ldv, a.D);
+#pragma unroll
+    for (int n = 0; n < pieces.kMoves; ++n) {
+      fetch_keys(pieces, n, keys_to, k0, a.ldk, keys, i, a.D, k_at, wave);
+      fetch_keys(pieces, n, values_to, v0, a.ldv, keys, i, a.D, v_at, wave);
+    }
+  }
+};
+
+// Half a tile of scores (or of products with values): the half's rows times a lane's row.
+template <typename T, int kD>
+__device__ __forceinline__ f32x16 products(lds_bytes half, const u32x4 (&row)[kD / 16], uint32_t lane) {
+  const RowReader<kD> rows(lane);
+  f32x16 s = f32x16{};
+#pragma unroll
+  for (int x = 0; x < kD / 16; ++x) s = product<T>(rows(half, 0, x), row[x], s);
+  return s;
+}
+// An accumulator's rows, rounded, times the columns of half a tile.
+template <typename T, int kD>
+__device__ __forceinline__ void add_columns(f32x16 (&to)[kD / 32], lds_bytes half, const f32x16& v, uint32_t lane) {
+  const ColumnReader<kD> columns(lane);
+  const u32x4 p[2] = {operand<T>(v, 0), operand<T>(v, 1)};
+#pragma unroll
+  for (int x = 0; x < kD / 16; ++x) {
+    const int dt = x % (kD / 32);
+    const uint32_t at = (uint32_t)(uintptr_t)half + x / (kD / 32) * 16 * kD * 2;
+    to[dt] = product<T>(lds_read_turned(at + columns.at[0][dt], at + columns.at[1][dt]), p[x / (kD / 32)], to[dt]);
+  }
+}
+
+// The forward's columns in `again`: the weights, as they are known now (lse: of 2), times values
+// that are finite.
+template <typename T, int kD>
+__device__ __forceinline__ void make_rows_again(const WindowArgs& a, uint16_t (*lds)[kKeys * kD], const Again& again,
+                                                float lse) {
+  const Afresh at;
+  const OwnRow own(a, at);
+  u32x4 q[kD / 16];
+  own.load<kD>(q, a.q, a.ldq, a);
+  const float c = a.scale * kLog2e;
+  f32x16 o[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) o[dt] = f32x16{};
+#pragma unroll 1
+  for (int i = 0; i < own.keys.n; ++i) {
+    own.fetch<kD>(lds[0], lds[1], at, i, a);
+    meet();
+    make_finite<T, kD, kKeys, kThreads>(lds[1]);
+    meet();
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      f32x16 s = products<T, kD>(lds_of(lds[0]) + u * kKeys * kD, q, own.lane);
+      keep_seen(s, own.t, own.keys.start(i) + 32 * u + 4 * (int)own.h, own.keys.end(i), a.W, own.keys.below(i, a.S), -INFINITY);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, kWeightsUp<T> - lse));
+      add_columns<T, kD>(o, lds_of(lds[1]) + u * kKeys * kD, s, own.lane);
+    }
+    meet();
+  }
+  uint16_t* const mine = lds[0] + own.wave * 32 * kD;
+  put_rows<T, kD>(mine, o, __builtin_amdgcn_ldexpf(1.0f, -(int)kWeightsUp<T>), own.lane);
+  between_lanes();
+  again.template put<kD>(mine, [&](int x) {
+    return a.out + __shfl(own.token(), x) * a.ldout + (int64_t)__shfl(own.head, x) * a.D;
+  });
+}
+
 template <typename T, int kD>
 __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   // keys of two tiles; values of three, since a tile's are read out half a tile after its keys
@@ -367,7 +612,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5;
   RowTile r;
-  if (!row_tile(a, &r)) return;
+  if (!row_tile(a, blockIdx.x, &r)) return;
   const int row = 32 * wave + l;
   uint32_t g;
   const uint32_t dt_ = r.token(row, a, &g);
@@ -552,34 +797,55 @@ __global__ __launch_bounds__(kThreads, 2) void window_fwd_kernel(WindowArgs a) {
   meet();  // the tiles are read out, and what was fetched behind the last one is there
   uint16_t* mine = lds[0] + wave * 32 * kD;
   put_rows<T, kD>(mine, o, inverse, lane);
-  // rows that are not finite though their weights are, by the definition
+  // rows that are not finite though their weights are
   const uint64_t redo = __ballot(there && !finite_rows<kD>(o) && fabsf(m) < INFINITY && sum < INFINITY);
+  const uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32);
   between_lanes();
-  for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
-    const int x = __builtin_ctz(bad);
-    const int tx = __shfl(t, x), hx = __shfl(head, x);
-    const float mx = __shfl(m, x), ix = __shfl(inverse, x);
-    const uint16_t* qx = a.q + (r.base + tx) * a.ldq + (int64_t)hx * a.D;
-    float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
-    for (int i = 0; i < keys.n; ++i) {
-      const int j = keys.token(i, (int)lane);
-      const bool seen = j >= 0 && sees(tx, j, a.W, a.S);
-      const float s = seen ? dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D) : 0.0f;
-      const float p = __builtin_amdgcn_exp2f(fmaf(s - mx, c, kTermsUp<T>)) * ix;
-      for (uint64_t left = __ballot(seen); left; left &= left - 1) {
-        const int n = __builtin_ctzll(left);
-        const uint16_t* vx = a.v + (r.base + __shfl(j, n)) * a.ldv + (int64_t)r.head * a.D;
-        const float pn = __shfl(p, n);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if ((int)lane + 64 * e < a.D) y[e] = fmaf(pn, one_value<T>(vx[lane + 64 * e]), y[e]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e], 0.0f);
-  }
+  Again again;
+  if (bad) again = rows_again<T, kD>(bad, mine, v0, a.ldv, t, __shfl(t, 0), __shfl(t, wave_rows(r, wave) - 1), a);
   store_rows<kD>(mine, r, wave, lane, a);
+  if (!any_wave<kWaves>(lds[4], again.any())) return;
+  make_rows_again<T, kD>(a, lds, again, fmaf(m, c, __log2f(sum)) - kTermsUp<T>);
+}
+
+// dq's columns in `again`: d of what is seen alone, times keys that are finite; half a tile at a time.
+template <typename T, int kD>
+__device__ __forceinline__ void make_dq_again(const WindowArgs& a, uint16_t (*lds)[kKeys * kD], const Again& again, float lse,
+                                              float delta) {
+  const Afresh at;
+  const OwnRow own(a, at);
+  u32x4 q[kD / 16], go[kD / 16];
+  own.load<kD>(q, a.q, a.ldq, a);
+  own.load<kD>(go, a.grad_o, a.ldgo, a);
+  const float c = a.scale * kLog2e;
+  constexpr bool kHalf = __is_same(T, _Float16);
+  float up = kHalf ? kUp : 0.0f;
+  f32x16 dq[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) dq[dt] = f32x16{};
+#pragma unroll 1
+  for (int n = 0; n < 2 * own.keys.n; ++n) {
+    const int i = n / 2, u = n % 2;
+    own.fetch<kD>(lds[0], lds[1], at, i, a);
+    meet();
+    const f32x16 s = products<T, kD>(lds_of(lds[0]) + u * kKeys * kD, q, own.lane);
+    f32x16 d = products<T, kD>(lds_of(lds[1]) + u * kKeys * kD, go, own.lane);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) d[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, kHalf ? up - lse : -lse)) * (d[e] - delta);
+    keep_seen(d, own.t, own.keys.start(i) + 32 * u + 4 * (int)own.h, own.keys.end(i), a.W, own.keys.below(i, a.S), 0.0f);
+    if constexpr (kHalf) keep_in_range<kD>(d, dq, up);
+    meet();
+    make_finite<T, kD, kKeys, kThreads>(lds[0]);
+    meet();
+    add_columns<T, kD>(dq, lds_of(lds[0]) + u * kKeys * kD, d, own.lane);
+    meet();
+  }
+  uint16_t* const mine = lds[0] + own.wave * 32 * kD;
+  put_rows<T, kD>(mine, dq, kHalf ? a.scale * __builtin_amdgcn_ldexpf(1.0f, -(int)up) : a.scale, own.lane);
+  between_lanes();
+  again.template put<kD>(mine, [&](int x) {
+    return a.out + __shfl(own.token(), x) * a.ldout + (int64_t)__shfl(own.head, x) * a.D;
+  });
 }
 
 // dq of 128 rows, and delta.  Half a tile at a time: its scores, its values times the
@@ -591,7 +857,7 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5;
   RowTile r;
-  if (!row_tile(a, &r)) return;
+  if (!row_tile(a, blockIdx.x, &r)) return;
   const int row = 32 * wave + l;
   uint32_t g, g_last;
   const uint32_t ahead = r.token(row, a, &g);
@@ -773,37 +1039,13 @@ __global__ __launch_bounds__(kThreads, 2) void window_dq_kernel(WindowArgs a) {
   uint16_t* mine = lds[0][0] + wave * 32 * kD;
   put_rows<T, kD>(mine, dq, kHalf ? a.scale * __builtin_amdgcn_ldexpf(1.0f, -(int)up) : a.scale, lane);
   const uint64_t redo = __ballot(there && !finite_rows<kD>(dq) && fabsf(lse) < INFINITY && fabsf(delta) < INFINITY);
+  const uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32);
   between_lanes();
-  for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
-    const int x = __builtin_ctz(bad);
-    const int tx = __shfl(t, x), hx = __shfl(head, x);
-    const float lx = __shfl(lse, x), dx = __shfl(delta, x);
-    const uint16_t* qx = a.q + (r.base + tx) * a.ldq + (int64_t)hx * a.D;
-    const uint16_t* gx = a.grad_o + (r.base + tx) * a.ldgo + (int64_t)hx * a.D;
-    float y[2] = {0.0f, 0.0f};  // values lane, lane + 64
-    for (int i = 0; i < keys.n; ++i) {
-      const int j = keys.token(i, (int)lane);
-      const bool seen = j >= 0 && sees(tx, j, a.W, a.S);
-      float d = 0.0f;
-      if (seen) {
-        const float s = dot_row<T>(qx, a.k + (r.base + j) * a.ldk + (int64_t)r.head * a.D, a.D);
-        const float dp = dot_row<T>(gx, a.v + (r.base + j) * a.ldv + (int64_t)r.head * a.D, a.D);
-        d = __builtin_amdgcn_exp2f(fmaf(s, c, -lx)) * (dp - dx);
-      }
-      for (uint64_t left = __ballot(seen); left; left &= left - 1) {
-        const int n = __builtin_ctzll(left);
-        const uint16_t* kx = a.k + (r.base + __shfl(j, n)) * a.ldk + (int64_t)r.head * a.D;
-        const float dn = __shfl(d, n);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if ((int)lane + 64 * e < a.D) y[e] = fmaf(dn, one_value<T>(kx[lane + 64 * e]), y[e]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e] * a.scale, 0.0f);
-  }
+  Again again;
+  if (bad) again = rows_again<T, kD>(bad, mine, k0, a.ldk, t, __shfl(t, 0), __shfl(t, wave_rows(r, wave) - 1), a);
   store_rows<kD>(mine, r, wave, lane, a);
+  if (!any_wave<kWaves>(lds[1][0], again.any())) return;
+  make_dq_again<T, kD>(a, lds[0], again, lse, delta);
 }
 
 // The sinks' sums, fp32 and unscaled: [piece][key head][dk, dv][S][D], a piece for
@@ -813,38 +1055,274 @@ __device__ __forceinline__ float* piece_sums(const WindowArgs& a, int64_t piece,
   return a.sums + ((piece * a.Hk + head) * 2 + which) * a.S * a.D;
 }
 
-// dk (which: 0) or dv (1) of token j by the definition, by one wave: a lane's values
-// lane and lane + 64.
-template <typename T>
-__device__ __forceinline__ void define_key(float (&y)[2], const WindowArgs& a, int64_t base, int length, int head, int j,
-                                           int which) {
+// The columns of dk (which: 0) or dv (1) that rows of the tokens from .. to - 1 leave not finite in
+// all tokens that they see, beside those in `found`, and as far as `wanted` asks; bits as those of
+// columns_not_finite.  A NaN or -infinite lse makes a row's weights NaN or infinite; an
+// infinite or NaN value in grad_o always makes delta so, delta d, and d all of dk; dv takes
+// it as it is.
+template <typename T, int kD>
+__device__ __forceinline__ uint32_t columns_lost(const WindowArgs& a, int64_t base, int head, int from, int to, int which,
+                                                 uint32_t wanted, uint32_t found) {
+  constexpr int kAhead = 4;
   const int lane = threadIdx.x & 63, Hq = a.Hk * a.G;
-  const float c = a.scale * kLog2e;
-  const uint16_t* kj = a.k + (base + j) * a.ldk + (int64_t)head * a.D;
-  const uint16_t* vj = a.v + (base + j) * a.ldv + (int64_t)head * a.D;
-  const int behind = j < a.S ? length : (j + a.W < length ? j + a.W : length);
-  y[0] = y[1] = 0.0f;
-  for (int64_t row = (int64_t)j * a.G; row < (int64_t)behind * a.G; row += 64) {
-    const int64_t at = row + lane;
-    const bool in = at < (int64_t)behind * a.G;
-    float w = 0.0f;
-    if (in) {
-      const int64_t t = base + at / a.G;
-      const int hq = head * a.G + (int)(at % a.G);
-      const float s = dot_row<T>(a.q + t * a.ldq + (int64_t)hq * a.D, kj, a.D);
-      w = __builtin_amdgcn_exp2f(fmaf(s, c, -a.lse_in[t * Hq + hq] * kLog2e));
-      if (which == 0) w *= dot_row<T>(a.grad_o + t * a.ldgo + (int64_t)hq * a.D, vj, a.D) - a.delta[t * Hq + hq];
-    }
-    for (uint64_t left = __ballot(in); left; left &= left - 1) {
-      const int n = __builtin_ctzll(left);
-      const int64_t t = base + (row + n) / a.G, hq = head * a.G + (row + n) % a.G;
-      const uint16_t* from = which ? a.grad_o + t * a.ldgo + hq * a.D : a.q + t * a.ldq + hq * a.D;
-      const float wn = __shfl(w, n);
+  const int last = to * a.G;  // N * Hq is below 2^30
+  for (int i = from * a.G; i < last && __any(wanted & ~found); i += 64 * kAhead) {
+    float lse[kAhead], delta[kAhead];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (lane + 64 * e < a.D) y[e] = fmaf(wn, one_value<T>(from[lane + 64 * e]), y[e]);
+    for (int n = 0; n < kAhead; ++n) {
+      const int at = i + 64 * n + lane;
+      const int64_t row = at < last ? (base + at / a.G) * Hq + head * a.G + at % a.G : 0;
+      lse[n] = at < last ? a.lse_in[row] : 0.0f;
+      delta[n] = at < last ? a.delta[row] : 0.0f;
+    }
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const bool off = !(fabsf(delta[n]) < INFINITY);
+      if (__any(!(lse[n] > -INFINITY) || (which == 0 && off))) return 0xff;
+      const int at = i + 64 * n;
+      if (__any(off))
+        found = columns_not_finite<T, kD>(at, at + 64 < last ? at + 64 : last, a.D, wanted, found, [&](int x) {
+          return a.grad_o + (base + x / a.G) * a.ldgo + (int64_t)(head * a.G + x % a.G) * a.D;
+        });
     }
   }
+  return found;
+}
+
+// Whether dk of a token is lost by its value, which is part of every d.
+template <typename T>
+__device__ __forceinline__ bool lost_by_value(const WindowArgs& a, int64_t base, int head, int j) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* v = a.v + (base + j) * a.ldv + (int64_t)head * a.D;
+  bool off = false;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (lane + 64 * e < a.D) off |= not_finite<T>(v[lane + 64 * e]) != 0;
+  return __any(off);
+}
+
+// Of a wave's 32 keys from key0 on, in `bad`, whose dk or dv lies in LDS and is not finite, the
+// columns that are to be made again, as rows_again: `low(j)` .. `high(j)` - 1 are the tokens
+// whose rows' part of key j is in question, both rising with j.
+template <typename T, int kD, typename Low, typename High>
+__device__ __forceinline__ Again keys_again(uint32_t bad, const uint16_t* mine, const WindowArgs& a, int64_t base, int head,
+                                            int key0, int which, Low low, High high) {
+  uint32_t wanted = 0;
+  for (uint32_t left = bad; left; left &= left - 1) wanted |= columns_lost<T, kD>(mine, __builtin_ctz(left), a.D);
+  // the tokens that all of the keys have
+  const int begin = low(key0 + 31), most = high(key0), end = most > begin ? most : begin;
+  const uint32_t common = columns_lost<T, kD>(a, base, head, begin, end, which, wanted, 0);
+  Again again;
+  for (uint32_t left = bad; left; left &= left - 1) {
+    const int x = __builtin_ctz(left), j = key0 + x, from = low(j), to = high(j);
+    const uint32_t need = columns_lost<T, kD>(mine, x, a.D);
+    if (which == 0 && from < to && lost_by_value<T>(a, base, head, j)) continue;
+    uint32_t found = columns_lost<T, kD>(a, base, head, from, begin < to ? begin : to, which, need, common);
+    found = columns_lost<T, kD>(a, base, head, end > from ? end : from, to, which, need, found);
+    again.add<kD>(x, need & ~found);
+  }
+  return again;
+}
+
+// A workgroup's keys of a sequence and key head, and the rows whose part of their dk and dv it makes.
+struct KeyTile {
+  bool sinks;
+  int id, b, head, length;
+  int64_t base;    // the sequence's first token
+  int k0, keys;    // the first key; keys of the sequence, as far as they matter here
+  int from, to;    // the rows' tokens
+  int near, span;  // how far behind a key those lie that see it: `near` on, fewer than `span` further
+  __device__ __forceinline__ bool find(const WindowArgs& a, int block) {
+    const int wide_blocks = (int)gridDim.x - a.sink_blocks;
+    sinks = block >= wide_blocks;
+    const int at = sinks ? block - wide_blocks : neighbours(block, wide_blocks);
+    const int per_head = sinks ? a.sink_blocks / a.Hk : a.tiles;
+    id = at % per_head;
+    head = at / per_head;
+    const uint32_t unit = sinks ? (uint32_t)a.piece : (uint32_t)kRows;
+    const Sequence seq(a, id, 1, unit);
+    const int64_t tile = seq.tile;
+    b = seq.b;
+    base = seq.start;
+    length = (int)seq.length;
+    if (tile < 0 || length <= 0 || tile * unit >= length) return false;
+    k0 = sinks ? 0 : (int)tile * kRows;
+    from = k0;
+    to = k0 + kRows - 1 + a.W;
+    near = sinks ? a.W : 0;
+    if (sinks) {
+      from = (int)tile * a.piece > a.W ? (int)tile * a.piece : a.W;
+      to = ((int)tile + 1) * a.piece;
+    }
+    if (to > length) to = length;
+    keys = sinks ? (a.S < length ? a.S : length) : length;
+    span = sinks ? length : a.W;
+    return from < to;  // else no row of the piece sees a sink as one
+  }
+  // Keys and values of 128 tokens into LDS, values first.
+  template <int kD>
+  __device__ __forceinline__ void fetch(uint16_t* lds, uint32_t thread, uint32_t wave, const WindowArgs& a) const {
+    const Pieces<kD, kRows, 512> wide(thread);
+    const int n = keys - k0 < kRows ? keys - k0 : kRows;
+    wide.fetch(lds, a.v + (base + k0) * a.ldv + (int64_t)head * a.D, a.ldv, n, a.D, wide.offset(a.ldv, a.D), wave);
+    wide.fetch(lds + kRows * kD, a.k + (base + k0) * a.ldk + (int64_t)head * a.D, a.ldk, n, a.D, wide.offset(a.ldk, a.D), wave);
+  }
+  // Sinks that rows behind their window see too have their sums in fp32, joined by the next launch.
+  __device__ __forceinline__ bool part(const WindowArgs& a, int key) const { return sinks || (key < a.S && length > a.W); }
+  __device__ __forceinline__ float* to_part(const WindowArgs& a, int key, int which) const {
+    return piece_sums(a, sinks ? id : a.pieces + b, head, which) + (int64_t)key * a.D;
+  }
+  __device__ __forceinline__ uint16_t* out(const WindowArgs& a, int key, int which) const {
+    return (which ? a.grad_v + (base + key) * a.ldgv : a.grad_k + (base + key) * a.ldgk) + (int64_t)head * a.D;
+  }
+  // Keys before this one are the next launch's.
+  __device__ __forceinline__ int done(const WindowArgs& a) const { return length > a.W ? a.S : 0; }
+  // The tokens whose rows see key j, of those that are looked at here: low(j) .. high(j) - 1.
+  __device__ __forceinline__ int low(int j) const {
+    const int x = j + near < to ? j + near : to;
+    return x > from ? x : from;
+  }
+  __device__ __forceinline__ int high(int j) const { return to - j < span ? to : j + span; }
+};
+
+// The two halves of the rows that two waves have had for the same keys, joined: the first four
+// waves then have dk, the others dv.
+template <typename T, int kD>
+__device__ __forceinline__ void join_halves(f32x16 (&sum)[kD / 32], f32x16 (&dk)[kD / 32], f32x16 (&dv)[kD / 32], float up,
+                                            uint16_t* lds, uint32_t lane, uint32_t wave) {
+  const uint32_t quarter = wave & 3, half = wave >> 2;
+  if constexpr (__is_same(T, _Float16)) {
+    const float lowered = __builtin_amdgcn_ldexpf(1.0f, -(int)up);
+#pragma unroll
+    for (int dt = 0; dt < kD / 32; ++dt) {
+      dk[dt] *= lowered;
+      dv[dt] *= __builtin_amdgcn_ldexpf(1.0f, -(int)kWeightsUp<T>);
+    }
+  }
+  // The exchange: the first four waves' dv, then the others' dk, in the order they
+  // are there for each lane.
+  f32x4* const given = reinterpret_cast<f32x4*>(lds) + quarter * (kD / 8) * 64 + lane;
+#pragma unroll
+  for (int turn = 0; turn < 2; ++turn) {
+    if (half == (uint32_t)turn) {
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x16& x = turn ? dk[dt] : dv[dt];
+          given[(dt * 4 + j) * 64] = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+        }
+    }
+    __syncthreads();
+    if (half != (uint32_t)turn) {
+#pragma unroll
+      for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 x = given[(dt * 4 + j) * 64];
+          f32x16& to = turn ? dk[dt] : dv[dt];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[4 * j + e] += x[e];
+        }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) sum[dt] = half ? dv[dt] : dk[dt];
+}
+
+constexpr int kKeyWaves = 8, kKeyThreads = kKeyWaves * 64;
+
+// The columns in `again` of dk (the first four waves) and dv: weights and d of what is seen
+// alone, times queries and gradients that are finite.  LDS as the kernel has it.
+template <typename T, int kD>
+__device__ __forceinline__ void make_keys_again(const WindowArgs& a, uint16_t* lds, float* lses, float* deltas,
+                                                const Again& again) {
+  const Afresh afresh;
+  const uint32_t lane = afresh.thread & 63, wave = __builtin_amdgcn_readfirstlane(afresh.thread >> 6);
+  const uint32_t l = lane & 31, h = lane >> 5, quarter = wave & 3, half = wave >> 2;
+  KeyTile kt;
+  kt.find(a, afresh.block);
+  const int key0 = kt.k0 + 32 * (int)quarter, key = key0 + (int)l, which = (int)half;
+  const bool there = key < kt.keys;
+  uint16_t *const tq = lds + 2 * kRows * kD, *const tg = tq + kKeys * kD;
+  const float c = a.scale * kLog2e;
+  constexpr bool kHalf = __is_same(T, _Float16);
+  float up = kHalf ? kUp : 0.0f;
+  f32x16 dk[kD / 32], dv[kD / 32], sum[kD / 32];
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
+  __syncthreads();  // all waves have their rows out of LDS, and know that they are here
+  kt.fetch<kD>(lds, afresh.thread, wave, a);
+  const Pieces<kD, kKeys, kKeyThreads> pieces(afresh.thread);
+  const int64_t of_head = (int64_t)kt.head * a.G * a.D;
+  const int all = (kt.to - kt.from) * a.G;  // rows: N * Hq is below 2^30
+#pragma unroll 1
+  for (int i = 0; i * kKeys < all; ++i) {
+    const int t0 = kt.from + i * kKeys / a.G, x0 = i * kKeys % a.G;  // the first row's
+    const int64_t first = kt.base + t0;
+#pragma unroll
+    for (int j = 0; j < pieces.kMoves; ++j) {
+      const int row = (int)pieces.row + j * pieces.kStep;
+      const uint32_t t = a.by_G(x0 + row), g = x0 + row - t * a.G;
+      const bool in = i * kKeys + row < all && pieces.col < (uint32_t)a.D;
+      const uint32_t at = g * (uint32_t)(a.D * 2) + pieces.col * 2;
+      load_to_lds(pieces.lds_place(j, tq, wave), buffer_words(a.q + first * a.ldq + of_head),
+                  in ? at + t * (uint32_t)(a.ldq * 2) : kBeyond);
+      load_to_lds(pieces.lds_place(j, tg, wave), buffer_words(a.grad_o + first * a.ldgo + of_head),
+                  in ? at + t * (uint32_t)(a.ldgo * 2) : kBeyond);
+    }
+    if (wave == 0) {
+      const bool in = i * kKeys + (int)lane < all;
+      const uint32_t t = a.by_G(x0 + lane), g = x0 + lane - t * a.G;
+      const int64_t at = in ? (first + t) * (a.Hk * a.G) + kt.head * a.G + g : 0;
+      lses[lane] = in ? fmaf(a.lse_in[at], kLog2e, -kWeightsUp<T>) : INFINITY;
+      deltas[lane] = in ? a.delta[at] : 0.0f;
+    }
+    meet();
+    const RowReader<kD> rows(lane);
+    const lds_bytes hq = lds_of(tq) + half * kKeys * kD, hg = lds_of(tg) + half * kKeys * kD;
+    const lds_bytes hv = lds_of(lds) + quarter * kKeys * kD, hk = hv + kRows * kD * 2;
+    f32x16 s = f32x16{}, d = f32x16{};
+#pragma unroll
+    for (int x = 0; x < kD / 16; ++x) s = product<T>(rows(hq, 0, x), rows(hk, 0, x), s);
+#pragma unroll
+    for (int x = 0; x < kD / 16; ++x) d = product<T>(rows(hg, 0, x), rows(hv, 0, x), d);
+    const float raised = kHalf ? __builtin_amdgcn_ldexpf(1.0f, (int)(up - kWeightsUp<T>)) : 1.0f;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+      const int row = 32 * (int)half + 8 * (m / 4) + 4 * (int)h + m % 4;
+      const int behind = t0 + (int)a.by_G(x0 + row) - key - kt.near;
+      // (a row that is not there has an lse of infinity)
+      const bool seen = there && (uint32_t)behind < (uint32_t)kt.span && lses[row] != INFINITY;
+      const float w = __builtin_amdgcn_exp2f(fmaf(s[m], c, -lses[row]));
+      s[m] = seen ? w : 0.0f;
+      d[m] = seen ? w * (d[m] - deltas[row]) * raised : 0.0f;
+    }
+    if constexpr (kHalf) keep_in_range<kD>(d, dk, up);
+    meet();
+    make_finite<T, kD, 2 * kKeys, kKeyThreads>(tq);  // queries and gradients
+    meet();
+    add_columns<T, kD>(dk, hq, d, lane);
+    add_columns<T, kD>(dv, hg, s, lane);
+    meet();
+  }
+  join_halves<T, kD>(sum, dk, dv, up, lds, lane, wave);
+  const bool part = kt.part(a, key);
+  float* const to_part = kt.to_part(a, key, which);
+#pragma unroll
+  for (int dt = 0; dt < kD / 32; ++dt)
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+      const int col = 32 * dt + 8 * (m / 4) + m % 4;  // and 4 h
+      const uint32_t lower = __shfl(again.columns[dt / 2], col % 64), upper = __shfl(again.columns[dt / 2], col % 64 + 4);
+      if (part && there && ((h ? upper : lower) >> l & 1)) to_part[col + 4 * (int)h] = sum[dt][m];
+    }
+  uint16_t* const mine = lds + wave * 32 * kD;
+  put_rows<T, kD>(mine, sum, which ? 1.0f : a.scale, lane);
+  between_lanes();
+  if (!kt.sinks)
+    again.template put<kD>(mine, [&](int x) { return kt.out(a, key0 + x, which); }, kt.done(a) - key0);
 }
 
 // dk and dv of 128 keys, of the rows whose window they are in.  The last
@@ -856,7 +1334,6 @@ __device__ __forceinline__ void define_key(float (&y)[2], const WindowArgs& a, i
 // dk, the others dv.  Keys and values stay in LDS: in registers they would leave
 // none for operands on their way, and the waits for what is spilled wait for
 // the next tile too.
-constexpr int kKeyWaves = 8, kKeyThreads = kKeyWaves * 64;
 template <typename T, int kD>
 __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs a) {
   constexpr int kX = kD / 16;
@@ -866,35 +1343,15 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
   __shared__ __attribute__((aligned(16))) float lses[2][kKeys], deltas[2][kKeys];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l = lane & 31, h = lane >> 5, quarter = wave & 3, half = wave >> 2;
-  const int wide_blocks = (int)gridDim.x - a.sink_blocks;
-  const bool sinks = (int)blockIdx.x >= wide_blocks;
-  const int at = sinks ? (int)blockIdx.x - wide_blocks : neighbours(blockIdx.x, wide_blocks);
-  const int per_head = sinks ? a.sink_blocks / a.Hk : a.tiles, id = at % per_head, head = at / per_head;
-  const uint32_t unit = sinks ? (uint32_t)a.piece : (uint32_t)kRows;
-  const Sequence seq(a, id, 1, unit);
-  const int64_t base = seq.start, tile = seq.tile;
-  const int length = (int)seq.length;
-  if (tile < 0 || length <= 0 || tile * unit >= length) return;
-  const int k0 = sinks ? 0 : (int)tile * kRows;
-  // the rows' tokens, and how far behind a key those lie that see it: `near` on, fewer than `span` further
-  int from = k0, to = k0 + kRows - 1 + a.W;
-  const int near = sinks ? a.W : 0;
-  if (sinks) {
-    from = (int)tile * a.piece > a.W ? (int)tile * a.piece : a.W;
-    to = ((int)tile + 1) * a.piece;
-  }
-  if (to > length) to = length;
-  if (from >= to) return;  // no row of the piece sees a sink as one
-  const int key0 = k0 + 32 * (int)quarter, key = key0 + (int)l;
-  const int keys = sinks ? (a.S < length ? a.S : length) : length;  // of the sequence, as far as they matter here
+  KeyTile kt;
+  if (!kt.find(a, blockIdx.x)) return;
+  const bool sinks = kt.sinks;
+  const int64_t base = kt.base;
+  const int length = kt.length, head = kt.head, from = kt.from, to = kt.to, near = kt.near, keys = kt.keys;
+  const int key0 = kt.k0 + 32 * (int)quarter, key = key0 + (int)l;
   const bool active = key0 < keys, there = key < keys;
-  const int span = !there ? 0 : sinks ? length : a.W;
-
-  const Pieces<kD, kRows, kKeyThreads> wide(threadIdx.x);
-  const int n_keys = keys - k0 < kRows ? keys - k0 : kRows;
-  wide.fetch(lds, a.v + (base + k0) * a.ldv + (int64_t)head * a.D, a.ldv, n_keys, a.D, wide.offset(a.ldv, a.D), wave);
-  wide.fetch(lds + kRows * kD, a.k + (base + k0) * a.ldk + (int64_t)head * a.D, a.ldk, n_keys, a.D,
-             wide.offset(a.ldk, a.D), wave);
+  const int span = there ? kt.span : 0;
+  kt.fetch<kD>(lds, threadIdx.x, wave, a);
   uint16_t* const tiles = lds + 2 * kRows * kD;
 
   const Pieces<kD, kKeys, kKeyThreads> pieces(threadIdx.x);
@@ -1099,53 +1556,12 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  if (kHalf) {
-    const float lowered = __builtin_amdgcn_ldexpf(1.0f, -(int)up);
-#pragma unroll
-    for (int dt = 0; dt < kD / 32; ++dt) {
-      dk[dt] *= lowered;
-      dv[dt] *= __builtin_amdgcn_ldexpf(1.0f, -(int)kWeightsUp<T>);
-    }
-  }
-
-  // The exchange: the first four waves' dv, then the others' dk, in the order they
-  // are there for each lane.
-  f32x4* const given = reinterpret_cast<f32x4*>(lds) + quarter * (kD / 8) * 64 + lane;
-  meet();  // the tiles are read out, and what was fetched behind the last one is there
-#pragma unroll
-  for (int turn = 0; turn < 2; ++turn) {
-    if (half == (uint32_t)turn) {
-#pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x16& x = turn ? dk[dt] : dv[dt];
-          given[(dt * 4 + j) * 64] = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
-        }
-    }
-    __syncthreads();
-    if (half != (uint32_t)turn) {
-#pragma unroll
-      for (int dt = 0; dt < kD / 32; ++dt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x4 x = given[(dt * 4 + j) * 64];
-          f32x16& to = turn ? dk[dt] : dv[dt];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[4 * j + e] += x[e];
-        }
-    }
-    __syncthreads();
-  }
   const int which = (int)half;
   f32x16 sum[kD / 32];
-#pragma unroll
-  for (int dt = 0; dt < kD / 32; ++dt) sum[dt] = half ? dv[dt] : dk[dt];
-
-  // Sinks that rows behind their window see too: fp32, joined by the next launch.
-  const bool part = sinks || (key < a.S && length > a.W);
-  if (part && there) {
-    float* out = piece_sums(a, sinks ? id : a.pieces + seq.b, head, which) + (int64_t)key * a.D;
+  meet();  // the tiles are read out, and what was fetched behind the last one is there
+  join_halves<T, kD>(sum, dk, dv, up, lds, lane, wave);
+  if (kt.part(a, key) && there) {
+    float* const out = kt.to_part(a, key, which);
 #pragma unroll
     for (int dt = 0; dt < kD / 32; ++dt)
 #pragma unroll
@@ -1156,31 +1572,25 @@ __global__ __launch_bounds__(kKeyThreads, 2) void window_dkdv_kernel(WindowArgs 
               f32x4{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
       }
   }
-  if (sinks) return;
   uint16_t* const mine = lds + wave * 32 * kD;
-  const float times = which ? 1.0f : a.scale;
-  put_rows<T, kD>(mine, sum, times, lane);
-  const uint64_t redo = __ballot(there && !part && !finite_rows<kD>(sum));
+  put_rows<T, kD>(mine, sum, which ? 1.0f : a.scale, lane);
+  const uint64_t redo = __ballot(there && !finite_rows<kD>(sum));
+  const uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32);
   between_lanes();
-  for (uint32_t bad = (uint32_t)redo | (uint32_t)(redo >> 32); bad; bad &= bad - 1) {
-    const int x = __builtin_ctz(bad);
-    float y[2];
-    define_key<T>(y, a, base, length, head, key0 + x, which);
+  if (!sinks) {
+    const int done = kt.done(a);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if ((int)lane + 64 * e < a.D) mine[place<kD>(x, lane + 64 * e)] = (uint16_t)pack2<T>(y[e] * times, 0.0f);
+    for (int i = 0; i < kD / 16; ++i) {
+      const uint32_t x = (i * 64 + lane) / (kD / 8), col = (i * 64 + lane) % (kD / 8) * 8;
+      const int j = key0 + (int)x;
+      if (j >= done && j < length && (int)col < a.D) store16(kt.out(a, j, which) + col, load16(mine + place<kD>(x, col)));
+    }
   }
-  between_lanes();
-  uint16_t* out = which ? a.grad_v : a.grad_k;
-  const int64_t ld = which ? a.ldgv : a.ldgk;
-  const int done = length > a.W ? a.S : 0;  // keys before this one are the next launch's
-#pragma unroll
-  for (int i = 0; i < kD / 16; ++i) {
-    const uint32_t x = (i * 64 + lane) / (kD / 8), col = (i * 64 + lane) % (kD / 8) * 8;
-    const int j = key0 + (int)x;
-    if (j >= done && j < length && (int)col < a.D)
-      store16(out + (base + j) * ld + (int64_t)head * a.D + col, load16(mine + place<kD>(x, col)));
-  }
+  Again again;
+  if (bad)
+    again = keys_again<T, kD>(bad, mine, a, base, head, key0, which, [&](int j) { return kt.low(j); },
+                              [&](int j) { return kt.high(j); });
+  if (any_wave<kKeyWaves>(tiles, again.any())) make_keys_again<T, kD>(a, lds, lses[0], deltas[0], again);
 }
 
 // dk and dv of the sinks of sequences longer than the window: a wave for each
@@ -1210,14 +1620,7 @@ __global__ __launch_bounds__(kJoinThreads) void window_sinks_kernel(WindowArgs a
   for (int p = a.W / a.piece; p <= (length - 1) / a.piece; ++p) add(y, first + p);
   const float times = which ? 1.0f : a.scale;
   uint16_t* out = (which ? a.grad_v + (base + j) * a.ldgv : a.grad_k + (base + j) * a.ldgk) + (int64_t)head * a.D;
-  if (__any(mine && !(fabsf(y[0]) < INFINITY && fabsf(y[1]) < INFINITY))) {
-    define_key<T>(y, a, base, length, head, j, which);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (lane + 64 * e < a.D) out[lane + 64 * e] = (uint16_t)pack2<T>(y[e] * times, 0.0f);
-  } else if (mine) {
-    *reinterpret_cast<uint32_t*>(out + d) = pack2<T>(y[0] * times, y[1] * times);
-  }
+  if (mine) *reinterpret_cast<uint32_t*>(out + d) = pack2<T>(y[0] * times, y[1] * times);
 }
 
 struct WindowKernels {

@@ -476,13 +476,17 @@ int64_t words_of(int64_t chunks, int64_t tiles) {
   return kTicketWords + (chunks + groups + spans) * tiles * kTile;
 }
 
+// Workgroups up to which some are there for empty sequences: a launch counts its threads in 32 bits.
+constexpr int kBlocksMost = 1 << 22;
+
 hipError_t launch_scan(ScanArgs a, int dtype, bool back, void* workspace, hipStream_t stream) {
   const int64_t chunk = tokens_of_chunk(dtype);
   a.tiles = (int)tiles_of(a.D);
   a.chunks = (int)((a.N + chunk - 1) / chunk);
   a.words = a.chunks > 1 ? static_cast<uint64_t*>(workspace) : nullptr;
   const int most = a.state_out ? (a.B + kHanded * kWaves - 1) / (kHanded * kWaves) : 0;
-  a.handing = most > a.chunks ? most - a.chunks : 0;
+  const int there = most < kBlocksMost / a.tiles ? most : kBlocksMost / a.tiles;  // (else each has more of them)
+  a.handing = there > a.chunks ? there - a.chunks : 0;
   if (a.words) {
     uint64_t* words = a.words;
     int64_t n = words_of(a.chunks, a.tiles);

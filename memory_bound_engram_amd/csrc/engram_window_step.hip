@@ -85,11 +85,11 @@ __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t col) {
   return row * kD + ((col >> 3) ^ turn) * 8 + (col & 7);
 }
 
-// The list of a row: which tokens its tile's lines hold, and where they lie.
 // a % b for a >= 0: 64-bit division takes hundreds of instructions.
 __device__ __forceinline__ int rest_of(int64_t a, int b) {
   return a >> 32 == 0 ? (int)((uint32_t)a % (uint32_t)b) : (int)(a % b);
 }
+// The list of a row: which tokens its tile's lines hold, and where they lie.
 struct Seen {
   int64_t p;       // the row's position
   int sinks, n;    // tokens that are sinks; of the list

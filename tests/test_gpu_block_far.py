@@ -81,6 +81,24 @@ def test_window_attention_over_more_than_four_gigabytes(gpu, space, window, sink
                  "go": normal(gpu, *q, seed=4), "o": blank_q, "gq": blank_q, "gk": blank_k, "gv": blank_k}, call)
 
 
+def test_window_attention_of_values_that_are_not_finite(gpu, space):  # noqa: F811
+    hq, hk, d = 4, 2, 72
+    cu = torch.tensor([0, 3000, N - 5], device=gpu)
+    k, v, go = normal(gpu, N, hk, d, seed=2), normal(gpu, N, hk, d, seed=3), normal(gpu, N, hq, d, seed=4)
+    v[[700, 4100], :, 9], go[[1500, 4000], :, 70], k[2500, :, 3] = float("inf"), float("nan"), float("inf")
+
+    def call(p):
+        lse = poisoned((N, hq), F4, gpu)
+        eg.engram_window_attn_fwd(p["q"], p["k"], p["v"], cu, p["o"], 300, sinks=5, lse=lse, scale=0.1)
+        eg.engram_window_attn_bwd(p["go"], p["q"], p["k"], p["v"], p["o"], lse, cu, p["gq"], p["gk"], p["gv"],
+                                  ws(eg.engram_window_attn_bwd_workspace_bytes(N, 2, hq, hk, d, 300, 5), gpu), 300, sinks=5,
+                                  scale=0.1)
+        return {"lse": lse}
+    blank_q, blank_k = poisoned((N, hq, d), BF, gpu), poisoned((N, hk, d), BF, gpu)
+    both(space, {"q": normal(gpu, N, hq, d, seed=1), "k": k, "v": v, "go": go, "o": blank_q, "gq": blank_q, "gk": blank_k,
+                 "gv": blank_k}, call)
+
+
 def test_gated_scan(gpu, space):  # noqa: F811
     d = 264
     cu = torch.tensor([0, 3000, 3000, N - 5], device=gpu)

@@ -41,7 +41,8 @@ def touched(x, places, value):
 def spans(c):
     at = 0
     for n in c["lens"]:
-        yield slice(at, at + n)
+        if n:
+            yield slice(at, at + n)
         at += n
 
 
@@ -65,52 +66,63 @@ def any_sees(c, of_rows):
     return out
 
 
-@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("window,sinks", [(40, 5), (150, 0), (1 << 40, 0), (3, 100)])
-@pytest.mark.parametrize("value", [math.inf, math.nan])
-def test_values(gpu, window, sinks, dtype, value):
-    """In v: some columns of a few tokens, early, in the middle and late, beside each other and far apart."""
-    lens = [200, 333]
-    c = case(lens, 4, 2, 72, dtype, gpu, window, sinks, seed=1)
+# some columns of a few tokens, early, in the middle and late, beside each other and far apart
+PLACES = [(10, 3), (11, 7), (150, 3), (290, 1), (291, 4), (299, 1), (390, -1), (532, 0)]
+
+
+def check_values(c, value, dev):
+    """In v."""
+    hk, per = c["hk"], c["hq"] // c["hk"]
     (o64, eo), _ = forward64(c)
-    o, _ = run_forward(c, gpu)
-    c["v"] = touched(c["v"], [(10, 3), (11, 71), (150, 3), (290, 9), (291, 64), (299, 9), (390, 33), (532, 0)], value)
-    o2, lse = run_forward(c, gpu)
-    ok = ~any_seen(c, bad(c["v"])).repeat_interleave(2, 1)
-    held("o", o2, o64, eo, ok)
+    c["v"] = touched(c["v"], PLACES, value)
+    o, lse = run_forward(c, dev)
+    ok = ~any_seen(c, bad(c["v"])).repeat_interleave(per, 1)
+    held("o", o, o64, eo, ok)
     # the backward, from what the forward gave
     clean = {**c, "v": finite(c["v"])}
-    want = backward64(clean, torch.where(ok, o2, torch.zeros_like(o2)), lse)
-    gq, gk, gv = run_backward(c, o2, lse, gpu)
+    want = backward64(clean, torch.where(ok, o, torch.zeros_like(o)), lse)
+    gq, gk, gv = run_backward(c, o, lse, dev)
     fine = ok.all(2)  # rows that see no such value: their delta is finite
     check("grad_q", gq[fine], want[0][0][fine], 2 * want[0][1][fine])
     assert not torch.isfinite(gq[~fine]).any()
-    rows = ~fine.view(-1, 2, 2).all(2)
+    rows = ~fine.view(-1, hk, per).all(2)
     lost = any_sees(c, rows) | bad(c["v"]).any(2)  # dk of tokens that such a row sees
     check("grad_k", gk[~lost], want[1][0][~lost], 2 * want[1][1][~lost])
     assert not torch.isfinite(gk[lost]).any()
     check("grad_v", gv, want[2][0], 2 * want[2][1])  # weights do not know of v
 
 
-@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("window,sinks", [(40, 5), (150, 0), (1 << 40, 0), (3, 100)])
-@pytest.mark.parametrize("value", [math.inf, math.nan])
-def test_gradients(gpu, window, sinks, dtype, value):
-    """In grad_o, in columns of their own."""
-    lens = [200, 333]
-    c = case(lens, 4, 2, 72, dtype, gpu, window, sinks, seed=2)
-    o, lse = run_forward(c, gpu)
+def check_gradients(c, value, dev):
+    """In grad_o."""
+    hk, per = c["hk"], c["hq"] // c["hk"]
+    o, lse = run_forward(c, dev)
     want = backward64(c, o, lse)
-    c["go"] = touched(c["go"], [(10, 3), (11, 71), (150, 3), (290, 9), (291, 64), (299, 9), (390, 33), (532, 0)], value)
-    gq, gk, gv = run_backward(c, o, lse, gpu)
+    c["go"] = touched(c["go"], PLACES, value)
+    gq, gk, gv = run_backward(c, o, lse, dev)
     rows = bad(c["go"]).any(2)
     check("grad_q", gq[~rows], want[0][0][~rows], 2 * want[0][1][~rows])
     assert not torch.isfinite(gq[rows]).any()
-    lost = any_sees(c, rows.view(-1, 2, 2).any(2))
+    lost = any_sees(c, rows.view(-1, hk, per).any(2))
     check("grad_k", gk[~lost], want[1][0][~lost], 2 * want[1][1][~lost])
     assert not torch.isfinite(gk[lost]).any()
-    ok = ~any_sees(c, bad(c["go"]).view(-1, 2, 2, 72).any(2))
+    ok = ~any_sees(c, bad(c["go"]).view(-1, hk, per, c["d"]).any(2))
     held("grad_v", gv, want[2][0], 2 * want[2][1], ok)
+
+
+@pytest.mark.parametrize("check_them", [check_values, check_gradients], ids=["values", "gradients"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("window,sinks", [(40, 5), (150, 0), (1 << 40, 0), (3, 100)])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_seen_and_not_seen(gpu, window, sinks, dtype, value, check_them):
+    check_them(case([200, 333], 4, 2, 72, dtype, gpu, window, sinks, seed=1), value, gpu)
+
+
+@pytest.mark.parametrize("check_them", [check_values, check_gradients], ids=["values", "gradients"])
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 8), (3, 3, 128), (5, 1, 64), (32, 1, 40), (7, 7, 120)])
+def test_heads(gpu, hq, hk, d, check_them):
+    for dtype in (BF, FP):
+        print(f"infinite heads {hq}/{hk} d={d} {dtype}", flush=True)
+        check_them(case([200, 0, 333], hq, hk, d, dtype, gpu, 60, 9, seed=d, apart=True), math.inf, gpu)
 
 
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])

@@ -27,20 +27,25 @@
 // well; those rows' part of their dk and dv is summed in pieces of the sequence by
 // workgroups of their own, and a last, small launch joins it with the window's part.
 //
-// What bounds them.  A wave issues one instruction at a time, of any kind, and a
-// SIMD's two waves (the registers let in no more) do not fill the matrix cores:
-// at 7 sequences up to 8192 tokens, 40 + 8 heads of 128, window 1024 (the forward, 605
-// to 625 us, 0.9 PFLOP/s), they are busy 49% of the time, the vector units 53%.  The
-// backward of 5 sequences up to 4096, 32 + 8 heads, takes 640 to 660 us: dq 260
-// (matrix cores 43%), dk and dv 380 (36%, CUs 83%: 760 workgroups, one a CU at a
-// time, and the sinks' behind them).
-// So what counts is instructions: loops of a fixed
+// What bounds them.  7 sequences up to 8192 tokens, 40 + 8 heads of 128, window 1024: the
+// forward takes 595 to 635 us, 0.9 PFLOP/s.  The same call with a window of one token takes
+// 159 us, 129 of which are its bytes' at a copy's rate: that much is each workgroup's start (bounds,
+// queries, first tiles) and end, which the other workgroup of the CU overlaps only in part.  What
+// is beyond goes at 1.2 PFLOP/s (window 4096: 1344 us, 1.05 in all).  Over the call the matrix
+// cores are busy 48% of the time, the vector units 52%; a wave issues one instruction at a
+// time, of any kind, and a SIMD has two (the registers let in no more).  The
+// backward of 5 sequences up to 4096, 32 + 8 heads, takes 620 to 680 us (window 1: 178): dq 250
+// (matrix cores 44%, CUs 88%), dk and dv 390 (35%, 83%: 760 workgroups, one a CU at a
+// time as their LDS is over 128 KB, so that nothing hides their start and end, and the sinks' behind
+// them).  Heads of a size between 64 and 128 take the products of 128 (forward at 80: 568 us,
+// at 96: 585, at 64: 361).
+// What counted in the loops: a fixed
 // number of tiles, in which an operand's place in LDS is a constant behind an
 // address in a register (40 us of the forward's 676), few scalar instructions for a
 // tile's loads (25), no gap between sinks and window (40).  Tried and slower: 64 rows a wave, one
 // wave a SIMD (the products' results then lie where the vector unit cannot
 // read them, and registers spill); workgroups that stay and fetch the next
-// rows while they work on these, one a CU.
+// rows while they work on these, one of eight waves a CU.
 //
 // Rounding.  Sums, maxima and the softmax are fp32.  p and d are rounded to the
 // element type as operands of the second products; the sum of p is taken

@@ -150,12 +150,12 @@ template <typename T>
 constexpr float kWeightsUp = __is_same(T, _Float16) ? 14.0f : 0.0f;
 
 // d as an operand in fp16, whose steps below 2^-14 are all 2^-24: d of ordinary small
-// gradients over many keys lies there (4096 keys, grad_o of 1e-4: dq off by 4% of
-// its norm), and d itself may pass 65504.  So the kernels hold 2^up d: `up` is a
+// gradients over many keys lies there (3000 keys, heads of 64, grad_o of 1e-4: dq off by 1.2% of
+// its norm, 0.25% with this, which is its own rounding), and d itself may pass 65504.  So the kernels hold 2^up d: `up` is a
 // lane's own, as its row's (dq) or key's (dk) sums are, and goes down, the sums with
 // it, where a value would pass 2^kMostBits.  The largest then lies at 2^4 or more below
 // 2^5, so that this is rare, and what is less than 2^-18 of the largest loses digits:
-// 2^-30 of the largest at most.  (5 sequences up to 4096, 32 + 8 heads of 128, window
+// 2^-29 of the largest at most.  (5 sequences up to 4096, 32 + 8 heads of 128, window
 // 1024, fp16: 696 us, 677 without.)
 constexpr float kUp = 60.0f;      // where it begins: do . v is below 2^39
 constexpr int kMostBits = 15, kAimBits = 5;
@@ -166,7 +166,7 @@ __device__ __forceinline__ void keep_in_range(f32x16& d, f32x16 (&sums)[kD / 32]
   for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(d[e]));
   if (__any(top > (float)(1 << kMostBits))) {
     top = column_max(top);
-    // (an infinite or NaN result is made again by the definition)
+    // (an infinite or NaN d stays so, and with it the result)
     const int down = top > (float)(1 << kMostBits) && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - kAimBits : 0;
     const float times = __builtin_amdgcn_ldexpf(1.0f, -down);
     up -= (float)down;
